@@ -23,6 +23,8 @@ __all__ = ["gemm_f16", "gemm_bf16", "gemm_f16_f16out", "gemm_bf16_bf16out", "gem
            "gemm_fp8_blockscaled", "gemm_fp8_blockscaled_fmt", "gemm_fp8_rowscaled", "FP8_E4M3",
            "FP8_E5M2", "gemv_w8a8", "gemm_w8a8", "gemm_w8a8_kn", "gemm_w8a8_requant", "quantize_i8_rows",
            "quantize_fp8_blocks", "quantize_fp8",
+           "paged_kv_append", "paged_attention", "cache_fork", "cache_extend", "cache_free",
+           "cache_compact", "token_logprobs", "token_logprobs_backward", "TokenLogprobs",
            "MpdtError", "lib", "lib_path", "version"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -541,3 +543,7 @@ def quantize_fp8(X, fmt, block_rows, block_cols, q_out=None, scales_out=None):
     _check("quantize_fp8", lib().quantize_fp8(R, Cc, px, ldx, int(fmt), int(block_rows), int(block_cols),
                                               pq, ldq, ps, lds, _stream(X)))
     return q_out, scales_out
+
+
+from .serving import (TokenLogprobs, cache_compact, cache_extend, cache_fork, cache_free,  # noqa: E402
+                      paged_attention, paged_kv_append, token_logprobs, token_logprobs_backward)

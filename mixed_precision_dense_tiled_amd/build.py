@@ -21,6 +21,9 @@ ORACLE_LIB = os.path.join(ORACLE_DIR, "liboracle.so")
 
 HIP_SOURCES = ["abi.hip", "gemm.hip", "gemm_epi.hip", "gemm_fp8.hip", "gemm_fp8_general.hip", "gemv_w8a8.hip", "quant.hip"]
 
+# The serving operators (include/mpdt_serving.h), in libmpdt.so beside the above.
+SERVING_SOURCES = ["serving_abi.hip", "paged_attn.hip", "kv_cache.hip", "logprobs.hip"]
+
 # Per-source device-compiler options.  The one-wave FP8 GEMM rescales its MFMA
 # block sums with FP32 FMAs every K tile; VALU instructions cannot read AGPRs,
 # so its MFMAs are built in the form that writes VGPRs.
@@ -73,7 +76,7 @@ def _link(out: str, sources, extra_flags=()) -> str:
 
 
 def build_library(extra_flags=()) -> str:
-    return _link(LIB, HIP_SOURCES, extra_flags)
+    return _link(LIB, HIP_SOURCES + SERVING_SOURCES, extra_flags)
 
 
 CLOCK_LIB = os.path.join(PKG, "libmpdt_clock.so")
@@ -103,7 +106,7 @@ def build_oracle() -> str:
 def build_all():
     build_oracle()
     # the three HIP libraries in one compile pool
-    _build_libs([(LIB, HIP_SOURCES, ()), (PROBE_LIB, ["probes.hip"], ()),
+    _build_libs([(LIB, HIP_SOURCES + SERVING_SOURCES, ()), (PROBE_LIB, ["probes.hip"], ()),
                  (CLOCK_LIB, HIP_SOURCES, ("-DMPDT_CLOCK_STAMPS",))])
 
 

@@ -12,14 +12,13 @@
 #include <mutex>
 #include <string>
 
+#include "abi_common.hpp"
 #include "kernels.hpp"
 #include "mpdt.h"
 
 static_assert(MPDT_ACT_NONE == mpdt::ACT_NONE && MPDT_ACT_RELU == mpdt::ACT_RELU &&
                   MPDT_ACT_GELU == mpdt::ACT_GELU && MPDT_ACT_SILU == mpdt::ACT_SILU,
               "activation codes of the C ABI and the kernels agree");
-
-#define MPDT_EXPORT extern "C" __attribute__((visibility("default")))
 
 namespace {
 
@@ -572,6 +571,12 @@ MPDT_EXPORT mpdt_status quantize_fp8(int64_t R, int64_t C, const float* X, int64
     return run_quantize_fp8("quantize_fp8", R, C, X, ldx, fmt, block_rows, block_cols, Q, ldq, scales,
                             lds, stream);
 }
+
+namespace mpdt {
+mpdt_status abi_fail(mpdt_status s, const char* fn, const char* what) { return fail(s, fn, what); }
+mpdt_status abi_check_device(const char* fn) { return check_device(fn); }
+mpdt_status abi_launched(hipError_t e, const char* fn) { return launched(e, fn); }
+}  // namespace mpdt
 
 MPDT_EXPORT const char* mpdt_status_string(mpdt_status s) {
     switch (s) {

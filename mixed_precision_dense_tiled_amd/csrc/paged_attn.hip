@@ -1,0 +1,1128 @@
+// paged_attn.hip -- attention of new tokens over a paged key/value cache.
+//
+// For sequence b with n keys and nq new tokens (the last nq of the n), token
+// t stands at position p = n - nq + t and sees the keys j <= p, with a window
+// w only those with j > p - w.  With s_j = scale * (q . k_j), capped to
+// cap * tanh(s_j / cap) on request,
+//     out = sum_j exp(s_j) v_j / sum_j exp(s_j),   lse = log sum_j exp(s_j);
+// a token that sees no key gets out = 0 and lse = -inf.
+//
+// The work is cut into units (a tile of rows of one KV head; a row is one
+// token and one of the query heads that share the KV head) and each unit's
+// keys into tiles.  All tiles of all units stand in one line, which the
+// workgroups share evenly: a plan kernel writes the line down (lengths are
+// known on the device only), each workgroup walks its stretch with a running
+// maximum and sum per row, and units that several workgroups share are joined
+// by a last kernel.  Batches whose cache rows are short run in one launch,
+// one workgroup to a unit.
+//
+// Two kernels walk the tiles.  Few rows per sequence (single tokens): 16 rows
+// by 32 keys on 16x16x32 MFMAs, each wave with key tiles and an LDS ring of its
+// own, bound by the cache's bytes.  Many rows (chunks of a prompt): 256 rows by
+// 64 keys on 32x32x16 MFMAs, K and V shared by the workgroup, bound by the
+// matrix cores and the exponentials.  Both form S^T = K Q^T, so that a lane
+// holds scores of a single row: the running maximum and sum are one register
+// per row, and the MFMA's output layout is already the operand layout of
+// O^T = V^T P^T once V's keys are read in the same order (the transposing LDS
+// reads take any order of rows).
+//
+// Scores, maxima, sums and outputs are FP32.  P is rounded to the type that
+// the second MFMA takes (FP16 for FP16 and FP8 caches, BF16 for BF16): one
+// rounding per weight, independent from key to key, where the sum of the
+// weights keeps them unrounded.  FP8 keys and values are widened exactly;
+// their scales are per head and join the score's scale and the output.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "device_common.hpp"
+#include "gemm_common.hpp"
+#include "serving.hpp"
+
+namespace mpdt {
+namespace {
+
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr float NO_MAX = -1e30f;      // reference of a row that has seen no key
+constexpr float RESCALE = 8.0f;       // a row's reference moves when its maximum has outgrown it by 2^8
+constexpr int PAGES_LDS = 1024;       // page numbers of a stretch held in LDS
+
+typedef __attribute__((ext_vector_type(2))) float f32x2;
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
+
+// ---- element types ----------------------------------------------------------
+
+struct Bf16 {
+    using vec8 = bf16x8;
+    static constexpr float P_SHIFT = 0.0f;
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        bf16x2 r;
+        r[0] = (__bf16)a;
+        r[1] = (__bf16)b;
+        return __builtin_bit_cast(uint32_t, r);
+    }
+    static __device__ __forceinline__ uint32_t from_fp8_lo(uint32_t w) {
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
+    }
+    static __device__ __forceinline__ uint32_t from_fp8_hi(uint32_t w) {
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true));
+    }
+    static __device__ __forceinline__ f32x4 mma16(u32x4 a, u32x4 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ f32x16 mma32(u32x4 a, u32x4 b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    }
+};
+
+struct F16 {
+    // FP16 weights sit 2^7 higher (at most 2^15 with the lazy reference), so
+    // that small ones stay clear of the subnormals; the sum carries the same
+    // factor and it cancels.
+    static constexpr float P_SHIFT = 7.0f;
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        f16x2 r;
+        r[0] = (_Float16)a;
+        r[1] = (_Float16)b;
+        return __builtin_bit_cast(uint32_t, r);
+    }
+    static __device__ __forceinline__ uint32_t from_fp8_lo(uint32_t w) {
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false));
+    }
+    static __device__ __forceinline__ uint32_t from_fp8_hi(uint32_t w) {
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true));
+    }
+    static __device__ __forceinline__ f32x4 mma16(u32x4 a, u32x4 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                      __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ f32x16 mma32(u32x4 a, u32x4 b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
+                                                      __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    }
+};
+
+// 8 FP8 values widened to 8 16-bit ones.
+template <class E>
+__device__ __forceinline__ u32x4 widen8(u32x2 w) {
+    return u32x4{E::from_fp8_lo(w[0]), E::from_fp8_hi(w[0]), E::from_fp8_lo(w[1]), E::from_fp8_hi(w[1])};
+}
+
+// ---- the staged rows of K and V in LDS ---------------------------------------
+//
+// A row is CH chunks of 16 bytes (DP elements, padded to 8 chunks for 96 FP8
+// values); chunk c of row r lies at place c ^ swz(r), so that the reads below
+// touch every bank once.  MF: rows of an MFMA tile (16 or 32), which decides
+// the set of rows that one transposing read of V names.
+template <int DP, bool KV8, int MF>
+struct Rows {
+    static constexpr int CH = KV8 ? (DP <= 64 ? 4 : 8) : DP / 8;
+    static constexpr int BYTES = CH * 16;
+    static __device__ __forceinline__ int swz_k(int r) {
+        if constexpr (CH == 16 || CH == 8) return r & 7;
+        return (r >> 1) & 3;
+    }
+    static __device__ __forceinline__ int swz_v(int r) {
+        const int far = MF == 16 ? (r >> 4) & 1 : (r >> 3) & 1;   // the upper four of a transposing read's rows
+        if constexpr (KV8) {
+            if constexpr (CH == 8) return (r & 3) | (far << 2);
+            return ((r >> 1) & 1) | (far << 1);
+        }
+        if constexpr (CH == 12) return ((r >> 1) & 1) << 1;
+        return (r & 3) << 1;
+    }
+};
+
+// 16 bytes per lane straight into LDS: lane l's land at dst + 16 * l.  As the
+// buffer form in device_common.hpp, from 64-bit addresses.
+__device__ __forceinline__ void global_to_lds16(const char* src, MPDT_LDS char* dst) {
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                 :
+                 : "{m0}"((uint32_t)(uintptr_t)dst), "v"((uint64_t)(uintptr_t)src));
+}
+
+__device__ __forceinline__ u32x2 lds_load8(const MPDT_LDS char* base, uint32_t off) {
+    return *reinterpret_cast<const MPDT_LDS u32x2*>(base + off);
+}
+
+// ---- sequences, units and the plan --------------------------------------------
+
+struct Seq {
+    int start, nq, n;   // first row of q, new tokens, keys
+};
+
+// Numbers that point outside the batch are cut to it.
+__device__ __forceinline__ Seq seq_of(const SeqView& v, int64_t page_size, int b) {
+    Seq s;
+    const int c0 = v.cu_q[b], c1 = v.cu_q[b + 1];
+    s.start = min(max(c0, 0), v.tokens);
+    s.nq = min(max(c1, s.start), v.tokens) - s.start;
+    const int64_t most = page_size * v.width;
+    s.n = (int)min((int64_t)max(v.lens[b], 0), most);
+    return s;
+}
+
+// Keys [lo, hi) that any of the rows [r0, r1) of a sequence sees.
+struct Span32 {
+    int lo, hi;
+};
+__device__ __forceinline__ Span32 keys_of(const Seq& s, int group, int window, int r0, int r1) {
+    const int t0 = r0 / group, t1 = (r1 - 1) / group, past = s.n - s.nq;
+    Span32 k;
+    k.hi = min(max(past + t1 + 1, 0), s.n);
+    k.lo = window > 0 ? max(past + t0 + 1 - window, 0) : 0;
+    if (k.lo >= k.hi) k.lo = k.hi = 0;
+    return k;
+}
+
+// The plan in the workspace: head[0] entries (row tiles), head[1] key tiles
+// of all entries, then per entry {sequence, first row, first key tile, key
+// tiles} and the key tiles before it.  A KV head repeats the line once more.
+struct Plan {
+    int32_t* head;
+    i32x4* entry;
+    int32_t* before;
+    int32_t* first;     // row tiles before a sequence
+    float* part_o;      // partial outputs, two slots to a worker
+    f32x2* part_ml;     // their reference and sum
+};
+
+__host__ __device__ inline int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
+
+__host__ __device__ inline int64_t plan_layout(char* ws, int entries, int seqs, int workers, int tile_rows,
+                                               int dp, Plan* p) {
+    int64_t at = 0;
+    p->head = (int32_t*)(ws + at);
+    at += 256;
+    p->entry = (i32x4*)(ws + at);
+    at += up256((int64_t)entries * 16);
+    p->before = (int32_t*)(ws + at);
+    at += up256(((int64_t)entries + 1) * 4);
+    p->first = (int32_t*)(ws + at);
+    at += up256(((int64_t)seqs + 1) * 4);
+    p->part_ml = (f32x2*)(ws + at);
+    at += up256((int64_t)workers * 2 * tile_rows * 8);
+    p->part_o = (float*)(ws + at);
+    at += up256((int64_t)workers * 2 * tile_rows * dp * 4);
+    return at;
+}
+
+// Exclusive sum over the workgroup's threads; total to all.  red: one int a wave.
+template <int WAVES>
+__device__ __forceinline__ int block_scan(int x, int* red, int& total) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int s = x;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int y = __shfl_up(s, d);
+        if (lane >= d) s += y;
+    }
+    if (lane == 63) red[wave] = s;
+    __syncthreads();
+    int base = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+        const int r = red[w];
+        if (w < wave) base += r;
+        total += r;
+    }
+    __syncthreads();
+    return base + s - x;
+}
+
+__global__ __launch_bounds__(1024) void attn_plan_kernel(AttnArgs a, int key_tile) {
+    __shared__ int red[16];
+    Plan p;
+    plan_layout(a.ws, a.entries, a.sv.seqs, a.workers, a.tile_rows, 0, &p);
+    int run = 0;
+    for (int b0 = 0; b0 < a.sv.seqs; b0 += 1024) {
+        const int b = b0 + threadIdx.x;
+        int c = 0;
+        if (b < a.sv.seqs) {
+            const Seq s = seq_of(a.sv, a.kv.page_size, b);
+            c = (int)(((int64_t)s.nq * a.group + a.tile_rows - 1) / a.tile_rows);
+        }
+        int total;
+        const int at = run + block_scan<16>(c, red, total);
+        if (b < a.sv.seqs) p.first[b] = at;
+        run += total;
+    }
+    const int entries = min(run, a.entries);
+    if (threadIdx.x == 0) p.first[a.sv.seqs] = run;
+    __syncthreads();
+    int tiles = 0;
+    for (int e0 = 0; e0 < entries; e0 += 1024) {
+        const int e = e0 + threadIdx.x;
+        int c = 0;
+        i32x4 ent{0, 0, 0, 0};
+        if (e < entries) {
+            int lo = 0, hi = a.sv.seqs;      // first[lo] <= e < first[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (p.first[mid] <= e) lo = mid;
+                else hi = mid;
+            }
+            const Seq s = seq_of(a.sv, a.kv.page_size, lo);
+            const int r0 = (e - p.first[lo]) * a.tile_rows;
+            const Span32 k = keys_of(s, a.group, a.window, r0, min(r0 + a.tile_rows, s.nq * a.group));
+            const int t0 = k.lo / key_tile;
+            c = max((k.hi + key_tile - 1) / key_tile - t0, 1);
+            ent = i32x4{lo, r0, t0, c};
+        }
+        int total;
+        const int at = tiles + block_scan<16>(c, red, total);
+        if (e < entries) {
+            p.entry[e] = ent;
+            p.before[e] = at;
+        }
+        tiles += total;
+    }
+    if (threadIdx.x == 0) {
+        p.before[entries] = tiles;
+        p.head[0] = entries;
+        p.head[1] = tiles;
+    }
+}
+
+// Key tiles to a worker.
+__device__ __forceinline__ int64_t share_of(const AttnArgs& a, int64_t total) {
+    return max((total + a.workers - 1) / a.workers, (int64_t)a.min_tiles);
+}
+
+// Numbers of this workgroup's stretch: consecutive stretches run on one XCD
+// (workgroups go to the 8 XCDs in turn), so units of one KV head share an L2.
+__device__ __forceinline__ int worker_id() {
+    const int w = gridDim.x;
+    return w % 8 ? (int)blockIdx.x : (int)(blockIdx.x % 8) * (w / 8) + (int)(blockIdx.x / 8);
+}
+
+// Row tile `e` of a batch without a plan: all threads of the workgroup look
+// for the sequence that holds it.  box: {sequence, first row}; -1: none.
+template <int WAVES>
+__device__ __forceinline__ void find_entry(const AttnArgs& a, int e, int* red, int* box) {
+    if (threadIdx.x == 0) box[0] = -1;
+    __syncthreads();
+    int run = 0;
+    for (int b0 = 0; b0 < a.sv.seqs; b0 += WAVES * 64) {
+        const int b = b0 + threadIdx.x;
+        int c = 0;
+        if (b < a.sv.seqs) {
+            const Seq s = seq_of(a.sv, a.kv.page_size, b);
+            c = (int)(((int64_t)s.nq * a.group + a.tile_rows - 1) / a.tile_rows);
+        }
+        int total;
+        const int at = run + block_scan<WAVES>(c, red, total);
+        if (e >= at && e < at + c) {
+            box[0] = b;
+            box[1] = (e - at) * a.tile_rows;
+        }
+        run += total;
+        if (run > e) break;
+    }
+    __syncthreads();
+}
+
+// Page numbers of the keys from key tile `tile` on, into LDS; returns the
+// tile up to which they reach (at most `end`).  Called by all threads.
+template <int NT, int KT>
+__device__ __forceinline__ int fetch_pages(const AttnArgs& a, int b, int tile, int end, int* pages, int& first) {
+    const int64_t k0 = (int64_t)tile * KT, ps = a.kv.page_size;
+    first = (int)(k0 / ps);
+    const int64_t reach = ((int64_t)first + PAGES_LDS) * ps / KT;
+    const int stop = (int)min((int64_t)end, reach);
+    const int last = (int)min(((int64_t)stop * KT - 1) / ps, (int64_t)a.sv.width - 1);
+    const int32_t* row = a.sv.table + (int64_t)b * a.sv.ld_table;
+    for (int i = threadIdx.x; i <= last - first; i += NT) pages[i] = row[first + i];
+    __syncthreads();
+    return stop;
+}
+
+// Byte offset of a key's row in the cache, and whether there is such a key.
+__device__ __forceinline__ bool key_offset(const PagedKV& kv, const int* pages, int first, int key, int lo, int hi,
+                                           int64_t& off) {
+    const bool in = key >= lo && key < hi;
+    const int pi = kv.page_shift >= 0 ? key >> kv.page_shift : key / kv.page_size;
+    const int slot = key - pi * kv.page_size;
+    const int pg = in ? pages[pi - first] : -1;
+    const bool ok = pg >= 0 && pg < kv.pages;
+    off = ok ? pg * kv.page_b + slot * kv.slot_b : 0;
+    return ok;
+}
+
+__device__ __forceinline__ int64_t shfl64(int64_t v, int lane) {
+    const int lo = __shfl((int)(uint32_t)v, lane), hi = __shfl((int)(v >> 32), lane);
+    return (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo);
+}
+
+// Score in base-2 logarithms: s * c, or capped.
+struct Score {
+    float mul, cap2, inner;   // inner: 2 * log2(e) * scale / cap
+};
+__device__ __forceinline__ Score score_of(const AttnArgs& a, float k_scale) {
+    Score s;
+    s.mul = a.scale * k_scale * LOG2E;
+    s.cap2 = a.softcap * LOG2E;
+    s.inner = a.softcap > 0.0f ? 2.0f * LOG2E * a.scale * k_scale / a.softcap : 0.0f;
+    return s;
+}
+// cap * tanh(x / cap), tanh(y) = 1 - 2 / (exp(2 y) + 1); both ends saturate.
+template <bool CAP>
+__device__ __forceinline__ float score(const Score& c, float s) {
+    if constexpr (CAP) {
+        const float e = __builtin_amdgcn_exp2f(s * c.inner);
+        return c.cap2 - 2.0f * c.cap2 * __builtin_amdgcn_rcpf(e + 1.0f);
+    }
+    return s * c.mul;
+}
+
+// Four outputs of a row from d on, rounded once to the type of q.
+__device__ __forceinline__ void store_out4(const AttnArgs& a, char* row, int d, f32x4 v) {
+    u32x2 w;
+    if (a.q_type == DT_BF16) {
+        w = u32x2{Bf16::pack(v[0], v[1]), Bf16::pack(v[2], v[3])};
+    } else {
+        w = u32x2{F16::pack(v[0], v[1]), F16::pack(v[2], v[3])};
+    }
+    *reinterpret_cast<u32x2*>(row + 2 * d) = w;
+}
+
+__device__ __forceinline__ float lse_of(float ref, float sum) {
+    return sum > 0.0f || sum != sum ? (ref + __builtin_amdgcn_logf(sum)) * LN2 : -__builtin_inff();
+}
+
+// ---- few rows: 16 rows by 32 keys a wave ----------------------------------------
+
+constexpr int DEC_WAVES = 4, DEC_ROWS = 16, DEC_KEYS = 32;
+
+template <class E, bool KV8, int DP>
+struct Dec {
+    using R = Rows<DP, KV8, 16>;
+    static constexpr int HALF = DEC_KEYS * R::BYTES;         // K rows, then V rows
+    static constexpr int STAGE = 2 * HALF;
+    static constexpr int NST = KV8 && DP <= 64 ? 4 : (KV8 || DP <= 64 ? 3 : 2);
+    static constexpr int LOADS = 2 * DEC_KEYS * R::CH / 64;  // direct loads of a stage
+    static constexpr int RING = NST * STAGE;
+    static constexpr int OROW = DP * 4 + 16;                 // bytes of a row of outputs in LDS
+    static_assert(DEC_ROWS * OROW <= RING, "a wave's outputs fit its ring");
+    static_assert((NST - 1) * LOADS < 64, "vmcnt range");
+};
+
+// One wave's share of a tile: issue the loads of key tile `tile`; returns
+// which of its 32 keys exist.  Keys that do not exist are staged as copies of
+// one that does (their weight is zero), so that the count of loads is fixed.
+template <class E, bool KV8, int DP>
+__device__ __forceinline__ uint32_t dec_issue(const AttnArgs& a, const char* kb, const char* vb, const int* pages,
+                                              int first, int tile, int lo, int hi, MPDT_LDS char* dst) {
+    using D = Dec<E, KV8, DP>;
+    using R = typename D::R;
+    const int lane = threadIdx.x & 63;
+    int64_t off;
+    const bool ok = key_offset(a.kv, pages, first, tile * DEC_KEYS + (lane & 31), lo, hi, off);
+    const uint32_t mask = (uint32_t)__ballot(ok);
+    if (mask != 0xffffffffu) {
+        const int64_t other = shfl64(off, mask ? __builtin_ctz(mask) : 0);
+        if (!ok) off = other;
+    }
+    const int row_bytes = a.kv.dim * (KV8 ? 1 : 2);
+#pragma unroll
+    for (int i = 0; i < DEC_KEYS * R::CH / 64; ++i) {
+        const int c = i * 64 + lane, r = c / R::CH, pos = c % R::CH;
+        const int64_t o = shfl64(off, r);
+        int ck = (pos ^ R::swz_k(r)) * 16, cv = (pos ^ R::swz_v(r)) * 16;
+        if (ck >= row_bytes) ck = 0;
+        if (cv >= row_bytes) cv = 0;
+        global_to_lds16(kb + o + ck, dst + i * 1024);
+        global_to_lds16(vb + o + cv, dst + D::HALF + i * 1024);
+    }
+    return mask;
+}
+
+template <class E, class EP, bool KV8, int DP, bool CAP>
+__device__ __forceinline__ void dec_tile(const MPDT_LDS char* st, const u32x4 (&qf)[DP / 32], const Score& sc,
+                                         uint32_t mask, bool edge, int key0, int qpos, int qlow, float& ref,
+                                         float& sum, f32x4 (&o)[DP / 16]) {
+    using D = Dec<E, KV8, DP>;
+    using R = typename D::R;
+    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    f32x4 s[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+        const int r = 16 * ks + n;
+#pragma unroll
+        for (int d = 0; d < DP / 32; ++d) {
+            u32x4 kf;
+            if constexpr (KV8) {
+                kf = widen8<E>(lds_load8(st, r * R::BYTES + ((2 * d + (g >> 1)) ^ R::swz_k(r)) * 16 + (g & 1) * 8));
+            } else {
+                kf = lds_load16(st, r * R::BYTES + ((4 * d + g) ^ R::swz_k(r)) * 16);
+            }
+            s[ks] = E::mma16(kf, qf[d], s[ks]);
+        }
+    }
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = score<CAP>(sc, s[i >> 2][i & 3]);
+    if (edge) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int j = 16 * (i >> 2) + 4 * g + (i & 3);
+            const bool see = ((mask >> j) & 1) && key0 + j <= qpos && key0 + j > qlow;
+            if (!see) x[i] = -__builtin_inff();
+        }
+    }
+    float m = x[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = fmaxf(m, x[i]);
+    m = fmaxf(m, __shfl_xor(m, 16));
+    m = fmaxf(m, __shfl_xor(m, 32)) - EP::P_SHIFT;
+    if (__ballot(m > ref + RESCALE)) {
+        const float to = fmaxf(m, ref), f = __builtin_amdgcn_exp2f(ref - to);
+        ref = to;
+        sum *= f;
+#pragma unroll
+        for (int t = 0; t < DP / 16; ++t) o[t] *= f;
+    }
+    u32x4 p;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        x[i] = __builtin_amdgcn_exp2f(x[i] - ref);
+        sum += x[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = EP::pack(x[2 * i], x[2 * i + 1]);
+    const MPDT_LDS char* sv = st + D::HALF;
+#pragma unroll
+    for (int t = 0; t < DP / 16; ++t) {
+        u32x4 vf;
+        if constexpr (KV8) {
+            const int h = n >> 1, r = (h < 4 ? 4 * g + h : 16 + 4 * g + h - 4);
+            vf = widen8<EP>(lds_read_tr8(sv, r * R::BYTES + (t ^ R::swz_v(r)) * 16 + (n & 1) * 8));
+        } else {
+            const int r = 4 * g + (n >> 2), c = 2 * t + ((n & 3) >> 1), b = (n & 1) * 8;
+            const u32x2 v0 = lds_read_tr16(sv, r * R::BYTES + (c ^ R::swz_v(r)) * 16 + b);
+            const u32x2 v1 = lds_read_tr16(sv, (r + 16) * R::BYTES + (c ^ R::swz_v(r + 16)) * 16 + b);
+            vf = u32x4{v0[0], v0[1], v1[0], v1[1]};
+        }
+        o[t] = EP::mma16(vf, p, o[t]);
+    }
+}
+
+// DIRECT: one workgroup to a unit, no plan and no joining.
+template <class E, class EP, bool KV8, int DP, bool CAP, bool DIRECT>
+__global__ __launch_bounds__(64 * DEC_WAVES) void attn_decode_kernel(AttnArgs a) {
+    using D = Dec<E, KV8, DP>;
+    __shared__ __attribute__((aligned(1024))) char smem[DEC_WAVES * D::RING];
+    __shared__ int pages[PAGES_LDS];
+    __shared__ float ml[2][DEC_WAVES][DEC_ROWS];
+    __shared__ int red[DEC_WAVES], box[2];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n = lane & 15, g = lane >> 4;
+    MPDT_LDS char* ring = lds_cast(smem) + wave * D::RING;
+
+    Plan p;
+    int64_t at = 0, stop = 0, share = 1;
+    int worker = 0, line = 0, e = 0, h = 0;
+    int b, r0, t0, tiles;
+    if constexpr (DIRECT) {
+        find_entry<DEC_WAVES>(a, blockIdx.x, red, box);
+        b = box[0];
+        r0 = box[1];
+        h = blockIdx.y;
+        if (b < 0) return;
+        at = 0;
+        stop = 1;
+    } else {
+        plan_layout(a.ws, a.entries, a.sv.seqs, a.workers, a.tile_rows, DP, &p);
+        line = p.head[1];
+        const int entries = p.head[0];
+        const int64_t total = (int64_t)line * a.kv.kv_heads;
+        share = share_of(a, total);
+        worker = worker_id();
+        at = worker * share;
+        stop = min(at + share, total);
+        if (at >= stop) return;
+        h = (int)(at / line);
+        const int rem = (int)(at - (int64_t)h * line);
+        int lo = 0, hi = entries;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (p.before[mid] <= rem) lo = mid;
+            else hi = mid;
+        }
+        e = lo;
+    }
+    bool lead = true;    // the first stretch of this workgroup
+    while (at < stop) {
+        int seg_a, seg_e;      // key tiles of this stretch within the unit
+        bool whole = true;
+        if constexpr (!DIRECT) {
+            const i32x4 ent = p.entry[e];
+            b = ent[0];
+            r0 = ent[1];
+            t0 = ent[2];
+            tiles = ent[3];
+            const int64_t u0 = (int64_t)h * line + p.before[e];
+            seg_a = (int)(at - u0);
+            seg_e = (int)min((int64_t)tiles, stop - u0);
+            whole = seg_a == 0 && seg_e == tiles;
+        }
+        const Seq s = seq_of(a.sv, a.kv.page_size, b);
+        const int rows = s.nq * a.group, r1 = min(r0 + DEC_ROWS, rows);
+        const Span32 kr = keys_of(s, a.group, a.window, r0, r1);
+        if constexpr (DIRECT) {
+            t0 = kr.lo / DEC_KEYS;
+            tiles = max((kr.hi + DEC_KEYS - 1) / DEC_KEYS - t0, 1);
+            seg_a = 0;
+            seg_e = tiles;
+        }
+        // this lane's row
+        const int row = r0 + n, tok = row / a.group, qh = h * a.group + row % a.group;
+        const bool live = row < r1;
+        const int qpos = s.n - s.nq + tok, qlow = a.window > 0 ? qpos - a.window : -1;
+        u32x4 qf[DP / 32];
+#pragma unroll
+        for (int d = 0; d < DP / 32; ++d) {
+            const int c = 32 * d + 8 * g;
+            qf[d] = u32x4{0, 0, 0, 0};
+            if (live && c < a.kv.dim)
+                qf[d] = *reinterpret_cast<const u32x4*>(a.q + (int64_t)(s.start + tok) * a.q_tok_b +
+                                                        qh * a.q_head_b + 2 * c);
+        }
+        const Score sc = score_of(a, KV8 ? a.kv.k_scale[h] : 1.0f);
+        const char* kb = a.kv.k + h * a.kv.head_b;
+        const char* vb = a.kv.v + h * a.kv.head_b;
+        // rows of this tile see every key below `all_hi` and from `all_lo` on
+        const int all_hi = s.n - s.nq + r0 / a.group + 1;
+        const int all_lo = a.window > 0 ? s.n - s.nq + (r1 - 1) / a.group - a.window + 1 : 0;
+        float ref = NO_MAX, sum = 0.0f;
+        f32x4 o[DP / 16];
+#pragma unroll
+        for (int t = 0; t < DP / 16; ++t) o[t] = f32x4{0, 0, 0, 0};
+
+        for (int pos = seg_a; pos < seg_e;) {
+            int first;
+            const int upto = fetch_pages<64 * DEC_WAVES, DEC_KEYS>(a, b, t0 + pos, t0 + seg_e, pages, first) - t0;
+            uint32_t mask[D::NST];
+#pragma unroll
+            for (int i = 0; i < D::NST - 1; ++i) {
+                const int j = pos + wave + i * DEC_WAVES;
+                mask[i] = 0;
+                if (j < upto)
+                    mask[i] = dec_issue<E, KV8, DP>(a, kb, vb, pages, first, t0 + j, kr.lo, kr.hi,
+                                                    ring + i * D::STAGE);
+            }
+            int slot = 0;
+            for (int j = pos + wave; j < upto; j += DEC_WAVES) {
+                // the stage freed by the last tile takes the loads of the one NST - 1 on
+                const int ahead = j + (D::NST - 1) * DEC_WAVES;
+                const int fill = slot == 0 ? D::NST - 1 : slot - 1;
+                mask[D::NST - 1] = 0;
+                wait_lds();      // the last tile's reads of that stage have come back
+                if (ahead < upto) {
+                    mask[D::NST - 1] = dec_issue<E, KV8, DP>(a, kb, vb, pages, first, t0 + ahead, kr.lo, kr.hi,
+                                                             ring + fill * D::STAGE);
+                    wait_vmem<(D::NST - 1) * D::LOADS>();
+                } else {
+                    wait_vmem<0>();
+                }
+                __atomic_signal_fence(__ATOMIC_SEQ_CST);
+                __builtin_amdgcn_sched_barrier(0);
+                const int key0 = (t0 + j) * DEC_KEYS;
+                if (mask[0]) {
+                    const bool edge = mask[0] != 0xffffffffu || key0 + DEC_KEYS > all_hi || key0 < all_lo;
+                    dec_tile<E, EP, KV8, DP, CAP>(ring + slot * D::STAGE, qf, sc, mask[0], edge, key0, qpos, qlow,
+                                                  ref, sum, o);
+                }
+                __atomic_signal_fence(__ATOMIC_SEQ_CST);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int i = 0; i + 1 < D::NST; ++i) mask[i] = mask[i + 1];
+                slot = slot + 1 == D::NST ? 0 : slot + 1;
+            }
+            pos = upto;
+            __syncthreads();
+        }
+
+        // join the four waves: each writes its rows over its own ring
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        wait_lds();
+#pragma unroll
+        for (int t = 0; t < DP / 16; ++t)
+            lds_store16(ring, n * D::OROW + (16 * t + 4 * g) * 4, __builtin_bit_cast(u32x4, o[t]));
+        if (g == 0) {
+            ml[0][wave][n] = ref;
+            ml[1][wave][n] = sum;
+        }
+        __syncthreads();
+        {
+            const int rr = tid >> 4, dc = tid & 15;
+            float top = NO_MAX, den = 0.0f, w[DEC_WAVES];
+#pragma unroll
+            for (int i = 0; i < DEC_WAVES; ++i) top = fmaxf(top, ml[0][i][rr]);
+#pragma unroll
+            for (int i = 0; i < DEC_WAVES; ++i) {
+                w[i] = __builtin_amdgcn_exp2f(ml[0][i][rr] - top);
+                den += w[i] * ml[1][i][rr];
+            }
+            const int orow = r0 + rr, ot = orow / a.group, oh = h * a.group + orow % a.group;
+            const float inv = (den > 0.0f || den != den ? 1.0f / den : 0.0f) * (KV8 ? a.kv.v_scale[h] : 1.0f);
+            const int64_t slot_row = ((int64_t)worker * 2 + (lead ? 0 : 1)) * DEC_ROWS + rr;
+#pragma unroll
+            for (int k = 0; k < (DP + 63) / 64; ++k) {
+                const int d = 4 * dc + 64 * k;
+                if (d >= DP) break;
+                f32x4 v{0, 0, 0, 0};
+#pragma unroll
+                for (int i = 0; i < DEC_WAVES; ++i)
+                    v += w[i] * __builtin_bit_cast(f32x4, lds_load16(lds_cast(smem) + i * D::RING,
+                                                                     rr * D::OROW + d * 4));
+                if (whole) {
+                    if (orow < r1 && d < a.kv.dim)
+                        store_out4(a, a.out + (int64_t)(s.start + ot) * a.o_tok_b + oh * a.o_head_b, d, v * inv);
+                } else {
+                    *reinterpret_cast<f32x4*>(p.part_o + slot_row * DP + d) = v;
+                }
+            }
+            if (dc == 0) {
+                if (whole) {
+                    if (orow < r1 && a.lse) a.lse[(int64_t)(s.start + ot) * a.lse_tok + oh] = lse_of(top, den);
+                } else {
+                    p.part_ml[slot_row] = f32x2{top, den};
+                }
+            }
+        }
+        __syncthreads();
+        if constexpr (DIRECT) return;
+        at += seg_e - seg_a;
+        lead = false;
+        if (++e == p.head[0]) {
+            e = 0;
+            ++h;
+        }
+    }
+}
+
+// Units that several workers share: their partial sums joined in the order of
+// the keys.  One workgroup to 16 rows of a unit.
+template <int DP>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
+    Plan p;
+    plan_layout(a.ws, a.entries, a.sv.seqs, a.workers, a.tile_rows, DP, &p);
+    const int e = blockIdx.x, h = blockIdx.y, rr = blockIdx.z * 16 + (threadIdx.x >> 4), dc = threadIdx.x & 15;
+    if (e >= p.head[0]) return;
+    const int line = p.head[1];
+    const i32x4 ent = p.entry[e];
+    const int64_t u0 = (int64_t)h * line + p.before[e], u1 = u0 + ent[3];
+    const int64_t share = share_of(a, (int64_t)line * a.kv.kv_heads);
+    const int w0 = (int)(u0 / share), w1 = (int)((u1 - 1) / share);
+    if (w0 == w1) return;
+    const Seq s = seq_of(a.sv, a.kv.page_size, ent[0]);
+    const int row = ent[1] + rr;
+    if (row >= s.nq * a.group) return;
+    float top = NO_MAX;
+    for (int w = w0; w <= w1; ++w) {
+        const int64_t sr = ((int64_t)w * 2 + (w * share >= u0 ? 0 : 1)) * a.tile_rows + rr;
+        top = fmaxf(top, p.part_ml[sr][0]);
+    }
+    float den = 0.0f;
+    f32x4 v[(DP + 63) / 64];
+#pragma unroll
+    for (int k = 0; k < (DP + 63) / 64; ++k) v[k] = f32x4{0, 0, 0, 0};
+    for (int w = w0; w <= w1; ++w) {
+        const int64_t sr = ((int64_t)w * 2 + (w * share >= u0 ? 0 : 1)) * a.tile_rows + rr;
+        const f32x2 ml = p.part_ml[sr];
+        const float f = __builtin_amdgcn_exp2f(ml[0] - top);
+        den += f * ml[1];
+#pragma unroll
+        for (int k = 0; k < (DP + 63) / 64; ++k)
+            if (4 * dc + 64 * k < DP)
+                v[k] += f * *reinterpret_cast<const f32x4*>(p.part_o + sr * DP + 4 * dc + 64 * k);
+    }
+    const int tok = row / a.group, qh = h * a.group + row % a.group;
+    const float inv = (den > 0.0f || den != den ? 1.0f / den : 0.0f) *
+                      (a.kv.type == DT_E4M3 ? a.kv.v_scale[h] : 1.0f);
+    char* orow = a.out + (int64_t)(s.start + tok) * a.o_tok_b + qh * a.o_head_b;
+#pragma unroll
+    for (int k = 0; k < (DP + 63) / 64; ++k)
+        if (4 * dc + 64 * k < a.kv.dim) store_out4(a, orow, 4 * dc + 64 * k, v[k] * inv);
+    if (dc == 0 && a.lse) a.lse[(int64_t)(s.start + tok) * a.lse_tok + qh] = lse_of(top, den);
+}
+
+// ---- many rows: 256 rows by 64 keys a workgroup ------------------------------------
+
+constexpr int CHK_WAVES = 4, CHK_QS = 2, CHK_ROWS = CHK_WAVES * CHK_QS * 32, CHK_KEYS = 64, CHK_NST = 3;
+
+template <bool KV8, int DP>
+struct Chk {
+    using R = Rows<DP, KV8, 32>;
+    static constexpr int HALF = CHK_KEYS * R::BYTES;
+    static constexpr int STAGE = 2 * HALF;
+    static constexpr int PER = CHK_KEYS * R::CH / 64 / CHK_WAVES;   // loads of K (and of V) a wave
+    static constexpr int LOADS = 2 * PER;
+};
+
+template <bool KV8, int DP>
+__device__ __forceinline__ uint64_t chk_issue(const AttnArgs& a, const char* kb, const char* vb, const int* pages,
+                                              int first, int tile, int lo, int hi, MPDT_LDS char* dst) {
+    using D = Chk<KV8, DP>;
+    using R = typename D::R;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int64_t off;
+    const bool ok = key_offset(a.kv, pages, first, tile * CHK_KEYS + lane, lo, hi, off);
+    const uint64_t mask = __ballot(ok);
+    if (~mask) {
+        const int64_t other = shfl64(off, mask ? __builtin_ctzll(mask) : 0);
+        if (!ok) off = other;
+    }
+    const int row_bytes = a.kv.dim * (KV8 ? 1 : 2);
+#pragma unroll
+    for (int i = 0; i < D::PER; ++i) {
+        const int ii = wave * D::PER + i;
+        const int c = ii * 64 + lane, r = c / R::CH, pos = c % R::CH;
+        const int64_t o = shfl64(off, r);
+        int ck = (pos ^ R::swz_k(r)) * 16, cv = (pos ^ R::swz_v(r)) * 16;
+        if (ck >= row_bytes) ck = 0;
+        if (cv >= row_bytes) cv = 0;
+        global_to_lds16(kb + o + ck, dst + ii * 1024);
+        global_to_lds16(vb + o + cv, dst + D::HALF + ii * 1024);
+    }
+    return mask;
+}
+
+template <class E, class EP, bool KV8, int DP, bool CAP>
+__device__ __forceinline__ void chk_tile(const MPDT_LDS char* st, const u32x4 (&qf)[CHK_QS][DP / 16],
+                                         const Score& sc, uint64_t mask, bool edge, int key0,
+                                         const int (&qpos)[CHK_QS], const int (&qlow)[CHK_QS], float (&ref)[CHK_QS],
+                                         float (&sum)[CHK_QS], f32x16 (&o)[CHK_QS][(DP + 31) / 32]) {
+    using D = Chk<KV8, DP>;
+    using R = typename D::R;
+    const int lane = threadIdx.x & 63, n = lane & 31, h = lane >> 5;
+    constexpr int DT = (DP + 31) / 32;
+    f32x16 s[CHK_QS][2];
+#pragma unroll
+    for (int q = 0; q < CHK_QS; ++q)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[q][ks][i] = 0.0f;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+        const int r = 32 * ks + n;
+#pragma unroll
+        for (int d = 0; d < DP / 16; ++d) {
+            u32x4 kf;
+            if constexpr (KV8) {
+                kf = widen8<E>(lds_load8(st, r * R::BYTES + (d ^ R::swz_k(r)) * 16 + h * 8));
+            } else {
+                kf = lds_load16(st, r * R::BYTES + ((2 * d + h) ^ R::swz_k(r)) * 16);
+            }
+#pragma unroll
+            for (int q = 0; q < CHK_QS; ++q) s[q][ks] = E::mma32(kf, qf[q][d], s[q][ks]);
+        }
+    }
+    u32x4 p[CHK_QS][4];
+#pragma unroll
+    for (int q = 0; q < CHK_QS; ++q) {
+        float m = NO_MAX;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float x = score<CAP>(sc, s[q][ks][i]);
+                if (edge) {
+                    const int j = 32 * ks + 8 * (i >> 2) + 4 * h + (i & 3);
+                    const bool see = ((mask >> j) & 1) && key0 + j <= qpos[q] && key0 + j > qlow[q];
+                    if (!see) x = -__builtin_inff();
+                }
+                s[q][ks][i] = x;
+                m = fmaxf(m, x);
+            }
+        m = fmaxf(m, __shfl_xor(m, 32)) - EP::P_SHIFT;
+        if (__ballot(m > ref[q] + RESCALE)) {
+            const float to = fmaxf(m, ref[q]), f = __builtin_amdgcn_exp2f(ref[q] - to);
+            ref[q] = to;
+            sum[q] *= f;
+#pragma unroll
+            for (int t = 0; t < DT; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[q][t][i] *= f;
+        }
+        float add = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[q][ks][i] = __builtin_amdgcn_exp2f(s[q][ks][i] - ref[q]);
+                add += s[q][ks][i];
+            }
+        sum[q] += add;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                p[q][kk][i] = EP::pack(s[q][kk >> 1][8 * (kk & 1) + 2 * i], s[q][kk >> 1][8 * (kk & 1) + 2 * i + 1]);
+    }
+    const MPDT_LDS char* sv = st + D::HALF;
+    const int l16 = lane & 15, sub = (lane >> 4) & 1;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+        for (int t = 0; t < DT; ++t) {
+            u32x4 vf;
+            if constexpr (KV8) {
+                const int k = l16 >> 1, r = 16 * kk + 4 * h + (k < 4 ? k : k + 4);
+                vf = widen8<EP>(lds_read_tr8(sv, r * R::BYTES + ((2 * t + sub) ^ R::swz_v(r)) * 16 + (l16 & 1) * 8));
+            } else {
+                const int r = 16 * kk + 4 * h + (l16 >> 2), c = 4 * t + 2 * sub + ((l16 & 3) >> 1), b = (l16 & 1) * 8;
+                const u32x2 v0 = lds_read_tr16(sv, r * R::BYTES + (c ^ R::swz_v(r)) * 16 + b);
+                const u32x2 v1 = lds_read_tr16(sv, (r + 8) * R::BYTES + (c ^ R::swz_v(r + 8)) * 16 + b);
+                vf = u32x4{v0[0], v0[1], v1[0], v1[1]};
+            }
+#pragma unroll
+            for (int q = 0; q < CHK_QS; ++q) o[q][t] = EP::mma32(vf, p[q][kk], o[q][t]);
+        }
+    }
+}
+
+template <class E, class EP, bool KV8, int DP, bool CAP>
+__global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(1, 1))) void attn_chunk_kernel(
+    AttnArgs a) {
+    using D = Chk<KV8, DP>;
+    constexpr int DT = (DP + 31) / 32;
+    __shared__ __attribute__((aligned(1024))) char smem[CHK_NST * D::STAGE];
+    __shared__ int pages[PAGES_LDS];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n = lane & 31, half = lane >> 5;
+    MPDT_LDS char* lds = lds_cast(smem);
+    Plan p;
+    plan_layout(a.ws, a.entries, a.sv.seqs, a.workers, a.tile_rows, DP, &p);
+    const int line = p.head[1], entries = p.head[0];
+    const int64_t total = (int64_t)line * a.kv.kv_heads, share = share_of(a, total);
+    const int worker = worker_id();
+    int64_t at = worker * share;
+    const int64_t stop = min(at + share, total);
+    if (at >= stop) return;
+    int h = (int)(at / line), e;
+    {
+        const int rem = (int)(at - (int64_t)h * line);
+        int lo = 0, hi = entries;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (p.before[mid] <= rem) lo = mid;
+            else hi = mid;
+        }
+        e = lo;
+    }
+    bool lead = true;
+    while (at < stop) {
+        const i32x4 ent = p.entry[e];
+        const int b = ent[0], r0 = ent[1], t0 = ent[2], tiles = ent[3];
+        const int64_t u0 = (int64_t)h * line + p.before[e];
+        const int seg_a = (int)(at - u0), seg_e = (int)min((int64_t)tiles, stop - u0);
+        const bool whole = seg_a == 0 && seg_e == tiles;
+        const Seq s = seq_of(a.sv, a.kv.page_size, b);
+        const int rows = s.nq * a.group, r1 = min(r0 + CHK_ROWS, rows);
+        const Span32 kr = keys_of(s, a.group, a.window, r0, r1);
+        const int past = s.n - s.nq;
+        // this wave's rows: [w0, w1)
+        const int w0 = r0 + wave * 32 * CHK_QS, w1 = min(w0 + 32 * CHK_QS, r1);
+        const bool busy = w0 < w1;
+        const int w_hi = busy ? past + (w1 - 1) / a.group : -1;          // last key that any of them sees
+        const int all_hi = busy ? past + w0 / a.group + 1 : 0;           // every one sees keys below
+        const int all_lo = a.window > 0 && busy ? past + (w1 - 1) / a.group - a.window + 1 : 0;
+        const int w_lo = a.window > 0 && busy ? past + w0 / a.group - a.window + 1 : 0;
+        int qpos[CHK_QS], qlow[CHK_QS];
+        u32x4 qf[CHK_QS][DP / 16];
+        float ref[CHK_QS], sum[CHK_QS];
+        f32x16 o[CHK_QS][DT];
+#pragma unroll
+        for (int q = 0; q < CHK_QS; ++q) {
+            const int row = w0 + 32 * q + n, tok = row / a.group, qh = h * a.group + row % a.group;
+            qpos[q] = past + tok;
+            qlow[q] = a.window > 0 ? qpos[q] - a.window : -1;
+            ref[q] = NO_MAX;
+            sum[q] = 0.0f;
+#pragma unroll
+            for (int d = 0; d < DP / 16; ++d) {
+                const int c = 16 * d + 8 * half;
+                qf[q][d] = u32x4{0, 0, 0, 0};
+                if (row < r1 && c < a.kv.dim)
+                    qf[q][d] = *reinterpret_cast<const u32x4*>(a.q + (int64_t)(s.start + tok) * a.q_tok_b +
+                                                               qh * a.q_head_b + 2 * c);
+            }
+#pragma unroll
+            for (int t = 0; t < DT; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[q][t][i] = 0.0f;
+        }
+        const Score sc = score_of(a, KV8 ? a.kv.k_scale[h] : 1.0f);
+        const char* kb = a.kv.k + h * a.kv.head_b;
+        const char* vb = a.kv.v + h * a.kv.head_b;
+
+        for (int pos = seg_a; pos < seg_e;) {
+            int first;
+            const int upto = fetch_pages<64 * CHK_WAVES, CHK_KEYS>(a, b, t0 + pos, t0 + seg_e, pages, first) - t0;
+            uint64_t m0 = 0, m1 = 0, m2 = 0;
+            m0 = chk_issue<KV8, DP>(a, kb, vb, pages, first, t0 + pos, kr.lo, kr.hi, lds);
+            if (pos + 1 < upto)
+                m1 = chk_issue<KV8, DP>(a, kb, vb, pages, first, t0 + pos + 1, kr.lo, kr.hi, lds + D::STAGE);
+            int slot = 0;
+            for (int j = pos; j < upto; ++j) {
+                if (j + 1 < upto) wait_vmem<D::LOADS>();
+                else wait_vmem<0>();
+                wait_lds();
+                wg_barrier();    // tile j has landed for all waves, and all are done with tile j - 1
+                if (j + 2 < upto) {
+                    const int fill = slot == 0 ? 2 : slot - 1;
+                    m2 = chk_issue<KV8, DP>(a, kb, vb, pages, first, t0 + j + 2, kr.lo, kr.hi,
+                                            lds + fill * D::STAGE);
+                }
+                const int key0 = (t0 + j) * CHK_KEYS;
+                if (m0 && busy && key0 <= w_hi && key0 + CHK_KEYS > w_lo) {
+                    const bool edge = ~m0 || key0 + CHK_KEYS > all_hi || key0 < all_lo;
+                    chk_tile<E, EP, KV8, DP, CAP>(lds + slot * D::STAGE, qf, sc, m0, edge, key0, qpos, qlow, ref, sum,
+                                                  o);
+                }
+                m0 = m1;
+                m1 = m2;
+                slot = slot == 2 ? 0 : slot + 1;
+            }
+            pos = upto;
+            wait_lds();
+            wg_barrier();    // page numbers and stages are free again
+        }
+
+#pragma unroll
+        for (int q = 0; q < CHK_QS; ++q) {
+            const float den = sum[q] + __shfl_xor(sum[q], 32);
+            const int in_tile = wave * 32 * CHK_QS + 32 * q + n, row = r0 + in_tile;
+            const int tok = row / a.group, qh = h * a.group + row % a.group;
+            if (row >= r1) continue;
+            if (whole) {
+                const float inv = (den > 0.0f || den != den ? 1.0f / den : 0.0f) * (KV8 ? a.kv.v_scale[h] : 1.0f);
+                char* orow = a.out + (int64_t)(s.start + tok) * a.o_tok_b + qh * a.o_head_b;
+#pragma unroll
+                for (int t = 0; t < DT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int d = 32 * t + 8 * i + 4 * half;
+                        if (d < a.kv.dim)
+                            store_out4(a, orow, d, f32x4{o[q][t][4 * i], o[q][t][4 * i + 1], o[q][t][4 * i + 2],
+                                                         o[q][t][4 * i + 3]} * inv);
+                    }
+                if (half == 0 && a.lse) a.lse[(int64_t)(s.start + tok) * a.lse_tok + qh] = lse_of(ref[q], den);
+            } else {
+                const int64_t sr = ((int64_t)worker * 2 + (lead ? 0 : 1)) * CHK_ROWS + in_tile;
+#pragma unroll
+                for (int t = 0; t < DT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<f32x4*>(p.part_o + sr * DP + 32 * t + 8 * i + 4 * half) =
+                            f32x4{o[q][t][4 * i], o[q][t][4 * i + 1], o[q][t][4 * i + 2], o[q][t][4 * i + 3]};
+                if (half == 0) p.part_ml[sr] = f32x2{ref[q], den};
+            }
+        }
+        at += seg_e - seg_a;
+        lead = false;
+        if (++e == entries) {
+            e = 0;
+            ++h;
+        }
+    }
+}
+
+// ---- choice and launch -----------------------------------------------------------
+
+constexpr int DP_OF(int dim) { return dim <= 64 ? 64 : dim <= 96 ? 96 : 128; }
+constexpr int CUS = 256;
+constexpr int DIRECT_KEYS = 1024;   // caches at most this long: one launch, a workgroup to a unit
+
+struct Shape {
+    bool few, direct;
+    int tile_rows, key_tile, workers, min_tiles, entries;
+};
+
+// Few rows to a sequence on average: the 16-row kernel.  Above, a 256-row tile
+// reads the cache once where 16-row tiles would read it rows / 16 times.
+Shape shape_of(const AttnArgs& a) {
+    Shape s;
+    const int64_t rows = (int64_t)a.sv.tokens * a.group;
+    s.few = rows <= (int64_t)32 * a.sv.seqs;
+    s.direct = s.few && (int64_t)a.sv.width * a.kv.page_size <= DIRECT_KEYS;
+    s.tile_rows = s.few ? DEC_ROWS : CHK_ROWS;
+    s.key_tile = s.few ? DEC_KEYS : CHK_KEYS;
+    s.workers = CUS;
+    s.min_tiles = 4;
+    s.entries = (int)(rows / s.tile_rows + std::min<int64_t>(a.sv.seqs, a.sv.tokens));
+    return s;
+}
+
+template <class E, class EP, bool KV8, int DP, bool CAP>
+hipError_t launch_as(const AttnArgs& a, const Shape& s, hipStream_t stream) {
+    hipError_t err;
+    if (s.direct) {
+        hipLaunchKernelGGL((attn_decode_kernel<E, EP, KV8, DP, CAP, true>),
+                           dim3((unsigned)s.entries, (unsigned)a.kv.kv_heads), dim3(64 * DEC_WAVES), 0, stream, a);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL(attn_plan_kernel, dim3(1), dim3(1024), 0, stream, a, s.key_tile);
+    if ((err = hipGetLastError()) != hipSuccess) return err;
+    if (s.few) {
+        hipLaunchKernelGGL((attn_decode_kernel<E, EP, KV8, DP, CAP, false>), dim3((unsigned)s.workers),
+                           dim3(64 * DEC_WAVES), 0, stream, a);
+    } else {
+        hipLaunchKernelGGL((attn_chunk_kernel<E, EP, KV8, DP, CAP>), dim3((unsigned)s.workers), dim3(64 * CHK_WAVES),
+                           0, stream, a);
+    }
+    if ((err = hipGetLastError()) != hipSuccess) return err;
+    hipLaunchKernelGGL((attn_join_kernel<DP>), dim3((unsigned)s.entries, (unsigned)a.kv.kv_heads, s.tile_rows / 16),
+                       dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
+template <class E, class EP, bool KV8, int DP>
+hipError_t launch_cap(const AttnArgs& a, const Shape& s, hipStream_t stream) {
+    return a.softcap > 0.0f ? launch_as<E, EP, KV8, DP, true>(a, s, stream)
+                            : launch_as<E, EP, KV8, DP, false>(a, s, stream);
+}
+
+template <class E, class EP, bool KV8>
+hipError_t launch_dim(const AttnArgs& a, const Shape& s, hipStream_t stream) {
+    switch (DP_OF(a.kv.dim)) {
+        case 64: return launch_cap<E, EP, KV8, 64>(a, s, stream);
+        case 96: return launch_cap<E, EP, KV8, 96>(a, s, stream);
+        default: return launch_cap<E, EP, KV8, 128>(a, s, stream);
+    }
+}
+
+}  // namespace
+
+int64_t attn_workspace(const AttnArgs& a) {
+    const Shape s = shape_of(a);
+    if (s.direct) return 0;
+    Plan p;
+    return plan_layout(nullptr, s.entries, a.sv.seqs, s.workers, s.tile_rows, DP_OF(a.kv.dim), &p);
+}
+
+hipError_t launch_paged_attention(const AttnArgs& in, hipStream_t stream) {
+    AttnArgs a = in;
+    const Shape s = shape_of(a);
+    a.tile_rows = s.tile_rows;
+    a.entries = s.entries;
+    a.workers = s.workers;
+    a.min_tiles = s.min_tiles;
+    const bool kv8 = a.kv.type == DT_E4M3;
+    if (a.q_type == DT_BF16) {
+        return kv8 ? launch_dim<Bf16, F16, true>(a, s, stream) : launch_dim<Bf16, Bf16, false>(a, s, stream);
+    }
+    return kv8 ? launch_dim<F16, F16, true>(a, s, stream) : launch_dim<F16, F16, false>(a, s, stream);
+}
+
+}  // namespace mpdt
