@@ -360,6 +360,13 @@ __device__ __forceinline__ int64_t shfl64(int64_t v, int lane) {
     return (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo);
 }
 
+// Bits first to last (both may lie outside 0 to 63) of a 64-bit word.
+__device__ __forceinline__ uint64_t from_to(int first, int last) {
+    const uint64_t upto = last >= 63 ? ~0ull : last < 0 ? 0 : (2ull << last) - 1;
+    const uint64_t below = first >= 64 ? ~0ull : first <= 0 ? 0 : (1ull << first) - 1;
+    return upto & ~below;
+}
+
 // Score in base-2 logarithms: s * c, or capped.
 struct Score {
     float mul, cap2, inner;   // inner: 2 * log2(e) * scale / cap
@@ -469,11 +476,10 @@ __device__ __forceinline__ void dec_tile(const MPDT_LDS char* st, const u32x4 (&
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = score<CAP>(sc, s[i >> 2][i & 3]);
     if (edge) {
+        const uint32_t seen = (mask & (uint32_t)from_to(qlow + 1 - key0, qpos - key0)) >> (4 * g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int j = 16 * (i >> 2) + 4 * g + (i & 3);
-            const bool see = ((mask >> j) & 1) && key0 + j <= qpos && key0 + j > qlow;
-            if (!see) x[i] = -__builtin_inff();
+            x[i] = seen & (1u << (16 * (i >> 2) + (i & 3))) ? x[i] : -__builtin_inff();
         }
     }
     float m = x[0];
@@ -756,24 +762,32 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
 }
 
 // ---- many rows: 256 rows by 64 keys a workgroup ------------------------------------
+//
+// Eight waves of 32 rows, two to a SIMD.  The two take turns: while one runs
+// the MFMAs of O += V P of a tile and S of the next, the other runs its
+// softmax, so that matrix and vector units both work all the time; barriers
+// between the two phases keep them apart.  K and V tiles are shared by the
+// eight waves in a ring of CHK_NST stages.
 
-constexpr int CHK_WAVES = 4, CHK_QS = 2, CHK_ROWS = CHK_WAVES * CHK_QS * 32, CHK_KEYS = 64, CHK_NST = 3;
+constexpr int CHK_WAVES = 8, CHK_ROWS = CHK_WAVES * 32, CHK_KEYS = 64;
 
 template <bool KV8, int DP>
 struct Chk {
     using R = Rows<DP, KV8, 32>;
     static constexpr int HALF = CHK_KEYS * R::BYTES;
     static constexpr int STAGE = 2 * HALF;
-    static constexpr int PER = CHK_KEYS * R::CH / 64 / CHK_WAVES;   // loads of K (and of V) a wave
-    static constexpr int LOADS = 2 * PER;
+    static constexpr int NST = 4;
+    static constexpr int LOADS = 2 * R::CH / CHK_WAVES;   // direct loads of a tile by a wave
+    static_assert(2 * R::CH % CHK_WAVES == 0, "whole loads");
 };
 
+// Issue this wave's part of tile `tile`; returns which of its 64 keys exist.
 template <bool KV8, int DP>
 __device__ __forceinline__ uint64_t chk_issue(const AttnArgs& a, const char* kb, const char* vb, const int* pages,
-                                              int first, int tile, int lo, int hi, MPDT_LDS char* dst) {
+                                              int first, int tile, int lo, int hi, MPDT_LDS char* dst, int wave) {
     using D = Chk<KV8, DP>;
     using R = typename D::R;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
     int64_t off;
     const bool ok = key_offset(a.kv, pages, first, tile * CHK_KEYS + lane, lo, hi, off);
     const uint64_t mask = __ballot(ok);
@@ -783,38 +797,27 @@ __device__ __forceinline__ uint64_t chk_issue(const AttnArgs& a, const char* kb,
     }
     const int row_bytes = a.kv.dim * (KV8 ? 1 : 2);
 #pragma unroll
-    for (int i = 0; i < D::PER; ++i) {
-        const int ii = wave * D::PER + i;
-        const int c = ii * 64 + lane, r = c / R::CH, pos = c % R::CH;
-        const int64_t o = shfl64(off, r);
-        int ck = (pos ^ R::swz_k(r)) * 16, cv = (pos ^ R::swz_v(r)) * 16;
-        if (ck >= row_bytes) ck = 0;
-        if (cv >= row_bytes) cv = 0;
-        global_to_lds16(kb + o + ck, dst + ii * 1024);
-        global_to_lds16(vb + o + cv, dst + D::HALF + ii * 1024);
+    for (int i = 0; i < D::LOADS; ++i) {
+        const int ii = wave * D::LOADS + i;            // K's pieces, then V's
+        const bool is_v = ii >= R::CH;
+        const int c = (is_v ? ii - R::CH : ii) * 64 + lane, r = c / R::CH, pos = c % R::CH;
+        int from = (pos ^ (is_v ? R::swz_v(r) : R::swz_k(r))) * 16;
+        if (from >= row_bytes) from = 0;
+        global_to_lds16((is_v ? vb : kb) + shfl64(off, r) + from, dst + ii * 1024);
     }
     return mask;
 }
 
-template <class E, class EP, bool KV8, int DP, bool CAP>
-__device__ __forceinline__ void chk_tile(const MPDT_LDS char* st, const u32x4 (&qf)[CHK_QS][DP / 16],
-                                         const Score& sc, uint64_t mask, bool edge, int key0,
-                                         const int (&qpos)[CHK_QS], const int (&qlow)[CHK_QS], float (&ref)[CHK_QS],
-                                         float (&sum)[CHK_QS], f32x16 (&o)[CHK_QS][(DP + 31) / 32]) {
-    using D = Chk<KV8, DP>;
-    using R = typename D::R;
+// S^T of a tile: 64 keys by this wave's 32 rows.
+template <class E, bool KV8, int DP>
+__device__ __forceinline__ void chk_scores(const MPDT_LDS char* st, const u32x4 (&qf)[DP / 16], f32x16 (&s)[2]) {
+    using R = typename Chk<KV8, DP>::R;
     const int lane = threadIdx.x & 63, n = lane & 31, h = lane >> 5;
-    constexpr int DT = (DP + 31) / 32;
-    f32x16 s[CHK_QS][2];
-#pragma unroll
-    for (int q = 0; q < CHK_QS; ++q)
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s[q][ks][i] = 0.0f;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
         const int r = 32 * ks + n;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[ks][i] = 0.0f;
 #pragma unroll
         for (int d = 0; d < DP / 16; ++d) {
             u32x4 kf;
@@ -823,58 +826,79 @@ __device__ __forceinline__ void chk_tile(const MPDT_LDS char* st, const u32x4 (&
             } else {
                 kf = lds_load16(st, r * R::BYTES + ((2 * d + h) ^ R::swz_k(r)) * 16);
             }
-#pragma unroll
-            for (int q = 0; q < CHK_QS; ++q) s[q][ks] = E::mma32(kf, qf[q][d], s[q][ks]);
+            s[ks] = E::mma32(kf, qf[d], s[ks]);
         }
     }
-    u32x4 p[CHK_QS][4];
+}
+
+// Weights of a tile from its scores, with the running maximum and sum.
+template <class EP, int DP, bool CAP>
+__device__ __forceinline__ void chk_weights(f32x16 (&s)[2], const Score& sc, uint64_t mask, bool edge, int key0,
+                                            int qpos, int qlow, float& ref, float& sum,
+                                            f32x16 (&o)[(DP + 31) / 32], u32x4 (&p)[4]) {
+    const int h = (threadIdx.x & 63) >> 5;
+    if constexpr (CAP) {
 #pragma unroll
-    for (int q = 0; q < CHK_QS; ++q) {
-        float m = NO_MAX;
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[ks][i] = score<true>(sc, s[ks][i]);
+    }
+    if (edge) {
+        // the keys of this half of the wave that the row sees, in the order of
+        // its registers
+        const uint64_t seen = (mask & from_to(qlow + 1 - key0, qpos - key0)) >> (4 * h);
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                float x = score<CAP>(sc, s[q][ks][i]);
-                if (edge) {
-                    const int j = 32 * ks + 8 * (i >> 2) + 4 * h + (i & 3);
-                    const bool see = ((mask >> j) & 1) && key0 + j <= qpos[q] && key0 + j > qlow[q];
-                    if (!see) x = -__builtin_inff();
-                }
-                s[q][ks][i] = x;
-                m = fmaxf(m, x);
+                const uint32_t w = (uint32_t)(seen >> (32 * ks));
+                s[ks][i] = w & (1u << (8 * (i >> 2) + (i & 3))) ? s[ks][i] : -__builtin_inff();
             }
-        m = fmaxf(m, __shfl_xor(m, 32)) - EP::P_SHIFT;
-        if (__ballot(m > ref[q] + RESCALE)) {
-            const float to = fmaxf(m, ref[q]), f = __builtin_amdgcn_exp2f(ref[q] - to);
-            ref[q] = to;
-            sum[q] *= f;
-#pragma unroll
-            for (int t = 0; t < DT; ++t)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[q][t][i] *= f;
-        }
-        float add = 0.0f;
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                s[q][ks][i] = __builtin_amdgcn_exp2f(s[q][ks][i] - ref[q]);
-                add += s[q][ks][i];
-            }
-        sum[q] += add;
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                p[q][kk][i] = EP::pack(s[q][kk >> 1][8 * (kk & 1) + 2 * i], s[q][kk >> 1][8 * (kk & 1) + 2 * i + 1]);
     }
+    const float mul = CAP ? 1.0f : sc.mul;       // positive
+    float m = s[0][0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) m = fmaxf(m, s[0][i]);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = fmaxf(m, s[1][i]);
+    m = fmaxf(m, __shfl_xor(m, 32)) * mul - EP::P_SHIFT;
+    if (__ballot(m > ref + RESCALE)) {
+        const float to = fmaxf(m, ref), f = __builtin_amdgcn_exp2f(ref - to);
+        ref = to;
+        sum *= f;
+#pragma unroll
+        for (int t = 0; t < (DP + 31) / 32; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[t][i] *= f;
+    }
+    float add = 0.0f;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            s[ks][i] = __builtin_amdgcn_exp2f(fmaf(s[ks][i], mul, -ref));
+            add += s[ks][i];
+        }
+    sum += add;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            p[kk][i] = EP::pack(s[kk >> 1][8 * (kk & 1) + 2 * i], s[kk >> 1][8 * (kk & 1) + 2 * i + 1]);
+}
+
+// O^T += V^T P^T of a tile.
+template <class EP, bool KV8, int DP>
+__device__ __forceinline__ void chk_values(const MPDT_LDS char* st, const u32x4 (&p)[4],
+                                           f32x16 (&o)[(DP + 31) / 32]) {
+    using D = Chk<KV8, DP>;
+    using R = typename D::R;
+    const int lane = threadIdx.x & 63, h = lane >> 5, l16 = lane & 15, sub = (lane >> 4) & 1;
     const MPDT_LDS char* sv = st + D::HALF;
-    const int l16 = lane & 15, sub = (lane >> 4) & 1;
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
 #pragma unroll
-        for (int t = 0; t < DT; ++t) {
+        for (int t = 0; t < (DP + 31) / 32; ++t) {
             u32x4 vf;
             if constexpr (KV8) {
                 const int k = l16 >> 1, r = 16 * kk + 4 * h + (k < 4 ? k : k + 4);
@@ -885,21 +909,21 @@ __device__ __forceinline__ void chk_tile(const MPDT_LDS char* st, const u32x4 (&
                 const u32x2 v1 = lds_read_tr16(sv, (r + 8) * R::BYTES + (c ^ R::swz_v(r + 8)) * 16 + b);
                 vf = u32x4{v0[0], v0[1], v1[0], v1[1]};
             }
-#pragma unroll
-            for (int q = 0; q < CHK_QS; ++q) o[q][t] = EP::mma32(vf, p[q][kk], o[q][t]);
+            o[t] = EP::mma32(vf, p[kk], o[t]);
         }
     }
 }
 
 template <class E, class EP, bool KV8, int DP, bool CAP>
-__global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(1, 1))) void attn_chunk_kernel(
+__global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(2, 2))) void attn_chunk_kernel(
     AttnArgs a) {
     using D = Chk<KV8, DP>;
-    constexpr int DT = (DP + 31) / 32;
-    __shared__ __attribute__((aligned(1024))) char smem[CHK_NST * D::STAGE];
+    constexpr int DT = (DP + 31) / 32, NST = D::NST;
+    __shared__ __attribute__((aligned(1024))) char smem[NST * D::STAGE];
     __shared__ int pages[PAGES_LDS];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 31, half = lane >> 5;
+    const bool second = wave >= CHK_WAVES / 2;     // waves w and w + 4 share a SIMD
     MPDT_LDS char* lds = lds_cast(smem);
     Plan p;
     plan_layout(a.ws, a.entries, a.sv.seqs, a.workers, a.tile_rows, DP, &p);
@@ -932,79 +956,112 @@ __global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(
         const Span32 kr = keys_of(s, a.group, a.window, r0, r1);
         const int past = s.n - s.nq;
         // this wave's rows: [w0, w1)
-        const int w0 = r0 + wave * 32 * CHK_QS, w1 = min(w0 + 32 * CHK_QS, r1);
+        const int w0 = r0 + wave * 32, w1 = min(w0 + 32, r1);
         const bool busy = w0 < w1;
         const int w_hi = busy ? past + (w1 - 1) / a.group : -1;          // last key that any of them sees
         const int all_hi = busy ? past + w0 / a.group + 1 : 0;           // every one sees keys below
         const int all_lo = a.window > 0 && busy ? past + (w1 - 1) / a.group - a.window + 1 : 0;
         const int w_lo = a.window > 0 && busy ? past + w0 / a.group - a.window + 1 : 0;
-        int qpos[CHK_QS], qlow[CHK_QS];
-        u32x4 qf[CHK_QS][DP / 16];
-        float ref[CHK_QS], sum[CHK_QS];
-        f32x16 o[CHK_QS][DT];
-#pragma unroll
-        for (int q = 0; q < CHK_QS; ++q) {
-            const int row = w0 + 32 * q + n, tok = row / a.group, qh = h * a.group + row % a.group;
-            qpos[q] = past + tok;
-            qlow[q] = a.window > 0 ? qpos[q] - a.window : -1;
-            ref[q] = NO_MAX;
-            sum[q] = 0.0f;
-#pragma unroll
-            for (int d = 0; d < DP / 16; ++d) {
-                const int c = 16 * d + 8 * half;
-                qf[q][d] = u32x4{0, 0, 0, 0};
-                if (row < r1 && c < a.kv.dim)
-                    qf[q][d] = *reinterpret_cast<const u32x4*>(a.q + (int64_t)(s.start + tok) * a.q_tok_b +
-                                                               qh * a.q_head_b + 2 * c);
-            }
-#pragma unroll
-            for (int t = 0; t < DT; ++t)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[q][t][i] = 0.0f;
+        const int row = w0 + n, tok = row / a.group, qh = h * a.group + row % a.group;
+        const int qpos = past + tok, qlow = a.window > 0 ? qpos - a.window : -1;
+        Score sc = score_of(a, KV8 ? a.kv.k_scale[h] : 1.0f);
+        // the largest score is the factor times the largest product where the
+        // factor is positive: a negative one goes to q's signs, a zero to q
+        uint32_t keep = 0xffffffffu, flip = 0;
+        if constexpr (!CAP) {
+            if (sc.mul < 0.0f) flip = 0x80008000u;
+            if (sc.mul == 0.0f) keep = 0;
+            sc.mul = sc.mul == 0.0f ? 1.0f : fabsf(sc.mul);
         }
-        const Score sc = score_of(a, KV8 ? a.kv.k_scale[h] : 1.0f);
+        u32x4 qf[DP / 16];
+#pragma unroll
+        for (int d = 0; d < DP / 16; ++d) {
+            const int c = 16 * d + 8 * half;
+            qf[d] = u32x4{0, 0, 0, 0};
+            if (row < r1 && c < a.kv.dim)
+                qf[d] = *reinterpret_cast<const u32x4*>(a.q + (int64_t)(s.start + tok) * a.q_tok_b +
+                                                        qh * a.q_head_b + 2 * c);
+            qf[d] = (qf[d] & keep) ^ flip;
+        }
+        float ref = NO_MAX, sum = 0.0f;
+        f32x16 o[DT], sc_tile[2];
+        u32x4 pw[4];
+#pragma unroll
+        for (int t = 0; t < DT; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[t][i] = 0.0f;
         const char* kb = a.kv.k + h * a.kv.head_b;
         const char* vb = a.kv.v + h * a.kv.head_b;
 
         for (int pos = seg_a; pos < seg_e;) {
             int first;
             const int upto = fetch_pages<64 * CHK_WAVES, CHK_KEYS>(a, b, t0 + pos, t0 + seg_e, pages, first) - t0;
-            uint64_t m0 = 0, m1 = 0, m2 = 0;
-            m0 = chk_issue<KV8, DP>(a, kb, vb, pages, first, t0 + pos, kr.lo, kr.hi, lds);
-            if (pos + 1 < upto)
-                m1 = chk_issue<KV8, DP>(a, kb, vb, pages, first, t0 + pos + 1, kr.lo, kr.hi, lds + D::STAGE);
+            uint64_t mask[NST];      // of the tiles j, j + 1, ...
+#pragma unroll
+            for (int i = 0; i < NST; ++i) mask[i] = 0;
+#pragma unroll
+            for (int i = 0; i < NST - 1; ++i)
+                if (pos + i < upto)
+                    mask[i] = chk_issue<KV8, DP>(a, kb, vb, pages, first, t0 + pos + i, kr.lo, kr.hi,
+                                                 lds + i * D::STAGE, wave);
+            // whether this wave has to do with a tile
+            auto act = [&](uint64_t m, int j) {
+                const int k0 = (t0 + j) * CHK_KEYS;
+                return m != 0 && busy && k0 <= w_hi && k0 + CHK_KEYS > w_lo;
+            };
+            if (pos + NST - 2 < upto) wait_vmem<(NST - 2) * D::LOADS>();
+            else wait_vmem<0>();
+            wg_barrier();
+            if (act(mask[0], pos)) chk_scores<E, KV8, DP>(lds, qf, sc_tile);
+            // From here on the first four waves run one phase ahead.  A tile j
+            // has landed for all before a first wave's MFMAs of tile j - 1, and
+            // its stage is free after a second wave's MFMAs of tile j.
+            if (second) {
+                if (pos + NST - 2 < upto) wait_vmem<(NST - 3) * D::LOADS>();
+                else wait_vmem<0>();
+                wg_barrier();
+            }
             int slot = 0;
             for (int j = pos; j < upto; ++j) {
-                if (j + 1 < upto) wait_vmem<D::LOADS>();
-                else wait_vmem<0>();
+                const bool now = act(mask[0], j);
+                const int next = slot + 1 == NST ? 0 : slot + 1, fill = slot == 0 ? NST - 1 : slot - 1;
+                const int ahead = j + NST - 1;
+                if (second && ahead < upto)
+                    mask[NST - 1] = chk_issue<KV8, DP>(a, kb, vb, pages, first, t0 + ahead, kr.lo, kr.hi,
+                                                       lds + fill * D::STAGE, wave);
+                if (now) {
+                    const int key0 = (t0 + j) * CHK_KEYS;
+                    const bool edge = ~mask[0] || key0 + CHK_KEYS > all_hi || key0 < all_lo;
+                    chk_weights<EP, DP, CAP>(sc_tile, sc, mask[0], edge, key0, qpos, qlow, ref, sum, o, pw);
+                }
+                if (!second) {
+                    if (ahead - 1 < upto) wait_vmem<(NST - 3) * D::LOADS>();
+                    else wait_vmem<0>();
+                }
+                wg_barrier();
+                if (!second && ahead < upto)
+                    mask[NST - 1] = chk_issue<KV8, DP>(a, kb, vb, pages, first, t0 + ahead, kr.lo, kr.hi,
+                                                       lds + fill * D::STAGE, wave);
+                if (now) chk_values<EP, KV8, DP>(lds + slot * D::STAGE, pw, o);
+                if (j + 1 < upto && act(mask[1], j + 1))
+                    chk_scores<E, KV8, DP>(lds + next * D::STAGE, qf, sc_tile);
+                if (second) {
+                    if (ahead < upto) wait_vmem<(NST - 3) * D::LOADS>();
+                    else wait_vmem<0>();
+                }
                 wait_lds();
-                wg_barrier();    // tile j has landed for all waves, and all are done with tile j - 1
-                if (j + 2 < upto) {
-                    const int fill = slot == 0 ? 2 : slot - 1;
-                    m2 = chk_issue<KV8, DP>(a, kb, vb, pages, first, t0 + j + 2, kr.lo, kr.hi,
-                                            lds + fill * D::STAGE);
-                }
-                const int key0 = (t0 + j) * CHK_KEYS;
-                if (m0 && busy && key0 <= w_hi && key0 + CHK_KEYS > w_lo) {
-                    const bool edge = ~m0 || key0 + CHK_KEYS > all_hi || key0 < all_lo;
-                    chk_tile<E, EP, KV8, DP, CAP>(lds + slot * D::STAGE, qf, sc, m0, edge, key0, qpos, qlow, ref, sum,
-                                                  o);
-                }
-                m0 = m1;
-                m1 = m2;
-                slot = slot == 2 ? 0 : slot + 1;
+                wg_barrier();
+#pragma unroll
+                for (int i = 0; i + 1 < NST; ++i) mask[i] = mask[i + 1];
+                slot = next;
             }
+            if (!second) wg_barrier();
             pos = upto;
-            wait_lds();
-            wg_barrier();    // page numbers and stages are free again
+            __syncthreads();     // page numbers and stages are free again
         }
 
-#pragma unroll
-        for (int q = 0; q < CHK_QS; ++q) {
-            const float den = sum[q] + __shfl_xor(sum[q], 32);
-            const int in_tile = wave * 32 * CHK_QS + 32 * q + n, row = r0 + in_tile;
-            const int tok = row / a.group, qh = h * a.group + row % a.group;
-            if (row >= r1) continue;
+        const float den = sum + __shfl_xor(sum, 32);
+        if (row < r1) {
             if (whole) {
                 const float inv = (den > 0.0f || den != den ? 1.0f / den : 0.0f) * (KV8 ? a.kv.v_scale[h] : 1.0f);
                 char* orow = a.out + (int64_t)(s.start + tok) * a.o_tok_b + qh * a.o_head_b;
@@ -1014,19 +1071,19 @@ __global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(
                     for (int i = 0; i < 4; ++i) {
                         const int d = 32 * t + 8 * i + 4 * half;
                         if (d < a.kv.dim)
-                            store_out4(a, orow, d, f32x4{o[q][t][4 * i], o[q][t][4 * i + 1], o[q][t][4 * i + 2],
-                                                         o[q][t][4 * i + 3]} * inv);
+                            store_out4(a, orow, d, f32x4{o[t][4 * i], o[t][4 * i + 1], o[t][4 * i + 2],
+                                                         o[t][4 * i + 3]} * inv);
                     }
-                if (half == 0 && a.lse) a.lse[(int64_t)(s.start + tok) * a.lse_tok + qh] = lse_of(ref[q], den);
+                if (half == 0 && a.lse) a.lse[(int64_t)(s.start + tok) * a.lse_tok + qh] = lse_of(ref, den);
             } else {
-                const int64_t sr = ((int64_t)worker * 2 + (lead ? 0 : 1)) * CHK_ROWS + in_tile;
+                const int64_t sr = ((int64_t)worker * 2 + (lead ? 0 : 1)) * CHK_ROWS + wave * 32 + n;
 #pragma unroll
                 for (int t = 0; t < DT; ++t)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         *reinterpret_cast<f32x4*>(p.part_o + sr * DP + 32 * t + 8 * i + 4 * half) =
-                            f32x4{o[q][t][4 * i], o[q][t][4 * i + 1], o[q][t][4 * i + 2], o[q][t][4 * i + 3]};
-                if (half == 0) p.part_ml[sr] = f32x2{ref[q], den};
+                            f32x4{o[t][4 * i], o[t][4 * i + 1], o[t][4 * i + 2], o[t][4 * i + 3]};
+                if (half == 0) p.part_ml[sr] = f32x2{ref, den};
             }
         }
         at += seg_e - seg_a;
