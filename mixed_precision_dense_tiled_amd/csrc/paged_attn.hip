@@ -116,25 +116,38 @@ __device__ __forceinline__ u32x4 widen8(u32x2 w) {
 // ---- the staged rows of K and V in LDS ---------------------------------------
 //
 // A row is CH chunks of 16 bytes (DP elements, padded to 8 chunks for 96 FP8
-// values); chunk c of row r lies at place c ^ swz(r), so that the reads below
-// touch every bank once.  MF: rows of an MFMA tile (16 or 32), which decides
-// the set of rows that one transposing read of V names.
+// values); chunk c of row r lies at place c ^ swz(r).  LDS has 64 banks of 4
+// bytes: 16 places.  A cycle serves 16 lanes of a 16-byte read of K (16 rows,
+// one chunk) and 32 lanes of an 8-byte transposing read of V (4 or 8 rows, 64
+// or 32 bytes side by side; 16 rows of 16 bytes of FP8 at MF = 16), and the
+// swizzles below spread each of these sets over all 16 places.  MF: rows of an
+// MFMA tile (16 or 32), which decides the rows that a read of V names.
 template <int DP, bool KV8, int MF>
 struct Rows {
     static constexpr int CH = KV8 ? (DP <= 64 ? 4 : 8) : DP / 8;
     static constexpr int BYTES = CH * 16;
     static __device__ __forceinline__ int swz_k(int r) {
-        if constexpr (CH == 16 || CH == 8) return r & 7;
-        return (r >> 1) & 3;
+        if constexpr (CH == 16) return r & 15;
+        if constexpr (CH == 8) return (r >> 1) & 7;
+        return (r >> 2) & 3;                              // 12 (rows start at 4 places in turn), 4
     }
     static __device__ __forceinline__ int swz_v(int r) {
-        const int far = MF == 16 ? (r >> 4) & 1 : (r >> 3) & 1;   // the upper four of a transposing read's rows
-        if constexpr (KV8) {
-            if constexpr (CH == 8) return (r & 3) | (far << 2);
-            return ((r >> 1) & 1) | (far << 1);
+        if constexpr (KV8 && MF == 32) {                  // rows 0..3 and 8..11
+            if constexpr (CH == 8) return ((r >> 1) & 1) << 1 | ((r >> 3) & 1) << 2;
+            return ((r >> 3) & 1) << 1;
         }
-        if constexpr (CH == 12) return ((r >> 1) & 1) << 1;
-        return (r & 3) << 1;
+        if constexpr (KV8) {                              // rows 0..7 and 16..23
+            if constexpr (CH == 8) return ((r >> 1) & 3) | ((r >> 4) & 1) << 2;
+            return ((r >> 2) & 1) | ((r >> 4) & 1) << 1;
+        }
+        if constexpr (MF == 32) {                         // rows 0..3, 64 bytes
+            if constexpr (CH == 16) return (r & 3) << 2;
+            if constexpr (CH == 8) return ((r >> 1) & 1) << 2;
+            return 0;
+        }
+        if constexpr (CH == 16) return (r & 7) << 1;      // rows 0..7, 32 bytes
+        if constexpr (CH == 8) return ((r >> 1) & 3) << 1;
+        return ((r >> 2) & 1) << 1;
     }
 };
 
@@ -818,15 +831,17 @@ __device__ __forceinline__ void chk_scores(const MPDT_LDS char* st, const u32x4 
         const int r = 32 * ks + n;
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[ks][i] = 0.0f;
+        if constexpr (KV8) {
 #pragma unroll
-        for (int d = 0; d < DP / 16; ++d) {
-            u32x4 kf;
-            if constexpr (KV8) {
-                kf = widen8<E>(lds_load8(st, r * R::BYTES + (d ^ R::swz_k(r)) * 16 + h * 8));
-            } else {
-                kf = lds_load16(st, r * R::BYTES + ((2 * d + h) ^ R::swz_k(r)) * 16);
+            for (int d = 0; d < DP / 32; ++d) {        // 16 bytes: two steps
+                const u32x4 w = lds_load16(st, r * R::BYTES + ((2 * d + h) ^ R::swz_k(r)) * 16);
+                s[ks] = E::mma32(widen8<E>(u32x2{w[0], w[1]}), qf[2 * d], s[ks]);
+                s[ks] = E::mma32(widen8<E>(u32x2{w[2], w[3]}), qf[2 * d + 1], s[ks]);
             }
-            s[ks] = E::mma32(kf, qf[d], s[ks]);
+        } else {
+#pragma unroll
+            for (int d = 0; d < DP / 16; ++d)
+                s[ks] = E::mma32(lds_load16(st, r * R::BYTES + ((2 * d + h) ^ R::swz_k(r)) * 16), qf[d], s[ks]);
         }
     }
 }
@@ -976,7 +991,8 @@ __global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(
         u32x4 qf[DP / 16];
 #pragma unroll
         for (int d = 0; d < DP / 16; ++d) {
-            const int c = 16 * d + 8 * half;
+            // (an FP8 key's 16 bytes are two steps of its half of the wave)
+            const int c = KV8 ? 32 * (d / 2) + 16 * half + 8 * (d % 2) : 16 * d + 8 * half;
             qf[d] = u32x4{0, 0, 0, 0};
             if (row < r1 && c < a.kv.dim)
                 qf[d] = *reinterpret_cast<const u32x4*>(a.q + (int64_t)(s.start + tok) * a.q_tok_b +
