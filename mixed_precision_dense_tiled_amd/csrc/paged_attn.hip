@@ -163,6 +163,14 @@ __device__ __forceinline__ u32x2 lds_load8(const MPDT_LDS char* base, uint32_t o
     return *reinterpret_cast<const MPDT_LDS u32x2*>(base + off);
 }
 
+// A value that every lane of the wave has, told to the compiler: numbers read
+// from memory would otherwise live in vector registers, and all that depends
+// on them.
+__device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ float uni(float x) {
+    return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(x)));
+}
+
 // ---- sequences, units and the plan --------------------------------------------
 
 struct Seq {
@@ -178,6 +186,12 @@ __device__ __forceinline__ Seq seq_of(const SeqView& v, int64_t page_size, int b
     const int64_t most = page_size * v.width;
     s.n = (int)min((int64_t)max(v.lens[b], 0), most);
     return s;
+}
+
+// The same for a sequence that the whole wave works on.
+__device__ __forceinline__ Seq uniform_seq(const SeqView& v, int64_t page_size, int b) {
+    const Seq s = seq_of(v, page_size, b);
+    return Seq{uni(s.start), uni(s.nq), uni(s.n)};
 }
 
 // Keys [lo, hi) that any of the rows [r0, r1) of a sequence sees.
@@ -201,6 +215,7 @@ struct Plan {
     i32x4* entry;
     int32_t* before;
     int32_t* first;     // row tiles before a sequence
+    char* zeros;        // 16 bytes
     float* part_o;      // partial outputs, two slots to a worker
     f32x2* part_ml;     // their reference and sum
 };
@@ -211,6 +226,7 @@ __host__ __device__ inline int64_t plan_layout(char* ws, int entries, int seqs, 
                                                int dp, Plan* p) {
     int64_t at = 0;
     p->head = (int32_t*)(ws + at);
+    p->zeros = ws + 128;
     at += 256;
     p->entry = (i32x4*)(ws + at);
     at += up256((int64_t)entries * 16);
@@ -268,6 +284,7 @@ __global__ __launch_bounds__(1024) void attn_plan_kernel(AttnArgs a, int key_til
     }
     const int entries = min(run, a.entries);
     if (threadIdx.x == 0) p.first[a.sv.seqs] = run;
+    if (threadIdx.x < 4) reinterpret_cast<int32_t*>(p.zeros)[threadIdx.x] = 0;
     __syncthreads();
     int tiles = 0;
     for (int e0 = 0; e0 < entries; e0 += 1024) {
@@ -546,20 +563,20 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void attn_decode_kernel(AttnArgs a)
 
     Plan p;
     int64_t at = 0, stop = 0, share = 1;
-    int worker = 0, line = 0, e = 0, h = 0;
+    int worker = 0, line = 0, entries = 0, e = 0, h = 0;
     int b, r0, t0, tiles;
     if constexpr (DIRECT) {
         find_entry<DEC_WAVES>(a, blockIdx.x, red, box);
-        b = box[0];
-        r0 = box[1];
+        b = uni(box[0]);
+        r0 = uni(box[1]);
         h = blockIdx.y;
         if (b < 0) return;
         at = 0;
         stop = 1;
     } else {
         plan_layout(a.ws, a.entries, a.sv.seqs, a.workers, a.tile_rows, DP, &p);
-        line = p.head[1];
-        const int entries = p.head[0];
+        line = uni(p.head[1]);
+        entries = uni(p.head[0]);
         const int64_t total = (int64_t)line * a.kv.kv_heads;
         share = share_of(a, total);
         worker = worker_id();
@@ -571,7 +588,7 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void attn_decode_kernel(AttnArgs a)
         int lo = 0, hi = entries;
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
-            if (p.before[mid] <= rem) lo = mid;
+            if (uni(p.before[mid]) <= rem) lo = mid;
             else hi = mid;
         }
         e = lo;
@@ -582,16 +599,16 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void attn_decode_kernel(AttnArgs a)
         bool whole = true;
         if constexpr (!DIRECT) {
             const i32x4 ent = p.entry[e];
-            b = ent[0];
-            r0 = ent[1];
-            t0 = ent[2];
-            tiles = ent[3];
-            const int64_t u0 = (int64_t)h * line + p.before[e];
+            b = uni(ent[0]);
+            r0 = uni(ent[1]);
+            t0 = uni(ent[2]);
+            tiles = uni(ent[3]);
+            const int64_t u0 = (int64_t)h * line + uni(p.before[e]);
             seg_a = (int)(at - u0);
             seg_e = (int)min((int64_t)tiles, stop - u0);
             whole = seg_a == 0 && seg_e == tiles;
         }
-        const Seq s = seq_of(a.sv, a.kv.page_size, b);
+        const Seq s = uniform_seq(a.sv, a.kv.page_size, b);
         const int rows = s.nq * a.group, r1 = min(r0 + DEC_ROWS, rows);
         const Span32 kr = keys_of(s, a.group, a.window, r0, r1);
         if constexpr (DIRECT) {
@@ -613,7 +630,7 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void attn_decode_kernel(AttnArgs a)
                 qf[d] = *reinterpret_cast<const u32x4*>(a.q + (int64_t)(s.start + tok) * a.q_tok_b +
                                                         qh * a.q_head_b + 2 * c);
         }
-        const Score sc = score_of(a, KV8 ? a.kv.k_scale[h] : 1.0f);
+        const Score sc = score_of(a, KV8 ? uni(a.kv.k_scale[h]) : 1.0f);
         const char* kb = a.kv.k + h * a.kv.head_b;
         const char* vb = a.kv.v + h * a.kv.head_b;
         // rows of this tile see every key below `all_hi` and from `all_lo` on
@@ -721,7 +738,7 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void attn_decode_kernel(AttnArgs a)
         if constexpr (DIRECT) return;
         at += seg_e - seg_a;
         lead = false;
-        if (++e == p.head[0]) {
+        if (++e == entries) {
             e = 0;
             ++h;
         }
@@ -795,19 +812,23 @@ struct Chk {
 };
 
 // Issue this wave's part of tile `tile`; returns which of its 64 keys exist.
+// Keys that do not exist are staged as zeros (from the workspace), so that a
+// weight of zero times their value is zero.
 template <bool KV8, int DP>
-__device__ __forceinline__ uint64_t chk_issue(const AttnArgs& a, const char* kb, const char* vb, const int* pages,
-                                              int first, int tile, int lo, int hi, MPDT_LDS char* dst, int wave) {
+__device__ __forceinline__ uint64_t chk_issue(const AttnArgs& a, const char* kb, const char* vb, const char* zeros,
+                                              const int* pages, int first, int tile, int lo, int hi,
+                                              MPDT_LDS char* dst, int wave) {
     using D = Chk<KV8, DP>;
     using R = typename D::R;
-    const int lane = threadIdx.x & 63;
+    // (opaque, so that what follows from it is worked out anew for each tile:
+    // kept in registers across the loop it would push others into scratch,
+    // whose loads wait for all loads in flight)
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
     int64_t off;
     const bool ok = key_offset(a.kv, pages, first, tile * CHK_KEYS + lane, lo, hi, off);
     const uint64_t mask = __ballot(ok);
-    if (~mask) {
-        const int64_t other = shfl64(off, mask ? __builtin_ctzll(mask) : 0);
-        if (!ok) off = other;
-    }
+    if (!ok) off = -1;
     const int row_bytes = a.kv.dim * (KV8 ? 1 : 2);
 #pragma unroll
     for (int i = 0; i < D::LOADS; ++i) {
@@ -816,34 +837,10 @@ __device__ __forceinline__ uint64_t chk_issue(const AttnArgs& a, const char* kb,
         const int c = (is_v ? ii - R::CH : ii) * 64 + lane, r = c / R::CH, pos = c % R::CH;
         int from = (pos ^ (is_v ? R::swz_v(r) : R::swz_k(r))) * 16;
         if (from >= row_bytes) from = 0;
-        global_to_lds16((is_v ? vb : kb) + shfl64(off, r) + from, dst + ii * 1024);
+        const int64_t o = shfl64(off, r);
+        global_to_lds16(o >= 0 ? (is_v ? vb : kb) + o + from : zeros, dst + ii * 1024);
     }
     return mask;
-}
-
-// S^T of a tile: 64 keys by this wave's 32 rows.
-template <class E, bool KV8, int DP>
-__device__ __forceinline__ void chk_scores(const MPDT_LDS char* st, const u32x4 (&qf)[DP / 16], f32x16 (&s)[2]) {
-    using R = typename Chk<KV8, DP>::R;
-    const int lane = threadIdx.x & 63, n = lane & 31, h = lane >> 5;
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-        const int r = 32 * ks + n;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[ks][i] = 0.0f;
-        if constexpr (KV8) {
-#pragma unroll
-            for (int d = 0; d < DP / 32; ++d) {        // 16 bytes: two steps
-                const u32x4 w = lds_load16(st, r * R::BYTES + ((2 * d + h) ^ R::swz_k(r)) * 16);
-                s[ks] = E::mma32(widen8<E>(u32x2{w[0], w[1]}), qf[2 * d], s[ks]);
-                s[ks] = E::mma32(widen8<E>(u32x2{w[2], w[3]}), qf[2 * d + 1], s[ks]);
-            }
-        } else {
-#pragma unroll
-            for (int d = 0; d < DP / 16; ++d)
-                s[ks] = E::mma32(lds_load16(st, r * R::BYTES + ((2 * d + h) ^ R::swz_k(r)) * 16), qf[d], s[ks]);
-        }
-    }
 }
 
 // Weights of a tile from its scores, with the running maximum and sum.
@@ -902,32 +899,122 @@ __device__ __forceinline__ void chk_weights(f32x16 (&s)[2], const Score& sc, uin
             p[kk][i] = EP::pack(s[kk >> 1][8 * (kk & 1) + 2 * i], s[kk >> 1][8 * (kk & 1) + 2 * i + 1]);
 }
 
-// O^T += V^T P^T of a tile.
-template <class EP, bool KV8, int DP>
-__device__ __forceinline__ void chk_values(const MPDT_LDS char* st, const u32x4 (&p)[4],
-                                           f32x16 (&o)[(DP + 31) / 32]) {
+// The MFMAs of a phase: O^T += V^T P^T of one tile (DO_V) and S^T = K Q^T of
+// the next (DO_K), in groups of four or so whose operands are read from LDS
+// two groups ahead.  (Left to itself the compiler reads each operand right
+// before its MFMA and waits out the LDS latency 32 times a tile.)
+template <class E, class EP, bool KV8, int DP>
+struct ChkMma {
     using D = Chk<KV8, DP>;
     using R = typename D::R;
-    const int lane = threadIdx.x & 63, h = lane >> 5, l16 = lane & 15, sub = (lane >> 4) & 1;
-    const MPDT_LDS char* sv = st + D::HALF;
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-#pragma unroll
-        for (int t = 0; t < (DP + 31) / 32; ++t) {
-            u32x4 vf;
-            if constexpr (KV8) {
-                const int k = l16 >> 1, r = 16 * kk + 4 * h + (k < 4 ? k : k + 4);
-                vf = widen8<EP>(lds_read_tr8(sv, r * R::BYTES + ((2 * t + sub) ^ R::swz_v(r)) * 16 + (l16 & 1) * 8));
-            } else {
-                const int r = 16 * kk + 4 * h + (l16 >> 2), c = 4 * t + 2 * sub + ((l16 & 3) >> 1), b = (l16 & 1) * 8;
-                const u32x2 v0 = lds_read_tr16(sv, r * R::BYTES + (c ^ R::swz_v(r)) * 16 + b);
-                const u32x2 v1 = lds_read_tr16(sv, (r + 8) * R::BYTES + (c ^ R::swz_v(r + 8)) * 16 + b);
-                vf = u32x4{v0[0], v0[1], v1[0], v1[1]};
-            }
-            o[t] = EP::mma32(vf, p[kk], o[t]);
+    static constexpr int DT = (DP + 31) / 32, NV = 4, NK = DP / 32, AHEAD = 2, NBUF = AHEAD + 1;
+    struct Frag {
+        u32x4 x[4];
+    };
+    Frag buf[NBUF];
+
+    // Where this lane reads: its byte in the first operand of K and of V.  The
+    // others follow by flipping bits of the chunk (rows of 12 chunks: by adding
+    // four chunks at a time, which their swizzle leaves alone).
+    uint32_t k_at, v_at;
+    __device__ __forceinline__ ChkMma() {
+        const int lane = threadIdx.x & 63, n = lane & 31, h = lane >> 5, l16 = lane & 15, sub = (lane >> 4) & 1;
+        k_at = n * R::BYTES + (h ^ R::swz_k(n)) * 16;
+        if constexpr (KV8) {
+            const int k = l16 >> 1, r = 4 * h + (k < 4 ? k : k + 4);
+            v_at = D::HALF + r * R::BYTES + (sub ^ R::swz_v(r)) * 16 + (l16 & 1) * 8;
+        } else {
+            const int r = 4 * h + (l16 >> 2);
+            v_at = D::HALF + r * R::BYTES + ((2 * sub + ((l16 & 3) >> 1)) ^ R::swz_v(r)) * 16 + (l16 & 1) * 8;
         }
     }
-}
+    // four: groups of four chunks; two: a pair of chunks
+    static __device__ __forceinline__ uint32_t chunk(uint32_t at, int four, int two) {
+        if constexpr (R::CH == 12) return (at ^ (two * 32)) + four * 64;
+        return at ^ (four * 64 + two * 32);
+    }
+
+    // operands of V: keys 16 kk to 16 kk + 15, all of dim
+    __device__ __forceinline__ void load_v(Frag& f, const MPDT_LDS char* st, int kk) {
+#pragma unroll
+        for (int t = 0; t < DT; ++t) {
+            if constexpr (KV8) {
+                const u32x2 w = lds_read_tr8(st, chunk(v_at, t / 2, t % 2) + 16 * kk * R::BYTES);
+                f.x[t][0] = w[0];
+                f.x[t][1] = w[1];
+            } else {
+                const uint32_t at = chunk(v_at, t, 0) + 16 * kk * R::BYTES;
+                const u32x2 v0 = lds_read_tr16(st, at), v1 = lds_read_tr16(st, at + 8 * R::BYTES);
+                f.x[t] = u32x4{v0[0], v0[1], v1[0], v1[1]};
+            }
+        }
+    }
+    static __device__ __forceinline__ void mma_v(const Frag& f, const u32x4& p, f32x16 (&o)[DT]) {
+#pragma unroll
+        for (int t = 0; t < DT; ++t) {
+            if constexpr (KV8) o[t] = EP::mma32(widen8<EP>(u32x2{f.x[t][0], f.x[t][1]}), p, o[t]);
+            else o[t] = EP::mma32(f.x[t], p, o[t]);
+        }
+    }
+    // operands of K: all 64 keys, 32 values of dim
+    __device__ __forceinline__ void load_k(Frag& f, const MPDT_LDS char* st, int d) {
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            if constexpr (KV8) {
+                f.x[ks] = lds_load16(st, chunk(k_at, d / 2, d % 2) + 32 * ks * R::BYTES);
+            } else {
+                f.x[ks] = lds_load16(st, chunk(k_at, d, 0) + 32 * ks * R::BYTES);
+                f.x[2 + ks] = lds_load16(st, chunk(k_at, d, 1) + 32 * ks * R::BYTES);
+            }
+        }
+    }
+    static __device__ __forceinline__ void mma_k(const Frag& f, const u32x4& q0, const u32x4& q1, f32x16 (&s)[2]) {
+        if constexpr (KV8) {
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) s[ks] = E::mma32(widen8<E>(u32x2{f.x[ks][0], f.x[ks][1]}), q0, s[ks]);
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) s[ks] = E::mma32(widen8<E>(u32x2{f.x[ks][2], f.x[ks][3]}), q1, s[ks]);
+        } else {
+            s[0] = E::mma32(f.x[0], q0, s[0]);
+            s[1] = E::mma32(f.x[1], q0, s[1]);
+            s[0] = E::mma32(f.x[2], q1, s[0]);
+            s[1] = E::mma32(f.x[3], q1, s[1]);
+        }
+    }
+
+    template <bool DO_V, int G>
+    __device__ __forceinline__ void load(const MPDT_LDS char* sv, const MPDT_LDS char* sk) {
+        if constexpr (DO_V && G < NV) load_v(buf[G % NBUF], sv, G);
+        else load_k(buf[G % NBUF], sk, DO_V ? G - NV : G);
+    }
+    // the first groups, from the phase before
+    template <bool DO_V, bool DO_K>
+    __device__ __forceinline__ void begin(const MPDT_LDS char* sv, const MPDT_LDS char* sk) {
+        constexpr int NG = (DO_V ? NV : 0) + (DO_K ? NK : 0);
+        static_for<0, AHEAD < NG ? AHEAD : NG>([&](auto g) { load<DO_V, decltype(g)::value>(sv, sk); });
+    }
+    template <bool DO_V, bool DO_K>
+    __device__ __forceinline__ void finish(const MPDT_LDS char* sv, const MPDT_LDS char* sk, const u32x4 (&p)[4],
+                                           const u32x4 (&qf)[DP / 16], f32x16 (&o)[DT], f32x16 (&s)[2]) {
+        constexpr int NG = (DO_V ? NV : 0) + (DO_K ? NK : 0);
+        if constexpr (DO_K) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[0][i] = s[1][i] = 0.0f;
+        }
+        static_for<0, NG>([&](auto gc) {
+            constexpr int g = decltype(gc)::value;
+            if constexpr (g + AHEAD < NG) load<DO_V, g + AHEAD>(sv, sk);
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (DO_V && g < NV) {
+                mma_v(buf[g % NBUF], p[g], o);
+            } else {
+                constexpr int d = DO_V ? g - NV : g;
+                mma_k(buf[g % NBUF], qf[2 * d], qf[2 * d + 1], s);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    }
+};
 
 template <class E, class EP, bool KV8, int DP, bool CAP>
 __global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(2, 2))) void attn_chunk_kernel(
@@ -942,7 +1029,7 @@ __global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(
     MPDT_LDS char* lds = lds_cast(smem);
     Plan p;
     plan_layout(a.ws, a.entries, a.sv.seqs, a.workers, a.tile_rows, DP, &p);
-    const int line = p.head[1], entries = p.head[0];
+    const int line = uni(p.head[1]), entries = uni(p.head[0]);
     const int64_t total = (int64_t)line * a.kv.kv_heads, share = share_of(a, total);
     const int worker = worker_id();
     int64_t at = worker * share;
@@ -954,7 +1041,7 @@ __global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(
         int lo = 0, hi = entries;
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
-            if (p.before[mid] <= rem) lo = mid;
+            if (uni(p.before[mid]) <= rem) lo = mid;
             else hi = mid;
         }
         e = lo;
@@ -962,11 +1049,11 @@ __global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(
     bool lead = true;
     while (at < stop) {
         const i32x4 ent = p.entry[e];
-        const int b = ent[0], r0 = ent[1], t0 = ent[2], tiles = ent[3];
-        const int64_t u0 = (int64_t)h * line + p.before[e];
+        const int b = uni(ent[0]), r0 = uni(ent[1]), t0 = uni(ent[2]), tiles = uni(ent[3]);
+        const int64_t u0 = (int64_t)h * line + uni(p.before[e]);
         const int seg_a = (int)(at - u0), seg_e = (int)min((int64_t)tiles, stop - u0);
         const bool whole = seg_a == 0 && seg_e == tiles;
-        const Seq s = seq_of(a.sv, a.kv.page_size, b);
+        const Seq s = uniform_seq(a.sv, a.kv.page_size, b);
         const int rows = s.nq * a.group, r1 = min(r0 + CHK_ROWS, rows);
         const Span32 kr = keys_of(s, a.group, a.window, r0, r1);
         const int past = s.n - s.nq;
@@ -979,7 +1066,7 @@ __global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(
         const int w_lo = a.window > 0 && busy ? past + w0 / a.group - a.window + 1 : 0;
         const int row = w0 + n, tok = row / a.group, qh = h * a.group + row % a.group;
         const int qpos = past + tok, qlow = a.window > 0 ? qpos - a.window : -1;
-        Score sc = score_of(a, KV8 ? a.kv.k_scale[h] : 1.0f);
+        Score sc = score_of(a, KV8 ? uni(a.kv.k_scale[h]) : 1.0f);
         // the largest score is the factor times the largest product where the
         // factor is positive: a negative one goes to q's signs, a zero to q
         uint32_t keep = 0xffffffffu, flip = 0;
@@ -1002,6 +1089,7 @@ __global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(
         float ref = NO_MAX, sum = 0.0f;
         f32x16 o[DT], sc_tile[2];
         u32x4 pw[4];
+        ChkMma<E, EP, KV8, DP> mma;
 #pragma unroll
         for (int t = 0; t < DT; ++t)
 #pragma unroll
@@ -1012,64 +1100,97 @@ __global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(
         for (int pos = seg_a; pos < seg_e;) {
             int first;
             const int upto = fetch_pages<64 * CHK_WAVES, CHK_KEYS>(a, b, t0 + pos, t0 + seg_e, pages, first) - t0;
-            uint64_t mask[NST];      // of the tiles j, j + 1, ...
+            // tiles [ja, jb) hold keys that this wave's rows see
+            int ja = upto, jb = upto;
+            if (busy && w_hi >= w_lo) {
+                ja = min(max(max(w_lo, 0) / CHK_KEYS - t0, pos), upto);
+                jb = min(max(w_hi < 0 ? pos : w_hi / CHK_KEYS + 1 - t0, ja), upto);
+            }
+            uint64_t mask[NST];      // which keys of the tiles j, j + 1, ... exist
+            auto issue = [&](int j, MPDT_LDS char* dst) {
+                return chk_issue<KV8, DP>(a, kb, vb, p.zeros, pages, first, t0 + j, kr.lo, kr.hi, dst, wave);
+            };
 #pragma unroll
             for (int i = 0; i < NST; ++i) mask[i] = 0;
 #pragma unroll
             for (int i = 0; i < NST - 1; ++i)
-                if (pos + i < upto)
-                    mask[i] = chk_issue<KV8, DP>(a, kb, vb, pages, first, t0 + pos + i, kr.lo, kr.hi,
-                                                 lds + i * D::STAGE, wave);
-            // whether this wave has to do with a tile
-            auto act = [&](uint64_t m, int j) {
-                const int k0 = (t0 + j) * CHK_KEYS;
-                return m != 0 && busy && k0 <= w_hi && k0 + CHK_KEYS > w_lo;
-            };
+                if (pos + i < upto) mask[i] = issue(pos + i, lds + i * D::STAGE);
             if (pos + NST - 2 < upto) wait_vmem<(NST - 2) * D::LOADS>();
             else wait_vmem<0>();
             wg_barrier();
-            if (act(mask[0], pos)) chk_scores<E, KV8, DP>(lds, qf, sc_tile);
+            int j = pos, slot = 0;
             // From here on the first four waves run one phase ahead.  A tile j
             // has landed for all before a first wave's MFMAs of tile j - 1, and
             // its stage is free after a second wave's MFMAs of tile j.
-            if (second) {
-                if (pos + NST - 2 < upto) wait_vmem<(NST - 3) * D::LOADS>();
-                else wait_vmem<0>();
-                wg_barrier();
-            }
-            int slot = 0;
-            for (int j = pos; j < upto; ++j) {
-                const bool now = act(mask[0], j);
-                const int next = slot + 1 == NST ? 0 : slot + 1, fill = slot == 0 ? NST - 1 : slot - 1;
+            auto refill = [&] {
                 const int ahead = j + NST - 1;
-                if (second && ahead < upto)
-                    mask[NST - 1] = chk_issue<KV8, DP>(a, kb, vb, pages, first, t0 + ahead, kr.lo, kr.hi,
-                                                       lds + fill * D::STAGE, wave);
-                if (now) {
-                    const int key0 = (t0 + j) * CHK_KEYS;
-                    const bool edge = ~mask[0] || key0 + CHK_KEYS > all_hi || key0 < all_lo;
-                    chk_weights<EP, DP, CAP>(sc_tile, sc, mask[0], edge, key0, qpos, qlow, ref, sum, o, pw);
-                }
-                if (!second) {
-                    if (ahead - 1 < upto) wait_vmem<(NST - 3) * D::LOADS>();
-                    else wait_vmem<0>();
-                }
+                if (ahead < upto) mask[NST - 1] = issue(ahead, lds + (slot == 0 ? NST - 1 : slot - 1) * D::STAGE);
+            };
+            auto landed = [&](int newest) {
+                if (newest < upto) wait_vmem<(NST - 3) * D::LOADS>();
+                else wait_vmem<0>();
+            };
+            auto enter_softmax = [&] {
+                if (second) refill();
+            };
+            auto enter_mma = [&] {
+                if (!second) landed(j + NST - 2);
                 wg_barrier();
-                if (!second && ahead < upto)
-                    mask[NST - 1] = chk_issue<KV8, DP>(a, kb, vb, pages, first, t0 + ahead, kr.lo, kr.hi,
-                                                       lds + fill * D::STAGE, wave);
-                if (now) chk_values<EP, KV8, DP>(lds + slot * D::STAGE, pw, o);
-                if (j + 1 < upto && act(mask[1], j + 1))
-                    chk_scores<E, KV8, DP>(lds + next * D::STAGE, qf, sc_tile);
-                if (second) {
-                    if (ahead < upto) wait_vmem<(NST - 3) * D::LOADS>();
-                    else wait_vmem<0>();
-                }
+                if (!second) refill();
+            };
+            auto leave_mma = [&] {
+                if (second) landed(j + NST - 1);
                 wait_lds();
                 wg_barrier();
 #pragma unroll
                 for (int i = 0; i + 1 < NST; ++i) mask[i] = mask[i + 1];
-                slot = next;
+                slot = slot + 1 == NST ? 0 : slot + 1;
+                ++j;
+            };
+            auto here = [&] { return lds + slot * D::STAGE; };
+            auto there = [&] { return lds + (slot + 1 == NST ? 0 : slot + 1) * D::STAGE; };
+            auto weights = [&] {
+                const int key0 = (t0 + j) * CHK_KEYS;
+                const bool edge = ~mask[0] || key0 + CHK_KEYS > all_hi || key0 < all_lo;
+                mma.template begin<true, false>(here(), here());
+                __builtin_amdgcn_sched_barrier(0);
+                chk_weights<EP, DP, CAP>(sc_tile, sc, mask[0], edge, key0, qpos, qlow, ref, sum, o, pw);
+            };
+            if (ja == pos && ja < jb) {
+                mma.template begin<false, true>(lds, lds);
+                mma.template finish<false, true>(lds, lds, pw, qf, o, sc_tile);
+            }
+            if (second) {
+                landed(pos + NST - 2);
+                wg_barrier();
+            }
+            while (j < ja) {
+                enter_softmax();
+                enter_mma();
+                if (j + 1 == ja && ja < jb) {
+                    mma.template begin<false, true>(there(), there());
+                    mma.template finish<false, true>(there(), there(), pw, qf, o, sc_tile);
+                }
+                leave_mma();
+            }
+            while (j + 1 < jb) {
+                enter_softmax();
+                weights();
+                enter_mma();
+                mma.template finish<true, true>(here(), there(), pw, qf, o, sc_tile);
+                leave_mma();
+            }
+            if (j < jb) {
+                enter_softmax();
+                weights();
+                enter_mma();
+                mma.template finish<true, false>(here(), here(), pw, qf, o, sc_tile);
+                leave_mma();
+            }
+            while (j < upto) {
+                enter_softmax();
+                enter_mma();
+                leave_mma();
             }
             if (!second) wg_barrier();
             pos = upto;
@@ -1077,7 +1198,11 @@ __global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(
         }
 
         const float den = sum + __shfl_xor(sum, 32);
-        if (row < r1) {
+        int n_out = threadIdx.x & 31;       // (opaque: nothing of this is kept across the loop)
+        asm volatile("" : "+v"(n_out));
+        const int out_row = w0 + n_out;
+        if (out_row < r1) {
+            const int tok = out_row / a.group, qh = h * a.group + out_row % a.group;
             if (whole) {
                 const float inv = (den > 0.0f || den != den ? 1.0f / den : 0.0f) * (KV8 ? a.kv.v_scale[h] : 1.0f);
                 char* orow = a.out + (int64_t)(s.start + tok) * a.o_tok_b + qh * a.o_head_b;
