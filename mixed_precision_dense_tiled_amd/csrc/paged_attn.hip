@@ -159,6 +159,13 @@ __device__ __forceinline__ void global_to_lds16(const char* src, MPDT_LDS char* 
                  : "{m0}"((uint32_t)(uintptr_t)dst), "v"((uint64_t)(uintptr_t)src));
 }
 
+// The same from a scalar base and a 32-bit offset per lane.
+__device__ __forceinline__ void global_to_lds16(const char* base, uint32_t off, MPDT_LDS char* dst) {
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "{m0}"((uint32_t)(uintptr_t)dst), "v"(off), "s"((uint64_t)(uintptr_t)base));
+}
+
 __device__ __forceinline__ u32x2 lds_load8(const MPDT_LDS char* base, uint32_t off) {
     return *reinterpret_cast<const MPDT_LDS u32x2*>(base + off);
 }
@@ -358,31 +365,46 @@ __device__ __forceinline__ void find_entry(const AttnArgs& a, int e, int* red, i
     __syncthreads();
 }
 
-// Page numbers of the keys from key tile `tile` on, into LDS; returns the
-// tile up to which they reach (at most `end`).  Called by all threads.
+// The byte offsets of the pages that hold the keys from key tile `tile` on,
+// into LDS (-1: no such page); returns the tile up to which they reach (at most
+// `end`).  clean: all of them exist.  Called by all threads.
 template <int NT, int KT>
-__device__ __forceinline__ int fetch_pages(const AttnArgs& a, int b, int tile, int end, int* pages, int& first) {
+__device__ __forceinline__ int fetch_pages(const AttnArgs& a, int b, int tile, int end, int64_t* pages, int& first,
+                                           bool* clean = nullptr) {
     const int64_t k0 = (int64_t)tile * KT, ps = a.kv.page_size;
     first = (int)(k0 / ps);
     const int64_t reach = ((int64_t)first + PAGES_LDS) * ps / KT;
     const int stop = (int)min((int64_t)end, reach);
     const int last = (int)min(((int64_t)stop * KT - 1) / ps, (int64_t)a.sv.width - 1);
     const int32_t* row = a.sv.table + (int64_t)b * a.sv.ld_table;
-    for (int i = threadIdx.x; i <= last - first; i += NT) pages[i] = row[first + i];
-    __syncthreads();
+    int bad = 0;
+    for (int i = threadIdx.x; i <= last - first; i += NT) {
+        const int pg = row[first + i];
+        const bool ok = pg >= 0 && pg < a.kv.pages;
+        pages[i] = ok ? pg * a.kv.page_b : -1;
+        bad |= !ok;
+    }
+    bad = __syncthreads_or(bad);
+    if (clean) *clean = !uni(bad);
     return stop;
 }
 
+// Place of a key: its page's entry and its slot.
+struct Place {
+    int entry, slot;
+};
+__device__ __forceinline__ Place place_of(const PagedKV& kv, int first, int key) {
+    const int pi = kv.page_of(key);
+    return Place{pi - first, key - pi * kv.page_size};
+}
+
 // Byte offset of a key's row in the cache, and whether there is such a key.
-__device__ __forceinline__ bool key_offset(const PagedKV& kv, const int* pages, int first, int key, int lo, int hi,
-                                           int64_t& off) {
-    const bool in = key >= lo && key < hi;
-    const int pi = kv.page_shift >= 0 ? key >> kv.page_shift : key / kv.page_size;
-    const int slot = key - pi * kv.page_size;
-    const int pg = in ? pages[pi - first] : -1;
-    const bool ok = pg >= 0 && pg < kv.pages;
-    off = ok ? pg * kv.page_b + slot * kv.slot_b : 0;
-    return ok;
+__device__ __forceinline__ bool key_offset(const PagedKV& kv, const int64_t* pages, int first, int key, int lo,
+                                           int hi, int64_t& off) {
+    const Place p = place_of(kv, first, key);
+    const int64_t pg = key >= lo && key < hi ? pages[p.entry] : -1;
+    off = pg >= 0 ? pg + p.slot * kv.slot_b : 0;
+    return pg >= 0;
 }
 
 __device__ __forceinline__ int64_t shfl64(int64_t v, int lane) {
@@ -454,7 +476,7 @@ struct Dec {
 // which of its 32 keys exist.  Keys that do not exist are staged as copies of
 // one that does (their weight is zero), so that the count of loads is fixed.
 template <class E, bool KV8, int DP>
-__device__ __forceinline__ uint32_t dec_issue(const AttnArgs& a, const char* kb, const char* vb, const int* pages,
+__device__ __forceinline__ uint32_t dec_issue(const AttnArgs& a, const char* kb, const char* vb, const int64_t* pages,
                                               int first, int tile, int lo, int hi, MPDT_LDS char* dst) {
     using D = Dec<E, KV8, DP>;
     using R = typename D::R;
@@ -554,7 +576,7 @@ template <class E, class EP, bool KV8, int DP, bool CAP, bool DIRECT>
 __global__ __launch_bounds__(64 * DEC_WAVES) void attn_decode_kernel(AttnArgs a) {
     using D = Dec<E, KV8, DP>;
     __shared__ __attribute__((aligned(1024))) char smem[DEC_WAVES * D::RING];
-    __shared__ int pages[PAGES_LDS];
+    __shared__ int64_t pages[PAGES_LDS];
     __shared__ float ml[2][DEC_WAVES][DEC_ROWS];
     __shared__ int red[DEC_WAVES], box[2];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -811,37 +833,100 @@ struct Chk {
     static_assert(2 * R::CH % CHK_WAVES == 0, "whole loads");
 };
 
-// Issue this wave's part of tile `tile`; returns which of its 64 keys exist.
-// Keys that do not exist are staged as zeros (from the workspace), so that a
-// weight of zero times their value is zero.
-template <bool KV8, int DP>
-__device__ __forceinline__ uint64_t chk_issue(const AttnArgs& a, const char* kb, const char* vb, const char* zeros,
-                                              const int* pages, int first, int tile, int lo, int hi,
-                                              MPDT_LDS char* dst, int wave) {
+// One wave's part of the loads of a tile, 16 keys of K or of V: look() asks
+// for their pages, found() takes the answer, and step<i>() issues the i-th load, so that the work can stand
+// between MFMAs.  PAGE16: pages hold a multiple of 16 tokens, so that a wave's
+// keys lie in one page and its address is scalar; a lane's own offset then is
+// the same for every tile.  Keys that do not exist are staged as zeros (from
+// the workspace): a weight of zero times their value is zero.
+template <bool KV8, int DP, bool PAGE16>
+struct ChkRefill {
     using D = Chk<KV8, DP>;
     using R = typename D::R;
-    // (opaque, so that what follows from it is worked out anew for each tile:
-    // kept in registers across the loop it would push others into scratch,
-    // whose loads wait for all loads in flight)
-    int lane = threadIdx.x & 63;
-    asm volatile("" : "+v"(lane));
-    int64_t off;
-    const bool ok = key_offset(a.kv, pages, first, tile * CHK_KEYS + lane, lo, hi, off);
-    const uint64_t mask = __ballot(ok);
-    if (!ok) off = -1;
-    const int row_bytes = a.kv.dim * (KV8 ? 1 : 2);
-#pragma unroll
-    for (int i = 0; i < D::LOADS; ++i) {
-        const int ii = wave * D::LOADS + i;            // K's pieces, then V's
-        const bool is_v = ii >= R::CH;
-        const int c = (is_v ? ii - R::CH : ii) * 64 + lane, r = c / R::CH, pos = c % R::CH;
-        int from = (pos ^ (is_v ? R::swz_v(r) : R::swz_k(r))) * 16;
-        if (from >= row_bytes) from = 0;
-        const int64_t o = shfl64(off, r);
-        global_to_lds16(o >= 0 ? (is_v ? vb : kb) + o + from : zeros, dst + ii * 1024);
+    static constexpr int ROWS = 64 / R::CH;      // keys of a load (rows of 12 chunks: 16 keys of three loads)
+    const AttnArgs& a;
+    const char *base, *zeros;    // K or V of the head
+    const int64_t* pages;
+    int first, lo, hi, key16;    // key16: this wave's first key in a tile
+    bool is_v, clean;
+    int lane, key0;
+    uint64_t mask;
+    int64_t page[PAGE16 ? 1 : D::LOADS];
+    uint32_t own[D::LOADS];      // PAGE16: a lane's offset in its load
+    const char* from;            // PAGE16: the wave's first key
+
+    __device__ __forceinline__ ChkRefill(const AttnArgs& a_, const char* kb, const char* vb, const char* z, int wave)
+        : a(a_), zeros(z) {
+        is_v = wave >= CHK_WAVES / 2;
+        base = is_v ? vb : kb;
+        key16 = wave % (CHK_WAVES / 2) * 16;
+        lane = threadIdx.x & 63;
+        if constexpr (PAGE16)
+            static_for<0, D::LOADS>([&](auto i) {
+                constexpr int I = decltype(i)::value;
+                own[I] = (uint32_t)(row_of<I>() * a.kv.slot_b) + chunk_of<I>();
+            });
     }
-    return mask;
-}
+    template <int I>
+    __device__ __forceinline__ int row_of() const {      // among the wave's 16
+        return (I * 64 + lane) / R::CH;
+    }
+    template <int I>
+    __device__ __forceinline__ uint32_t chunk_of() const {
+        const int r = key16 + row_of<I>(), pos = (I * 64 + lane) % R::CH;
+        const int from = (pos ^ (is_v ? R::swz_v(r) : R::swz_k(r))) * 16;
+        return from >= a.kv.dim * (KV8 ? 1 : 2) ? 0 : from;      // (dim below DP: any bytes of the row)
+    }
+
+    // Returns which of the tile's 64 keys exist.
+    __device__ __forceinline__ uint64_t look(int tile) {
+        key0 = tile * CHK_KEYS;
+        // (opaque, so that what follows from it is worked out anew for each tile:
+        // kept in registers across the loop it would push others into scratch,
+        // whose loads wait for all loads in flight)
+        lane = threadIdx.x & 63;
+        asm volatile("" : "+v"(lane));
+        if constexpr (PAGE16) {
+            page[0] = pages[a.kv.page_of(key0 + key16) - first];
+        } else {
+            static_for<0, D::LOADS>([&](auto i) {
+                constexpr int I = decltype(i)::value;
+                page[I] = pages[place_of(a.kv, first, key0 + key16 + row_of<I>()).entry];
+            });
+        }
+        mask = from_to(lo - key0, hi - 1 - key0);
+        if (!clean) mask &= __ballot(pages[place_of(a.kv, first, key0 + lane).entry] >= 0);
+        return mask;
+    }
+    // The page numbers have come back.
+    __device__ __forceinline__ void found() {
+        if constexpr (PAGE16) {
+            const int key = key0 + key16, pi = a.kv.page_of(key);
+            const int64_t pg =
+                (int64_t)((uint64_t)(uint32_t)uni((int)(page[0] >> 32)) << 32 | (uint32_t)uni((int)page[0]));
+            from = base + pg + (key - pi * a.kv.page_size) * a.kv.slot_b;
+        }
+    }
+    template <int I>
+    __device__ __forceinline__ void step(MPDT_LDS char* dst) {
+        MPDT_LDS char* d = dst + (is_v ? D::HALF : 0) + (key16 * R::CH / 64 + I) * 1024;
+        if constexpr (PAGE16) {
+            if (~mask) {
+                const char* src = from + own[I];
+                global_to_lds16((mask >> (key16 + row_of<I>())) & 1 ? src : zeros, d);
+            } else {
+                global_to_lds16(from, own[I], d);
+            }
+        } else {
+            const int slot = place_of(a.kv, first, key0 + key16 + row_of<I>()).slot;
+            const char* src = base + (page[I] + slot * a.kv.slot_b + chunk_of<I>());
+            global_to_lds16((mask >> (key16 + row_of<I>())) & 1 ? src : zeros, d);
+        }
+    }
+    __device__ __forceinline__ void steps(MPDT_LDS char* dst) {
+        static_for<0, D::LOADS>([&](auto i) { step<decltype(i)::value>(dst); });
+    }
+};
 
 // Weights of a tile from its scores, with the running maximum and sum.
 template <class EP, int DP, bool CAP>
@@ -897,6 +982,11 @@ __device__ __forceinline__ void chk_weights(f32x16 (&s)[2], const Score& sc, uin
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             p[kk][i] = EP::pack(s[kk >> 1][8 * (kk & 1) + 2 * i], s[kk >> 1][8 * (kk & 1) + 2 * i + 1]);
+    // all of it here: the compiler would move the exponentials past the barrier,
+    // next to the MFMAs that take them
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) asm volatile("" : "+v"(p[kk]));
+    asm volatile("" : "+v"(sum));
 }
 
 // The MFMAs of a phase: O^T += V^T P^T of one tile (DO_V) and S^T = K Q^T of
@@ -993,9 +1083,10 @@ struct ChkMma {
         constexpr int NG = (DO_V ? NV : 0) + (DO_K ? NK : 0);
         static_for<0, AHEAD < NG ? AHEAD : NG>([&](auto g) { load<DO_V, decltype(g)::value>(sv, sk); });
     }
-    template <bool DO_V, bool DO_K>
+    // between(g): work of the caller's after group g
+    template <bool DO_V, bool DO_K, class Fn>
     __device__ __forceinline__ void finish(const MPDT_LDS char* sv, const MPDT_LDS char* sk, const u32x4 (&p)[4],
-                                           const u32x4 (&qf)[DP / 16], f32x16 (&o)[DT], f32x16 (&s)[2]) {
+                                           const u32x4 (&qf)[DP / 16], f32x16 (&o)[DT], f32x16 (&s)[2], Fn&& between) {
         constexpr int NG = (DO_V ? NV : 0) + (DO_K ? NK : 0);
         if constexpr (DO_K) {
 #pragma unroll
@@ -1012,17 +1103,18 @@ struct ChkMma {
                 mma_k(buf[g % NBUF], qf[2 * d], qf[2 * d + 1], s);
             }
             __builtin_amdgcn_sched_barrier(0);
+            between(gc);
         });
     }
 };
 
-template <class E, class EP, bool KV8, int DP, bool CAP>
+template <class E, class EP, bool KV8, int DP, bool CAP, bool PAGE16>
 __global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(2, 2))) void attn_chunk_kernel(
     AttnArgs a) {
     using D = Chk<KV8, DP>;
     constexpr int DT = (DP + 31) / 32, NST = D::NST;
     __shared__ __attribute__((aligned(1024))) char smem[NST * D::STAGE];
-    __shared__ int pages[PAGES_LDS];
+    __shared__ int64_t pages[PAGES_LDS];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 31, half = lane >> 5;
     const bool second = wave >= CHK_WAVES / 2;     // waves w and w + 4 share a SIMD
@@ -1099,7 +1191,9 @@ __global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(
 
         for (int pos = seg_a; pos < seg_e;) {
             int first;
-            const int upto = fetch_pages<64 * CHK_WAVES, CHK_KEYS>(a, b, t0 + pos, t0 + seg_e, pages, first) - t0;
+            bool clean;
+            const int upto =
+                fetch_pages<64 * CHK_WAVES, CHK_KEYS>(a, b, t0 + pos, t0 + seg_e, pages, first, &clean) - t0;
             // tiles [ja, jb) hold keys that this wave's rows see
             int ja = upto, jb = upto;
             if (busy && w_hi >= w_lo) {
@@ -1107,39 +1201,40 @@ __global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(
                 jb = min(max(w_hi < 0 ? pos : w_hi / CHK_KEYS + 1 - t0, ja), upto);
             }
             uint64_t mask[NST];      // which keys of the tiles j, j + 1, ... exist
-            auto issue = [&](int j, MPDT_LDS char* dst) {
-                return chk_issue<KV8, DP>(a, kb, vb, p.zeros, pages, first, t0 + j, kr.lo, kr.hi, dst, wave);
-            };
+            ChkRefill<KV8, DP, PAGE16> refill(a, kb, vb, p.zeros, wave);
+            refill.pages = pages;
+            refill.first = first;
+            refill.clean = clean;
+            refill.lo = kr.lo;
+            refill.hi = kr.hi;
+            // (past the end the last tile comes again, into a stage that nobody
+            // reads: the count of loads in flight is always the same)
 #pragma unroll
-            for (int i = 0; i < NST; ++i) mask[i] = 0;
-#pragma unroll
-            for (int i = 0; i < NST - 1; ++i)
-                if (pos + i < upto) mask[i] = issue(pos + i, lds + i * D::STAGE);
-            if (pos + NST - 2 < upto) wait_vmem<(NST - 2) * D::LOADS>();
-            else wait_vmem<0>();
+            for (int i = 0; i < NST - 1; ++i) {
+                mask[i] = refill.look(t0 + min(pos + i, upto - 1));
+                refill.found();
+                refill.steps(lds + i * D::STAGE);
+            }
+            wait_vmem<(NST - 2) * D::LOADS>();
             wg_barrier();
             int j = pos, slot = 0;
             // From here on the first four waves run one phase ahead.  A tile j
             // has landed for all before a first wave's MFMAs of tile j - 1, and
-            // its stage is free after a second wave's MFMAs of tile j.
-            auto refill = [&] {
-                const int ahead = j + NST - 1;
-                if (ahead < upto) mask[NST - 1] = issue(ahead, lds + (slot == 0 ? NST - 1 : slot - 1) * D::STAGE);
-            };
-            auto landed = [&](int newest) {
-                if (newest < upto) wait_vmem<(NST - 3) * D::LOADS>();
-                else wait_vmem<0>();
-            };
-            auto enter_softmax = [&] {
-                if (second) refill();
-            };
+            // its stage is free after a second wave's MFMAs of tile j: it takes
+            // the loads of tile j + NST in the MFMA phase of tile j + 1.
+            auto landed = [&] { wait_vmem<(NST - 3) * D::LOADS>(); };
+            auto look = [&] { mask[NST - 1] = refill.look(t0 + min(j + NST - 1, upto - 1)); };
+            auto free_stage = [&] { return lds + (slot == 0 ? NST - 1 : slot - 1) * D::STAGE; };
+            // The MFMA phase goes first where both waves of the SIMD could issue.
             auto enter_mma = [&] {
-                if (!second) landed(j + NST - 2);
+                refill.found();
+                if (!second) landed();
                 wg_barrier();
-                if (!second) refill();
+                __builtin_amdgcn_s_setprio(1);
             };
             auto leave_mma = [&] {
-                if (second) landed(j + NST - 1);
+                __builtin_amdgcn_s_setprio(0);
+                if (second) landed();
                 wait_lds();
                 wg_barrier();
 #pragma unroll
@@ -1156,42 +1251,51 @@ __global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(
                 __builtin_amdgcn_sched_barrier(0);
                 chk_weights<EP, DP, CAP>(sc_tile, sc, mask[0], edge, key0, qpos, qlow, ref, sum, o, pw);
             };
+            auto nothing = [](auto) {};
             if (ja == pos && ja < jb) {
                 mma.template begin<false, true>(lds, lds);
-                mma.template finish<false, true>(lds, lds, pw, qf, o, sc_tile);
+                mma.template finish<false, true>(lds, lds, pw, qf, o, sc_tile, nothing);
             }
             if (second) {
-                landed(pos + NST - 2);
+                landed();
                 wg_barrier();
             }
             while (j < ja) {
-                enter_softmax();
+                look();
                 enter_mma();
+                refill.steps(free_stage());
                 if (j + 1 == ja && ja < jb) {
                     mma.template begin<false, true>(there(), there());
-                    mma.template finish<false, true>(there(), there(), pw, qf, o, sc_tile);
+                    mma.template finish<false, true>(there(), there(), pw, qf, o, sc_tile, nothing);
                 }
                 leave_mma();
             }
             while (j + 1 < jb) {
-                enter_softmax();
+                look();
                 weights();
                 enter_mma();
-                mma.template finish<true, true>(here(), there(), pw, qf, o, sc_tile);
+                MPDT_LDS char* to = free_stage();
+                mma.template finish<true, true>(here(), there(), pw, qf, o, sc_tile, [&](auto g) {
+                    constexpr int i = decltype(g)::value - 1;
+                    if constexpr (i >= 0 && i < D::LOADS) refill.template step<i>(to);
+                });
                 leave_mma();
             }
             if (j < jb) {
-                enter_softmax();
+                look();
                 weights();
                 enter_mma();
-                mma.template finish<true, false>(here(), here(), pw, qf, o, sc_tile);
+                refill.steps(free_stage());
+                mma.template finish<true, false>(here(), here(), pw, qf, o, sc_tile, nothing);
                 leave_mma();
             }
             while (j < upto) {
-                enter_softmax();
+                look();
                 enter_mma();
+                refill.steps(free_stage());
                 leave_mma();
             }
+            wait_vmem<0>();
             if (!second) wg_barrier();
             pos = upto;
             __syncthreads();     // page numbers and stages are free again
@@ -1275,9 +1379,12 @@ hipError_t launch_as(const AttnArgs& a, const Shape& s, hipStream_t stream) {
     if (s.few) {
         hipLaunchKernelGGL((attn_decode_kernel<E, EP, KV8, DP, CAP, false>), dim3((unsigned)s.workers),
                            dim3(64 * DEC_WAVES), 0, stream, a);
+    } else if (a.kv.page_size % 16 == 0) {
+        hipLaunchKernelGGL((attn_chunk_kernel<E, EP, KV8, DP, CAP, true>), dim3((unsigned)s.workers),
+                           dim3(64 * CHK_WAVES), 0, stream, a);
     } else {
-        hipLaunchKernelGGL((attn_chunk_kernel<E, EP, KV8, DP, CAP>), dim3((unsigned)s.workers), dim3(64 * CHK_WAVES),
-                           0, stream, a);
+        hipLaunchKernelGGL((attn_chunk_kernel<E, EP, KV8, DP, CAP, false>), dim3((unsigned)s.workers),
+                           dim3(64 * CHK_WAVES), 0, stream, a);
     }
     if ((err = hipGetLastError()) != hipSuccess) return err;
     hipLaunchKernelGGL((attn_join_kernel<DP>), dim3((unsigned)s.entries, (unsigned)a.kv.kv_heads, s.tile_rows / 16),

@@ -21,8 +21,14 @@ struct PagedKV {
     const float* v_scale;
     int64_t pages;
     int page_size;
-    int page_shift;         // log2(page_size), or -1 where it is no power of two
+    uint32_t page_mul;      // key / page_size = (mulhi(key, page_mul) + key) >> page_shift, key < 2^31
+    int page_shift;
     int kv_heads, dim, type;
+
+    __host__ __device__ int page_of(int key) const {
+        const uint32_t k = (uint32_t)key;
+        return (int)(((uint32_t)((uint64_t)k * page_mul >> 32) + k) >> page_shift);
+    }
 };
 
 // Which sequence holds which pages, and how long it is.

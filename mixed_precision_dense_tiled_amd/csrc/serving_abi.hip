@@ -78,6 +78,7 @@ mpdt_status check_cache(const char* fn, const mpdt_paged_kv* kv, const mpdt_sequ
     if (kv->dtype == MPDT_E4M3 && (!kv->k_scale || !kv->v_scale)) return invalid(fn, "an E4M3 cache needs scales");
     if (kv->dtype == MPDT_E4M3 && (off(kv->k_scale, 4) || off(kv->v_scale, 4)))
         return misaligned(fn, "pointer not aligned to its element size");
+    if (kv->slot_stride >= (int64_t(1) << 26)) return invalid(fn, "slot_stride must be below 2^26");
     const std::initializer_list<Axis> axes = {{kv->pages, kv->page_stride * es},
                                               {kv->page_size, kv->slot_stride * es},
                                               {kv->kv_heads, kv->head_stride * es}};
@@ -94,9 +95,11 @@ mpdt_status check_cache(const char* fn, const mpdt_paged_kv* kv, const mpdt_sequ
     o->v_scale = kv->v_scale;
     o->pages = kv->pages;
     o->page_size = (int)kv->page_size;
-    o->page_shift = -1;
-    for (int i = 0; i < 31; ++i)
-        if (kv->page_size == int64_t(1) << i) o->page_shift = i;
+    // division by a constant, rounded-up reciprocal: with s = ceil(log2 d) and
+    // m = floor(2^32 (2^s - d) / d) + 1, n / d = (mulhi(n, m) + n) >> s
+    o->page_shift = 0;
+    while ((int64_t(1) << o->page_shift) < kv->page_size) ++o->page_shift;
+    o->page_mul = (uint32_t)((((uint64_t(1) << o->page_shift) - kv->page_size) << 32) / kv->page_size + 1);
     o->kv_heads = (int)kv->kv_heads;
     o->dim = (int)kv->dim;
     o->type = kv->dtype;

@@ -157,7 +157,7 @@ def c_attn(kvs=None, sq=None, heads=8, dtype=0, q=P + 5 * GB, qt=512, qh=64, out
 def test_attention_abi():
     for k in (dict(dim=8), dict(dim=72), dict(dim=144), dict(pages=0), dict(page_size=0), dict(kv_heads=0),
               dict(dtype=2), dict(dtype=7), dict(k=None), dict(page_stride=-2048), dict(dtype=3),
-              dict(page_stride=1 << 50), dict(pages=(1 << 30) + 1)):
+              dict(page_stride=1 << 50), dict(slot_stride=1 << 26), dict(pages=(1 << 30) + 1)):
         assert c_attn(kv(**k)) == INVALID, k
     for k in (dict(k=P + 2), dict(slot_stride=129), dict(head_stride=60)):
         assert c_attn(kv(**k)) == MISALIGNED, k
