@@ -1112,6 +1112,7 @@ template <class E, class EP, bool KV8, int DP, bool CAP, bool PAGE16>
 __global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(2, 2))) void attn_chunk_kernel(
     AttnArgs a) {
     using D = Chk<KV8, DP>;
+    using MMA = ChkMma<E, EP, KV8, DP>;
     constexpr int DT = (DP + 31) / 32, NST = D::NST;
     __shared__ __attribute__((aligned(1024))) char smem[NST * D::STAGE];
     __shared__ int64_t pages[PAGES_LDS];
@@ -1181,7 +1182,7 @@ __global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(
         float ref = NO_MAX, sum = 0.0f;
         f32x16 o[DT], sc_tile[2];
         u32x4 pw[4];
-        ChkMma<E, EP, KV8, DP> mma;
+        MMA mma;
 #pragma unroll
         for (int t = 0; t < DT; ++t)
 #pragma unroll
@@ -1247,9 +1248,8 @@ __global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(
             auto weights = [&] {
                 const int key0 = (t0 + j) * CHK_KEYS;
                 const bool edge = ~mask[0] || key0 + CHK_KEYS > all_hi || key0 < all_lo;
-                mma.template begin<true, false>(here(), here());
-                __builtin_amdgcn_sched_barrier(0);
                 chk_weights<EP, DP, CAP>(sc_tile, sc, mask[0], edge, key0, qpos, qlow, ref, sum, o, pw);
+                mma.template begin<true, false>(here(), here());
             };
             auto nothing = [](auto) {};
             if (ja == pos && ja < jb) {
@@ -1276,7 +1276,8 @@ __global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(
                 enter_mma();
                 MPDT_LDS char* to = free_stage();
                 mma.template finish<true, true>(here(), there(), pw, qf, o, sc_tile, [&](auto g) {
-                    constexpr int i = decltype(g)::value - 1;
+                    // (after V's groups, whose operands are the most LDS reads)
+                    constexpr int i = decltype(g)::value - (MMA::NV + MMA::NK - D::LOADS);
                     if constexpr (i >= 0 && i < D::LOADS) refill.template step<i>(to);
                 });
                 leave_mma();
