@@ -109,7 +109,8 @@ struct LogprobArgs {
     float* top_logprob;     // [rows, top]
     int64_t* top_index;
     char* ws;
-    int segments;           // pieces of a row, one workgroup each
+    int segments;           // pieces of a row, one workgroup each (set by the launcher)
+    int chunks;             // chunks of a segment
     // backward
     const float* g_logprob; // [rows] or null
     const float* g_entropy;
@@ -117,7 +118,7 @@ struct LogprobArgs {
     int64_t ld_grad_b;
 };
 constexpr int LOGPROB_MAX_TOP = 64;
-int logprob_segments(int type, int64_t rows, int64_t vocab);
+bool logprob_fits(int type, int64_t rows, int64_t vocab);   // the launch's size
 int64_t logprob_workspace(int type, int64_t rows, int64_t vocab, int top);
 hipError_t launch_token_logprobs(const LogprobArgs& a, hipStream_t stream);
 hipError_t launch_token_logprobs_backward(const LogprobArgs& a, hipStream_t stream);

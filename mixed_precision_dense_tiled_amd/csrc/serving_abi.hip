@@ -337,7 +337,7 @@ mpdt_status check_logits(const char* fn, int dtype, int64_t rows, int64_t vocab,
         return misaligned(fn, "pointer not aligned to its element size");
     if (!span(logits, {{rows, ld * size_of(dtype)}}, vocab * size_of(dtype), b))
         return invalid(fn, "operand too large");
-    if (rows * mpdt::logprob_segments(dtype, rows, vocab) > 0x7fffffff) return invalid(fn, "too many rows");
+    if (!mpdt::logprob_fits(dtype, rows, vocab)) return invalid(fn, "too many rows");
     return MPDT_SUCCESS;
 }
 
@@ -364,7 +364,7 @@ MPDT_EXPORT mpdt_status token_logprobs(int dtype, int64_t rows, int64_t vocab, c
     if (!logprob || !lse || !entropy || (top > 0 && (!top_logprobs || !top_indices)))
         return invalid(fn, "output is NULL");
     const int64_t need = mpdt::logprob_workspace(dtype, rows, vocab, (int)top);
-    if (!workspace || workspace_bytes < need) return invalid(fn, "workspace too small");
+    if (workspace_bytes < need || (need > 0 && !workspace)) return invalid(fn, "workspace too small");
     if (off(logprob, 4) || off(lse, 4) || off(entropy, 4) || (top > 0 && (off(top_logprobs, 4) || off(top_indices, 8))) ||
         off(workspace, 16))
         return misaligned(fn, "pointer not aligned to its element size (workspace: 16 bytes)");
@@ -375,7 +375,7 @@ MPDT_EXPORT mpdt_status token_logprobs(int dtype, int64_t rows, int64_t vocab, c
     (void)span(entropy, {{1, 0}}, rows * 4, &outs[2]);
     (void)span(top_logprobs, {{top > 0, 0}}, rows * top * 4, &outs[3]);
     (void)span(top_indices, {{top > 0, 0}}, rows * top * 8, &outs[4]);
-    (void)span(workspace, {{1, 0}}, need, &outs[5]);
+    (void)span(workspace, {{need > 0, 0}}, need, &outs[5]);
     for (int i = 0; i < 6; ++i) {
         bool meets = outs[i].meets(bx) || outs[i].meets(bt);
         for (int j = 0; j < i; ++j) meets = meets || outs[i].meets(outs[j]);
@@ -396,7 +396,6 @@ MPDT_EXPORT mpdt_status token_logprobs(int dtype, int64_t rows, int64_t vocab, c
     a.top_logprob = top_logprobs;
     a.top_index = top_indices;
     a.ws = (char*)workspace;
-    a.segments = mpdt::logprob_segments(dtype, rows, vocab);
     return abi_launched(mpdt::launch_token_logprobs(a, (hipStream_t)stream), fn);
 }
 
@@ -437,6 +436,5 @@ MPDT_EXPORT mpdt_status token_logprobs_backward(int dtype, int64_t rows, int64_t
     a.g_entropy = g_entropy;
     a.grad = (char*)grad;
     a.ld_grad_b = ld_grad * size_of(dtype);
-    a.segments = mpdt::logprob_segments(dtype, rows, vocab);
     return abi_launched(mpdt::launch_token_logprobs_backward(a, (hipStream_t)stream), fn);
 }

@@ -353,12 +353,12 @@ def token_logprobs(logits, targets, top_k=0):
         top_v = torch.empty((rows, top_k), dtype=torch.float32, device=dev)
         top_i = torch.empty((rows, top_k), dtype=torch.int64, device=dev)
     size = L.token_logprobs_workspace(code, rows, vocab, top_k)
-    ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    ws = torch.empty(size, dtype=torch.uint8, device=dev) if size > 0 else None
     p = stats.data_ptr()
     _check("token_logprobs",
            L.token_logprobs(code, rows, vocab, logits.data_ptr(), ld, pt, top_k, p, p + 4 * rows, p + 8 * rows,
-                            top_v.data_ptr() if top_k else None, top_i.data_ptr() if top_k else None, ws.data_ptr(),
-                            size, _stream(logits)))
+                            top_v.data_ptr() if top_k else None, top_i.data_ptr() if top_k else None,
+                            None if ws is None else ws.data_ptr(), size, _stream(logits)))
     return TokenLogprobs(logprob, lse, entropy, top_v, top_i)
 
 

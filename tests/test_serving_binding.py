@@ -244,11 +244,11 @@ def test_logprobs_abi():
 
     for k in (dict(dtype=3), dict(rows=-1), dict(vocab=0), dict(x=None), dict(t=None), dict(ld=99), dict(top=65),
               dict(top=-1), dict(lp=None), dict(lse=None), dict(ent=None), dict(tv=None), dict(ti=None),
-              dict(ws=None), dict(n=1), dict(vocab=10, top=11), dict(rows=1 << 30, vocab=1 << 30, ld=1 << 30)):
+              dict(ws=None, vocab=9000, ld=9000), dict(n=1, vocab=9000, ld=9000), dict(vocab=10, top=11), dict(rows=1 << 30, vocab=1 << 30, ld=1 << 30)):
         assert call(**k) == INVALID, k
     for k in (dict(x=P + 2), dict(t=P + GB + 4), dict(ti=P + 6 * GB + 4), dict(ws=P + 7 * GB + 8)):
         assert call(**k) == MISALIGNED, k
-    assert call(lp=P + 64) == ALIASING and call(lse=P + 2 * GB) == ALIASING and call(ws=P + 6 * GB) == ALIASING
+    assert call(lp=P + 64) == ALIASING and call(lse=P + 2 * GB) == ALIASING and call(ws=P + 6 * GB, vocab=9000, ld=9000) == ALIASING
     assert call(rows=0) == SUCCESS
     assert L.token_logprobs_workspace(2, 4, 100, 65) == -1
 
