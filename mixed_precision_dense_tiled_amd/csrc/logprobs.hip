@@ -33,7 +33,6 @@ namespace mpdt {
 namespace {
 
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
-constexpr int NO_INDEX = 0x7fffffff;
 constexpr int NT = 256, WAVES = NT / 64;
 constexpr int CAND = 1024;            // room for gathered values
 constexpr int PRUNE = 192;            // more of them are cut to the k largest
@@ -74,6 +73,19 @@ struct Elem {
     }
 };
 
+// Maxima that pass a NaN over, without the extra operation that makes a
+// signalling one quiet first (fmaxf's).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+__device__ __forceinline__ float max2(float a, float b) {
+    float r;
+    asm("v_max_f32 %0, %1, %2" : "=v"(r) : "s"(b), "v"(a));
+    return r;
+}
+
 // A wave's maximum and sum by DPP (rows of 16 lanes, then across them): the
 // last lane's value, to all.
 template <int CTRL>
@@ -103,8 +115,8 @@ __device__ __forceinline__ float wave_sum(float v) {
     return last_lane(v);
 }
 
-// The k-th largest (k from 0) of the 64 lanes' values: a bitonic sort.
-__device__ __forceinline__ float wave_kth(float v, int k) {
+// The 64 lanes' values, largest first: a bitonic sort.
+__device__ __forceinline__ float wave_sorted(float v) {
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int size = 2; size <= 64; size <<= 1) {
@@ -115,7 +127,7 @@ __device__ __forceinline__ float wave_kth(float v, int k) {
             v = low == down ? fmaxf(v, o) : fminf(v, o);
         }
     }
-    return __shfl(v, k);
+    return v;
 }
 
 // Order of (value, index): larger first, NaN above all, then the lower index.
@@ -125,82 +137,81 @@ __device__ __forceinline__ uint64_t order_key(float x, int index) {
     return ((uint64_t)k << 32) | (uint32_t)~index;
 }
 
-struct TopShared {
-    float bound[WAVES];
-    float value[CAND];
-    int index[CAND];
-    uint64_t best[WAVES];
-    int count;
-    int odd;             // a value is no number
-};
-
-// The best such bound over the workgroup's values.  mine: this thread's
-// largest.  All threads call it.
-__device__ __forceinline__ float top_bound(TopShared& sh, int k, float mine) {
-    const float kth = wave_kth(mine, k - 1);
-    if ((threadIdx.x & 63) == 0) sh.bound[threadIdx.x >> 6] = kth;
-    __syncthreads();
-    float bound = sh.bound[0];
-#pragma unroll
-    for (int w = 1; w < WAVES; ++w) bound = fmaxf(bound, sh.bound[w]);
-    return bound;
+__device__ __forceinline__ int key_index(uint64_t key) { return (int)~(uint32_t)key; }
+__device__ __forceinline__ float key_value(uint64_t key) {
+    const uint32_t k = (uint32_t)(key >> 32);
+    return k == 0xffffffffu ? __builtin_nanf("") : __uint_as_float((k >> 31) ? k ^ 0x80000000u : ~k);
 }
 
-__device__ __forceinline__ void top_gather(TopShared& sh, float x, int index) {
-    const int at = atomicAdd(&sh.count, 1);
-    if (at < CAND) {
-        sh.value[at] = x;
-        sh.index[at] = index;
+struct TopShared {
+    float bound[2][WAVES];
+    uint64_t key[CAND];  // gathered values, as order keys
+    uint64_t best[WAVES];
+    int count;
+    int fresh[4];        // values gathered from a group of chunks, in turn: one barrier a group
+};
+constexpr int ODD = 1 << 20;          // added to them where a value is no number
+
+// A bound that at least k of the workgroup's values reach: the best wave's
+// k-th largest lane maximum, or where it is larger the smallest of the waves'
+// k/4-th.  mine: this thread's largest.  All threads call it.
+__device__ __forceinline__ float top_bound(TopShared& sh, int k, float mine) {
+    const float v = wave_sorted(mine);
+    const float whole = __shfl(v, k - 1), part = __shfl(v, (k - 1) / WAVES);
+    if ((threadIdx.x & 63) == 0) {
+        sh.bound[0][threadIdx.x >> 6] = whole;
+        sh.bound[1][threadIdx.x >> 6] = part;
     }
+    __syncthreads();
+    float best = sh.bound[0][0], least = sh.bound[1][0];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) {
+        best = fmaxf(best, sh.bound[0][w]);
+        least = fminf(least, sh.bound[1][w]);
+    }
+    return fmaxf(best, least);
+}
+
+__device__ __forceinline__ void top_gather(TopShared& sh, int kept, int* counter, float x, int index) {
+    const int at = kept + (atomicAdd(counter, 1) & (ODD - 1));
+    if (at < CAND) sh.key[at] = order_key(x, index);
 }
 
 // The k best of the `count` gathered values to the front of the list, in
 // order.  (Gathered in any order: the result is the same.)  All threads call it.
 __device__ __forceinline__ void top_sort(TopShared& sh, int k, int count) {
     constexpr int EACH = CAND / NT;
-    float x[EACH];
-    int ix[EACH], rank[EACH];
+    uint64_t key[EACH];
+    int rank[EACH];
 #pragma unroll
     for (int e = 0; e < EACH; ++e) {
         const int c = threadIdx.x + e * NT;
         rank[e] = k;
         if (c >= count) continue;
-        x[e] = sh.value[c];
-        ix[e] = sh.index[c];
-        const uint64_t key = order_key(x[e], ix[e]);
+        key[e] = sh.key[c];
         int r = 0;
-#pragma unroll 1
-        for (int j = 0; j < count; ++j) r += order_key(sh.value[j], sh.index[j]) > key;
+#pragma unroll 8
+        for (int j = 0; j < count; ++j) r += sh.key[j] > key[e];
         rank[e] = r;
     }
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < EACH; ++e)
-        if (rank[e] < k) {
-            sh.value[rank[e]] = x[e];
-            sh.index[rank[e]] = ix[e];
-        }
+        if (rank[e] < k) sh.key[rank[e]] = key[e];
     if (threadIdx.x == 0) sh.count = min(count, k);
     __syncthreads();
 }
 
-// One of k passes for the largest of the workgroup's N values a thread below
-// `last`; 0 where there is none.  All threads call it.
-template <class V, class I>
-__device__ __forceinline__ uint64_t top_next(TopShared& sh, int n, uint64_t last, V value, I index, float& bx,
-                                             int& bi, bool& mine) {
-    uint64_t best = 0;
+// One of k passes: the largest of the workgroup's keys below `last`, n a
+// thread; 0 where there is none.  All threads call it.
+template <class K>
+__device__ __forceinline__ uint64_t top_next(TopShared& sh, int n, uint64_t last, K key) {
+    uint64_t all = 0;
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
-        const int ix = index(i);
-        const uint64_t key = ix == NO_INDEX ? 0 : order_key(value(i), ix);
-        if (key < last && key > best) {
-            best = key;
-            bx = value(i);
-            bi = ix;
-        }
+        const uint64_t x = key(i);
+        if (x < last && x > all) all = x;
     }
-    uint64_t all = best;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
         const uint64_t o = ((uint64_t)(uint32_t)__shfl_xor((int)(all >> 32), d) << 32) |
@@ -213,22 +224,19 @@ __device__ __forceinline__ uint64_t top_next(TopShared& sh, int n, uint64_t last
 #pragma unroll
     for (int w = 1; w < WAVES; ++w) all = sh.best[w] > all ? sh.best[w] : all;
     __syncthreads();
-    mine = all != 0 && best == all;
     return all;
 }
 
-// Per segment in the workspace: maximum, sum, weighted sum, then `top` values
-// and indices.
+// Per segment in the workspace: maximum, sum, weighted sum, then the keys of its
+// `top` largest values (0: fewer).
 struct SegWs {
     float* stat;    // [rows][segments][4]
-    float* value;   // [rows][segments][top]
-    int* index;
+    uint64_t* key;  // [rows][segments][top]
 };
-__host__ __device__ inline SegWs seg_ws(char* ws, int64_t rows, int64_t segments, int top) {
+__host__ __device__ inline SegWs seg_ws(char* ws, int64_t rows, int64_t segments) {
     SegWs w;
     w.stat = (float*)ws;
-    w.value = (float*)(ws + rows * segments * 16);
-    w.index = (int*)(ws + rows * segments * (16 + 4 * (int64_t)top));
+    w.key = (uint64_t*)(ws + rows * segments * 16);
     return w;
 }
 
@@ -260,8 +268,9 @@ __device__ __forceinline__ void write_row(const LogprobArgs& a, int row, const R
 __device__ __forceinline__ void write_top(const LogprobArgs& a, int row, const RowResult& r, const TopShared& sh) {
     if ((int)threadIdx.x < a.top) {
         const int64_t at = (int64_t)row * a.top + threadIdx.x;
-        a.top_logprob[at] = r.nan ? __builtin_nanf("") : r.none ? NEG_INF : sh.value[threadIdx.x] - r.lse;
-        a.top_index[at] = sh.index[threadIdx.x];
+        const uint64_t key = sh.key[threadIdx.x];
+        a.top_logprob[at] = r.nan ? __builtin_nanf("") : r.none ? NEG_INF : key_value(key) - r.lse;
+        a.top_index[at] = key_index(key);
     }
 }
 
@@ -281,25 +290,24 @@ __global__ __launch_bounds__(NT) void logprob_segment_kernel(LogprobArgs a) {
     const char* aligned = base - skip * E::BYTES;
     const int chunk0 = seg * a.chunks, chunk1 = min(chunk0 + a.chunks, (a.vocab + skip + NT * N - 1) / (NT * N));
     auto first_of = [&](int chunk) { return chunk * (NT * N) - skip; };      // index of a chunk's first element
+    // (always from the row's own pieces, without a condition: loads under one
+    // would wait for each other)
+    const int last_piece = (a.vocab + skip - 1) / P;
     auto fetch = [&](int chunk, u32x4 (&v)[C]) {
-        const int first = first_of(chunk);
-        const bool inner = first >= 0 && first + NT * N <= a.vocab;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int i = first + (c * NT + tid) * P;
-            if (inner || (i + P > 0 && i < a.vocab))
-                v[c] = *reinterpret_cast<const u32x4*>(aligned + ((int64_t)chunk * (NT * C) + c * NT + tid) * 16);
+            const int piece = min(chunk * (NT * C) + c * NT + tid, last_piece);
+            v[c] = *reinterpret_cast<const u32x4*>(aligned + (int64_t)piece * 16);
         }
     };
     float m = NEG_INF, s = 0.0f, t = 0.0f, bound = NEG_INF;
-    int kept = 0;        // gathered values of the chunks so far
+    int kept = 0, before = 0, group = chunk0;    // gathered values, those of the groups before; this group's chunk
     if constexpr (TOP) {
-        if (tid == 0) sh.count = sh.odd = 0;
+        if (tid < 4) sh.fresh[tid] = 0;
+        if (tid == 0) sh.count = 0;
     }
     u32x4 v[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) v[c] = u32x4{0, 0, 0, 0};
-    if (chunk0 < chunk1) fetch(chunk0, v);
+    fetch(chunk0, v);
     for (int chunk = chunk0; chunk < chunk1; ++chunk) {
         const int first = first_of(chunk);
         float x[N];
@@ -307,7 +315,7 @@ __global__ __launch_bounds__(NT) void logprob_segment_kernel(LogprobArgs a) {
         for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int j = 0; j < P; ++j) x[c * P + j] = E::get(v[c], j);
-        if (chunk + 1 < chunk1) fetch(chunk + 1, v);
+        fetch(min(chunk + 1, chunk1 - 1), v);
         if (first < 0 || first + NT * N > a.vocab) {
 #pragma unroll
             for (int c = 0; c < C; ++c)
@@ -317,9 +325,9 @@ __global__ __launch_bounds__(NT) void logprob_segment_kernel(LogprobArgs a) {
                     if (i < 0 || i >= a.vocab) x[c * P + j] = NEG_INF;
                 }
         }
-        float mine = x[0];
+        float mine = max3(x[0], x[1], x[2]);
 #pragma unroll
-        for (int i = 1; i < N; ++i) mine = fmaxf(mine, x[i]);
+        for (int i = 3; i < N; i += 2) mine = max3(mine, x[i], x[i + 1 < N ? i + 1 : i]);
         // y = (x - m) log2(e), the difference first: a mask of the type's lowest
         // value would leave the range times log2(e).  Nothing but -inf so far: m
         // counts as 0.
@@ -334,67 +342,62 @@ __global__ __launch_bounds__(NT) void logprob_segment_kernel(LogprobArgs a) {
             const float y = (x[i] - from) * LOG2E;
             const float e = __builtin_amdgcn_exp2f(y);                 // no number where x is none, or +inf
             s1 += e;
-            t1 = fmaf(e, fmaxf(y, -1e30f), t1);                        // e = 0 times a finite y where x = -inf
+            t1 = fmaf(e, max2(y, -1e30f), t1);                        // e = 0 times a finite y where x = -inf
         }
         s += s1;
         t += t1;
         if constexpr (TOP) {
-            if (chunk == chunk0) bound = top_bound(sh, k, mine);
-            if (s1 != s1) sh.odd = 1;
+            // The first chunk is a group, then four at a time; groups count in turn.
+            const int since = chunk - chunk0, turn = ((since + 3) >> 2) & 3;
+            if (since == 0) bound = top_bound(sh, k, mine);
+            if (s1 != s1) atomicAdd(&sh.fresh[turn], ODD);
             if (mine >= bound) {
                 // (few threads after the first chunk; read again, as the values'
                 // registers are worth more to the loop above)
+                u32x4 w[C];
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    w[c] = *reinterpret_cast<const u32x4*>(
+                        aligned + (int64_t)min(chunk * (NT * C) + c * NT + tid, last_piece) * 16);
 #pragma unroll 1
                 for (int c = 0; c < C; ++c) {
                     const int i = first + (c * NT + tid) * P;
-                    if (i + P <= 0 || i >= a.vocab) continue;
-                    const u32x4 w = *reinterpret_cast<const u32x4*>(
-                        aligned + ((int64_t)chunk * (NT * C) + c * NT + tid) * 16);
 #pragma unroll
-                    for (int j = 0; j < P; ++j)
-                        if (E::get(w, j) >= bound && i + j >= 0 && i + j < a.vocab) top_gather(sh, E::get(w, j), i + j);
+                    for (int j = 0; j < P; ++j) {
+                        const float y = E::get(w[0], j);
+                        if (y >= bound && i + j >= 0 && i + j < a.vocab) top_gather(sh, kept, &sh.fresh[turn], y, i + j);
+                    }
+#pragma unroll
+                    for (int d = 0; d + 1 < C; ++d) w[d] = w[d + 1];
                 }
             }
+            if ((since & 3) && chunk + 1 < chunk1) continue;
             __syncthreads();
-            const int count = sh.count, odd = sh.odd;
-            __syncthreads();
-            if (odd || count > CAND) {
-                // one by one, in the place of what this chunk has gathered (read
-                // again: the rare path takes no registers from the others)
-                const int c0 = max(first, 0) + tid, c1 = min(first + NT * N, a.vocab);
+            kept += sh.fresh[turn];
+            if (tid == 0) sh.fresh[(turn + 2) & 3] = 0;
+            if (kept > CAND) {
+                // one by one over the group, in the place of what it has gathered
+                kept = before;
+                const int c0 = max(first_of(group), 0) + tid, c1 = min(first + NT * N, a.vocab);
                 uint64_t last = ~0ull;
-                int at = kept;
 #pragma unroll 1
                 for (int r = 0; r < k; ++r) {
-                    float bx = 0.0f;
-                    int bi = 0;
-                    bool mine_it = false;
-                    const uint64_t all =
-                        top_next(sh, (c1 - c0 + NT - 1) / NT, last, [&](int i) { return E::at(base, c0 + i * NT); },
-                                 [&](int i) { return c0 + i * NT; }, bx, bi, mine_it);
-                    if (all == 0) break;
-                    if (mine_it) {
-                        sh.value[at] = bx;
-                        sh.index[at] = bi;
-                    }
-                    ++at;
-                    last = all;
+                    last = top_next(sh, (c1 - c0 + NT - 1) / NT, last,
+                                    [&](int i) { return order_key(E::at(base, c0 + i * NT), c0 + i * NT); });
+                    if (last == 0) break;
+                    if (tid == 0) sh.key[kept] = last;
+                    ++kept;
                 }
-                if (tid == 0) {
-                    sh.count = at;
-                    sh.odd = 0;
-                }
-                kept = at;
                 __syncthreads();
-            } else {
-                kept = count;
             }
-            if (kept > (chunk == chunk0 ? k : PRUNE)) {
+            if (kept > (since == 0 ? k : PRUNE)) {
                 top_sort(sh, k, kept);
                 kept = k;
-                const float kth = sh.value[k - 1];
+                const float kth = key_value(sh.key[k - 1]);
                 bound = kth == kth ? kth : bound;
             }
+            before = kept;
+            group = chunk + 1;
         }
     }
     // the threads' running sums joined
@@ -427,14 +430,13 @@ __global__ __launch_bounds__(NT) void logprob_segment_kernel(LogprobArgs a) {
         if constexpr (TOP) write_top(a, row, r, sh);
         return;
     }
-    const SegWs ws = seg_ws(a.ws, a.rows, a.segments, k);
+    const SegWs ws = seg_ws(a.ws, a.rows, a.segments);
     const int64_t at = (int64_t)row * a.segments + seg;
     if (tid == 0) *reinterpret_cast<f32x4*>(ws.stat + at * 4) = f32x4{all, s, t, 0.0f};
     if constexpr (TOP) {
         const int have = sh.count;
         if (tid < k) {
-            ws.value[at * k + tid] = tid < have ? sh.value[tid] : NEG_INF;
-            ws.index[at * k + tid] = tid < have ? sh.index[tid] : NO_INDEX;
+            ws.key[at * k + tid] = tid < have ? sh.key[tid] : 0;
         }
     }
 }
@@ -445,11 +447,10 @@ __global__ __launch_bounds__(NT) void logprob_join_kernel(LogprobArgs a) {
     using E = Elem<TYPE>;
     __shared__ TopShared sh;
     const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 63, k = a.top;
-    const SegWs ws = seg_ws(a.ws, a.rows, a.segments, k);
+    const SegWs ws = seg_ws(a.ws, a.rows, a.segments);
     const f32x4* stat = reinterpret_cast<const f32x4*>(ws.stat) + (int64_t)row * a.segments;
     const int n = a.segments * k;
-    const float* val = ws.value + (int64_t)row * n;
-    const int* idx = ws.index + (int64_t)row * n;
+    const uint64_t* keys = ws.key + (int64_t)row * n;
     if (tid == 0) sh.count = 0;
     // every wave joins the statistics: 64 segments at a time
     float m = NEG_INF;
@@ -469,14 +470,19 @@ __global__ __launch_bounds__(NT) void logprob_join_kernel(LogprobArgs a) {
     if (tid == 0) write_row<E>(a, row, r);
     if (k == 0) return;
     // the k-th largest of the segments' own maxima bounds the k-th largest value
-    float mine = NEG_INF;
-    for (int g = tid; g < a.segments; g += NT) mine = fmaxf(mine, val[(int64_t)g * k]);
-    const float bound = top_bound(sh, k, mine);
+    uint64_t first = 0;
+    for (int g = tid; g < a.segments; g += NT) {
+        const uint64_t x = keys[(int64_t)g * k];
+        first = x > first ? x : first;
+    }
+    const float bound = top_bound(sh, k, first ? key_value(first) : NEG_INF);
     if (!r.nan) {
         for (int i = tid; i < n; i += NT) {
-            const float x = val[i];
-            const int ix = idx[i];
-            if (x >= bound && ix != NO_INDEX) top_gather(sh, x, ix);
+            const uint64_t x = keys[i];
+            if (x && key_value(x) >= bound) {
+                const int at = atomicAdd(&sh.count, 1);
+                if (at < CAND) sh.key[at] = x;
+            }
         }
     }
     __syncthreads();
@@ -487,15 +493,8 @@ __global__ __launch_bounds__(NT) void logprob_join_kernel(LogprobArgs a) {
     } else {
         uint64_t last = ~0ull;
         for (int i = 0; i < k; ++i) {
-            float bx = 0.0f;
-            int bi = 0;
-            bool mine_it = false;
-            last = top_next(sh, (n - tid + NT - 1) / NT, last, [&](int e) { return val[tid + e * NT]; },
-                            [&](int e) { return idx[tid + e * NT]; }, bx, bi, mine_it);
-            if (mine_it) {
-                sh.value[i] = bx;
-                sh.index[i] = bi;
-            }
+            last = top_next(sh, (n - tid + NT - 1) / NT, last, [&](int e) { return keys[tid + e * NT]; });
+            if (tid == 0) sh.key[i] = last;
         }
         __syncthreads();
     }
