@@ -116,13 +116,15 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // The 64 lanes' values, largest first: a bitonic sort.
-__device__ __forceinline__ float wave_sorted(float v) {
-    const int lane = threadIdx.x & 63;
+__device__ __forceinline__ float lane_xor(float v, int lane, int d) {
+    return __int_as_float(__builtin_amdgcn_ds_bpermute((lane ^ d) << 2, __float_as_int(v)));
+}
+__device__ __forceinline__ float wave_sorted(float v, int lane) {
 #pragma unroll
     for (int size = 2; size <= 64; size <<= 1) {
 #pragma unroll
         for (int d = size >> 1; d > 0; d >>= 1) {
-            const float o = __shfl_xor(v, d);
+            const float o = lane_xor(v, lane, d);
             const bool low = (lane & d) == 0, down = (lane & size) == 0 || size == 64;
             v = low == down ? fmaxf(v, o) : fminf(v, o);
         }
@@ -154,13 +156,15 @@ constexpr int ODD = 1 << 20;          // added to them where a value is no numbe
 
 // A bound that at least k of the workgroup's values reach: the best wave's
 // k-th largest lane maximum, or where it is larger the smallest of the waves'
-// k/4-th.  mine: this thread's largest.  All threads call it.
-__device__ __forceinline__ float top_bound(TopShared& sh, int k, float mine) {
-    const float v = wave_sorted(mine);
-    const float whole = __shfl(v, k - 1), part = __shfl(v, (k - 1) / WAVES);
-    if ((threadIdx.x & 63) == 0) {
-        sh.bound[0][threadIdx.x >> 6] = whole;
-        sh.bound[1][threadIdx.x >> 6] = part;
+// k/4-th.  mine: this thread's largest.  All threads call it (and the functions
+// below; their tid is opaque in the loop over chunks, see there).
+__device__ __forceinline__ float top_bound(TopShared& sh, int tid, int k, float mine) {
+    const float v = wave_sorted(mine, tid & 63);
+    const float whole = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), k - 1));
+    const float part = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), (k - 1) / WAVES));
+    if ((tid & 63) == 0) {
+        sh.bound[0][tid >> 6] = whole;
+        sh.bound[1][tid >> 6] = part;
     }
     __syncthreads();
     float best = sh.bound[0][0], least = sh.bound[1][0];
@@ -179,13 +183,13 @@ __device__ __forceinline__ void top_gather(TopShared& sh, int kept, int* counter
 
 // The k best of the `count` gathered values to the front of the list, in
 // order.  (Gathered in any order: the result is the same.)  All threads call it.
-__device__ __forceinline__ void top_sort(TopShared& sh, int k, int count) {
+__device__ __forceinline__ void top_sort(TopShared& sh, int tid, int k, int count) {
     constexpr int EACH = CAND / NT;
     uint64_t key[EACH];
     int rank[EACH];
 #pragma unroll
     for (int e = 0; e < EACH; ++e) {
-        const int c = threadIdx.x + e * NT;
+        const int c = tid + e * NT;
         rank[e] = k;
         if (c >= count) continue;
         key[e] = sh.key[c];
@@ -198,14 +202,14 @@ __device__ __forceinline__ void top_sort(TopShared& sh, int k, int count) {
 #pragma unroll
     for (int e = 0; e < EACH; ++e)
         if (rank[e] < k) sh.key[rank[e]] = key[e];
-    if (threadIdx.x == 0) sh.count = min(count, k);
+    if (tid == 0) sh.count = min(count, k);
     __syncthreads();
 }
 
 // One of k passes: the largest of the workgroup's keys below `last`, n a
 // thread; 0 where there is none.  All threads call it.
 template <class K>
-__device__ __forceinline__ uint64_t top_next(TopShared& sh, int n, uint64_t last, K key) {
+__device__ __forceinline__ uint64_t top_next(TopShared& sh, int tid, int n, uint64_t last, K key) {
     uint64_t all = 0;
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
@@ -214,11 +218,12 @@ __device__ __forceinline__ uint64_t top_next(TopShared& sh, int n, uint64_t last
     }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-        const uint64_t o = ((uint64_t)(uint32_t)__shfl_xor((int)(all >> 32), d) << 32) |
-                           (uint32_t)__shfl_xor((int)(uint32_t)all, d);
+        const int from = ((tid & 63) ^ d) << 2;
+        const uint64_t o = ((uint64_t)(uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)(all >> 32)) << 32) |
+                           (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)(uint32_t)all);
         all = o > all ? o : all;
     }
-    if ((threadIdx.x & 63) == 0) sh.best[threadIdx.x >> 6] = all;
+    if ((tid & 63) == 0) sh.best[tid >> 6] = all;
     __syncthreads();
     all = sh.best[0];
 #pragma unroll
@@ -343,13 +348,20 @@ __global__ __launch_bounds__(NT) void logprob_segment_kernel(LogprobArgs a) {
             const float e = __builtin_amdgcn_exp2f(y);                 // no number where x is none, or +inf
             s1 += e;
             t1 = fmaf(e, max2(y, -1e30f), t1);                        // e = 0 times a finite y where x = -inf
+            // eight at a time, and here: all exponentials at once, next to the
+            // first use of their sums, would hold twice the registers
+            if (i % 8 == 7) asm volatile("" : "+v"(s1), "+v"(t1));
         }
         s += s1;
         t += t1;
         if constexpr (TOP) {
+            // (opaque: what follows from it is worked out anew each time, where
+            // kept across the loop it would cost registers and with them waves)
+            int tid = threadIdx.x;
+            asm volatile("" : "+v"(tid));
             // The first chunk is a group, then four at a time; groups count in turn.
             const int since = chunk - chunk0, turn = ((since + 3) >> 2) & 3;
-            if (since == 0) bound = top_bound(sh, k, mine);
+            if (since == 0) bound = top_bound(sh, tid, k, mine);
             if (s1 != s1) atomicAdd(&sh.fresh[turn], ODD);
             if (mine >= bound) {
                 // (few threads after the first chunk; read again, as the values'
@@ -382,7 +394,7 @@ __global__ __launch_bounds__(NT) void logprob_segment_kernel(LogprobArgs a) {
                 uint64_t last = ~0ull;
 #pragma unroll 1
                 for (int r = 0; r < k; ++r) {
-                    last = top_next(sh, (c1 - c0 + NT - 1) / NT, last,
+                    last = top_next(sh, tid, (c1 - c0 + NT - 1) / NT, last,
                                     [&](int i) { return order_key(E::at(base, c0 + i * NT), c0 + i * NT); });
                     if (last == 0) break;
                     if (tid == 0) sh.key[kept] = last;
@@ -391,7 +403,7 @@ __global__ __launch_bounds__(NT) void logprob_segment_kernel(LogprobArgs a) {
                 __syncthreads();
             }
             if (kept > (since == 0 ? k : PRUNE)) {
-                top_sort(sh, k, kept);
+                top_sort(sh, tid, k, kept);
                 kept = k;
                 const float kth = key_value(sh.key[k - 1]);
                 bound = kth == kth ? kth : bound;
@@ -415,7 +427,7 @@ __global__ __launch_bounds__(NT) void logprob_segment_kernel(LogprobArgs a) {
         red[1][wave] = s;
         red[2][wave] = t;
     }
-    if constexpr (TOP) top_sort(sh, k, kept);
+    if constexpr (TOP) top_sort(sh, tid, k, kept);
     __syncthreads();
     s = red[1][0];
     t = red[2][0];
@@ -475,7 +487,7 @@ __global__ __launch_bounds__(NT) void logprob_join_kernel(LogprobArgs a) {
         const uint64_t x = keys[(int64_t)g * k];
         first = x > first ? x : first;
     }
-    const float bound = top_bound(sh, k, first ? key_value(first) : NEG_INF);
+    const float bound = top_bound(sh, tid, k, first ? key_value(first) : NEG_INF);
     if (!r.nan) {
         for (int i = tid; i < n; i += NT) {
             const uint64_t x = keys[i];
@@ -489,11 +501,11 @@ __global__ __launch_bounds__(NT) void logprob_join_kernel(LogprobArgs a) {
     const int count = sh.count;
     __syncthreads();
     if (!r.nan && count <= CAND) {
-        top_sort(sh, k, count);
+        top_sort(sh, tid, k, count);
     } else {
         uint64_t last = ~0ull;
         for (int i = 0; i < k; ++i) {
-            last = top_next(sh, (n - tid + NT - 1) / NT, last, [&](int e) { return keys[tid + e * NT]; });
+            last = top_next(sh, tid, (n - tid + NT - 1) / NT, last, [&](int e) { return keys[tid + e * NT]; });
             if (tid == 0) sh.key[i] = last;
         }
         __syncthreads();
