@@ -159,11 +159,18 @@ __device__ __forceinline__ void global_to_lds16(const char* src, MPDT_LDS char* 
                  : "{m0}"((uint32_t)(uintptr_t)dst), "v"((uint64_t)(uintptr_t)src));
 }
 
-// The same from a scalar base and a 32-bit offset per lane.
+// The same from a scalar base and a 32-bit offset per lane.  ONCE: the bytes
+// are read once (non-temporal).
+template <bool ONCE = false>
 __device__ __forceinline__ void global_to_lds16(const char* base, uint32_t off, MPDT_LDS char* dst) {
-    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :
-                 : "{m0}"((uint32_t)(uintptr_t)dst), "v"(off), "s"((uint64_t)(uintptr_t)base));
+    if constexpr (ONCE)
+        asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt"
+                     :
+                     : "{m0}"((uint32_t)(uintptr_t)dst), "v"(off), "s"((uint64_t)(uintptr_t)base));
+    else
+        asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                     :
+                     : "{m0}"((uint32_t)(uintptr_t)dst), "v"(off), "s"((uint64_t)(uintptr_t)base));
 }
 
 __device__ __forceinline__ u32x2 lds_load8(const MPDT_LDS char* base, uint32_t off) {
@@ -340,29 +347,50 @@ __device__ __forceinline__ int worker_id() {
 }
 
 // Row tile `e` of a batch without a plan: all threads of the workgroup look
-// for the sequence that holds it.  box: {sequence, first row}; -1: none.
+// for the sequence that holds it (-1: none) and the tile's first row.
 template <int WAVES>
-__device__ __forceinline__ void find_entry(const AttnArgs& a, int e, int* red, int* box) {
+__device__ __forceinline__ void find_entry(const AttnArgs& a, int e, int* red, int* box, int& b, int& r0) {
+    if (a.sv.seqs <= 64) {
+        // every wave for itself: one sequence a lane
+        const int lane = threadIdx.x & 63;
+        int c = 0;
+        if (lane < a.sv.seqs) {
+            const Seq s = seq_of(a.sv, a.kv.page_size, lane);
+            c = (int)(((int64_t)s.nq * a.group + a.tile_rows - 1) / a.tile_rows);
+        }
+        int upto = c;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int y = __shfl_up(upto, d);
+            if (lane >= d) upto += y;
+        }
+        const uint64_t in = __ballot(e >= upto - c && e < upto);
+        b = in ? __builtin_ctzll(in) : -1;
+        r0 = in ? (e - __builtin_amdgcn_readlane(upto - c, b)) * a.tile_rows : 0;
+        return;
+    }
     if (threadIdx.x == 0) box[0] = -1;
     __syncthreads();
     int run = 0;
     for (int b0 = 0; b0 < a.sv.seqs; b0 += WAVES * 64) {
-        const int b = b0 + threadIdx.x;
+        const int i = b0 + threadIdx.x;
         int c = 0;
-        if (b < a.sv.seqs) {
-            const Seq s = seq_of(a.sv, a.kv.page_size, b);
+        if (i < a.sv.seqs) {
+            const Seq s = seq_of(a.sv, a.kv.page_size, i);
             c = (int)(((int64_t)s.nq * a.group + a.tile_rows - 1) / a.tile_rows);
         }
         int total;
         const int at = run + block_scan<WAVES>(c, red, total);
         if (e >= at && e < at + c) {
-            box[0] = b;
+            box[0] = i;
             box[1] = (e - at) * a.tile_rows;
         }
         run += total;
         if (run > e) break;
     }
     __syncthreads();
+    b = uni(box[0]);
+    r0 = uni(box[1]);
 }
 
 // The byte offsets of the pages that hold the keys from key tile `tile` on,
@@ -472,35 +500,74 @@ struct Dec {
     static_assert((NST - 1) * LOADS < 64, "vmcnt range");
 };
 
-// One wave's share of a tile: issue the loads of key tile `tile`; returns
-// which of its 32 keys exist.  Keys that do not exist are staged as copies of
-// one that does (their weight is zero), so that the count of loads is fixed.
+// A wave's loads of its key tiles.
 template <class E, bool KV8, int DP>
-__device__ __forceinline__ uint32_t dec_issue(const AttnArgs& a, const char* kb, const char* vb, const int64_t* pages,
-                                              int first, int tile, int lo, int hi, MPDT_LDS char* dst) {
+struct DecLoads {
     using D = Dec<E, KV8, DP>;
     using R = typename D::R;
-    const int lane = threadIdx.x & 63;
-    int64_t off;
-    const bool ok = key_offset(a.kv, pages, first, tile * DEC_KEYS + (lane & 31), lo, hi, off);
-    const uint32_t mask = (uint32_t)__ballot(ok);
-    if (mask != 0xffffffffu) {
-        const int64_t other = shfl64(off, mask ? __builtin_ctz(mask) : 0);
-        if (!ok) off = other;
+    static constexpr int PER16 = R::CH / 4;      // loads of 16 keys, K or V
+    const AttnArgs& a;
+    const char *kb, *vb;         // K and V of the head
+    const int64_t* pages;
+    int first, lo, hi;
+    bool fast;                   // pages hold a multiple of 16 tokens, and all of them exist
+    uint32_t own_k[PER16], own_v[2][PER16];      // fast: a lane's offset in a load of 16 keys
+
+    __device__ __forceinline__ DecLoads(const AttnArgs& a_, const char* k, const char* v, const int64_t* p)
+        : a(a_), kb(k), vb(v), pages(p) {
+        static_for<0, PER16>([&](auto i) {
+            constexpr int I = decltype(i)::value;
+            const int c = I * 64 + (threadIdx.x & 63), r = c / R::CH, pos = c % R::CH;
+            const uint32_t row = (uint32_t)(r * a.kv.slot_b);
+            own_k[I] = row + in_row((pos ^ R::swz_k(r)) * 16);
+            own_v[0][I] = row + in_row((pos ^ R::swz_v(r)) * 16);
+            own_v[1][I] = row + in_row((pos ^ R::swz_v(r + 16)) * 16);
+        });
     }
-    const int row_bytes = a.kv.dim * (KV8 ? 1 : 2);
-#pragma unroll
-    for (int i = 0; i < DEC_KEYS * R::CH / 64; ++i) {
-        const int c = i * 64 + lane, r = c / R::CH, pos = c % R::CH;
-        const int64_t o = shfl64(off, r);
-        int ck = (pos ^ R::swz_k(r)) * 16, cv = (pos ^ R::swz_v(r)) * 16;
-        if (ck >= row_bytes) ck = 0;
-        if (cv >= row_bytes) cv = 0;
-        global_to_lds16(kb + o + ck, dst + i * 1024);
-        global_to_lds16(vb + o + cv, dst + D::HALF + i * 1024);
+    __device__ __forceinline__ int in_row(int from) const {      // (dim below DP: any bytes of the row)
+        return from >= a.kv.dim * (KV8 ? 1 : 2) ? 0 : from;
     }
-    return mask;
-}
+
+    // Issues the loads of key tile `tile`; returns which of its 32 keys exist.
+    // Keys that do not exist are staged as copies of one that does (their weight
+    // is zero), so that the count of loads is fixed.
+    __device__ __forceinline__ uint32_t issue(int tile, MPDT_LDS char* dst) const {
+        const int key0 = tile * DEC_KEYS;
+        if (fast && key0 >= lo && key0 + DEC_KEYS <= hi) {
+            // 16 keys lie in one page: scalar addresses
+            static_for<0, 2>([&](auto gc) {
+                constexpr int G = decltype(gc)::value;
+                const int key = key0 + 16 * G, pi = a.kv.page_of(key);
+                const int64_t e = pages[pi - first];
+                const int64_t pg = (int64_t)((uint64_t)(uint32_t)uni((int)(e >> 32)) << 32 | (uint32_t)uni((int)e)) +
+                                   (key - pi * a.kv.page_size) * a.kv.slot_b;
+                static_for<0, PER16>([&](auto i) {
+                    constexpr int I = decltype(i)::value;
+                    MPDT_LDS char* to = dst + (G * PER16 + I) * 1024;
+                    global_to_lds16<true>(kb + pg, own_k[I], to);
+                    global_to_lds16<true>(vb + pg, own_v[G][I], to + D::HALF);
+                });
+            });
+            return 0xffffffffu;
+        }
+        const int lane = threadIdx.x & 63;
+        int64_t off;
+        const bool ok = key_offset(a.kv, pages, first, key0 + (lane & 31), lo, hi, off);
+        const uint32_t mask = (uint32_t)__ballot(ok);
+        if (mask != 0xffffffffu) {
+            const int64_t other = shfl64(off, mask ? __builtin_ctz(mask) : 0);
+            if (!ok) off = other;
+        }
+#pragma unroll 1
+        for (int i = 0; i < 2 * PER16; ++i) {
+            const int c = i * 64 + lane, r = c / R::CH, pos = c % R::CH;
+            const int64_t o = shfl64(off, r);
+            global_to_lds16(kb + o + in_row((pos ^ R::swz_k(r)) * 16), dst + i * 1024);
+            global_to_lds16(vb + o + in_row((pos ^ R::swz_v(r)) * 16), dst + D::HALF + i * 1024);
+        }
+        return mask;
+    }
+};
 
 template <class E, class EP, bool KV8, int DP, bool CAP>
 __device__ __forceinline__ void dec_tile(const MPDT_LDS char* st, const u32x4 (&qf)[DP / 32], const Score& sc,
@@ -509,21 +576,48 @@ __device__ __forceinline__ void dec_tile(const MPDT_LDS char* st, const u32x4 (&
     using D = Dec<E, KV8, DP>;
     using R = typename D::R;
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    // All of K's operands are asked for before the first MFMA, and all of V's
+    // before the softmax (left to itself the compiler asks for one, waits out
+    // the LDS latency, and uses it).
     f32x4 s[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+    u32x4 kf[2][DP / 32];
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-        const int r = 16 * ks + n;
+    for (int d = 0; d < DP / 32; ++d)
 #pragma unroll
-        for (int d = 0; d < DP / 32; ++d) {
-            u32x4 kf;
+        for (int ks = 0; ks < 2; ++ks) {
+            const int r = 16 * ks + n;
             if constexpr (KV8) {
-                kf = widen8<E>(lds_load8(st, r * R::BYTES + ((2 * d + (g >> 1)) ^ R::swz_k(r)) * 16 + (g & 1) * 8));
+                const u32x2 w = lds_load8(st, r * R::BYTES + ((2 * d + (g >> 1)) ^ R::swz_k(r)) * 16 + (g & 1) * 8);
+                kf[ks][d][0] = w[0];
+                kf[ks][d][1] = w[1];
             } else {
-                kf = lds_load16(st, r * R::BYTES + ((4 * d + g) ^ R::swz_k(r)) * 16);
+                kf[ks][d] = lds_load16(st, r * R::BYTES + ((4 * d + g) ^ R::swz_k(r)) * 16);
             }
-            s[ks] = E::mma16(kf, qf[d], s[ks]);
+        }
+    const MPDT_LDS char* sv = st + D::HALF;
+    u32x4 vf[DP / 16];
+#pragma unroll
+    for (int t = 0; t < DP / 16; ++t) {
+        if constexpr (KV8) {
+            const int h = n >> 1, r = (h < 4 ? 4 * g + h : 16 + 4 * g + h - 4);
+            const u32x2 w = lds_read_tr8(sv, r * R::BYTES + (t ^ R::swz_v(r)) * 16 + (n & 1) * 8);
+            vf[t][0] = w[0];
+            vf[t][1] = w[1];
+        } else {
+            const int r = 4 * g + (n >> 2), c = 2 * t + ((n & 3) >> 1), b = (n & 1) * 8;
+            const u32x2 v0 = lds_read_tr16(sv, r * R::BYTES + (c ^ R::swz_v(r)) * 16 + b);
+            const u32x2 v1 = lds_read_tr16(sv, (r + 16) * R::BYTES + (c ^ R::swz_v(r + 16)) * 16 + b);
+            vf[t] = u32x4{v0[0], v0[1], v1[0], v1[1]};
         }
     }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            if constexpr (KV8) s[ks] = E::mma16(widen8<E>(u32x2{kf[ks][d][0], kf[ks][d][1]}), qf[d], s[ks]);
+            else s[ks] = E::mma16(kf[ks][d], qf[d], s[ks]);
+        }
     float x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = score<CAP>(sc, s[i >> 2][i & 3]);
@@ -554,20 +648,10 @@ __device__ __forceinline__ void dec_tile(const MPDT_LDS char* st, const u32x4 (&
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) p[i] = EP::pack(x[2 * i], x[2 * i + 1]);
-    const MPDT_LDS char* sv = st + D::HALF;
 #pragma unroll
     for (int t = 0; t < DP / 16; ++t) {
-        u32x4 vf;
-        if constexpr (KV8) {
-            const int h = n >> 1, r = (h < 4 ? 4 * g + h : 16 + 4 * g + h - 4);
-            vf = widen8<EP>(lds_read_tr8(sv, r * R::BYTES + (t ^ R::swz_v(r)) * 16 + (n & 1) * 8));
-        } else {
-            const int r = 4 * g + (n >> 2), c = 2 * t + ((n & 3) >> 1), b = (n & 1) * 8;
-            const u32x2 v0 = lds_read_tr16(sv, r * R::BYTES + (c ^ R::swz_v(r)) * 16 + b);
-            const u32x2 v1 = lds_read_tr16(sv, (r + 16) * R::BYTES + (c ^ R::swz_v(r + 16)) * 16 + b);
-            vf = u32x4{v0[0], v0[1], v1[0], v1[1]};
-        }
-        o[t] = EP::mma16(vf, p, o[t]);
+        if constexpr (KV8) o[t] = EP::mma16(widen8<EP>(u32x2{vf[t][0], vf[t][1]}), p, o[t]);
+        else o[t] = EP::mma16(vf[t], p, o[t]);
     }
 }
 
@@ -588,9 +672,7 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void attn_decode_kernel(AttnArgs a)
     int worker = 0, line = 0, entries = 0, e = 0, h = 0;
     int b, r0, t0, tiles;
     if constexpr (DIRECT) {
-        find_entry<DEC_WAVES>(a, blockIdx.x, red, box);
-        b = uni(box[0]);
-        r0 = uni(box[1]);
+        find_entry<DEC_WAVES>(a, blockIdx.x, red, box, b, r0);
         h = blockIdx.y;
         if (b < 0) return;
         at = 0;
@@ -658,22 +740,25 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void attn_decode_kernel(AttnArgs a)
         // rows of this tile see every key below `all_hi` and from `all_lo` on
         const int all_hi = s.n - s.nq + r0 / a.group + 1;
         const int all_lo = a.window > 0 ? s.n - s.nq + (r1 - 1) / a.group - a.window + 1 : 0;
+        DecLoads<E, KV8, DP> loads(a, kb, vb, pages);
+        loads.lo = kr.lo;
+        loads.hi = kr.hi;
         float ref = NO_MAX, sum = 0.0f;
         f32x4 o[DP / 16];
 #pragma unroll
         for (int t = 0; t < DP / 16; ++t) o[t] = f32x4{0, 0, 0, 0};
 
         for (int pos = seg_a; pos < seg_e;) {
-            int first;
-            const int upto = fetch_pages<64 * DEC_WAVES, DEC_KEYS>(a, b, t0 + pos, t0 + seg_e, pages, first) - t0;
+            bool clean;
+            const int upto = fetch_pages<64 * DEC_WAVES, DEC_KEYS>(a, b, t0 + pos, t0 + seg_e, pages, loads.first,
+                                                                   &clean) - t0;
+            loads.fast = clean && a.kv.page_size % 16 == 0;
             uint32_t mask[D::NST];
 #pragma unroll
             for (int i = 0; i < D::NST - 1; ++i) {
                 const int j = pos + wave + i * DEC_WAVES;
                 mask[i] = 0;
-                if (j < upto)
-                    mask[i] = dec_issue<E, KV8, DP>(a, kb, vb, pages, first, t0 + j, kr.lo, kr.hi,
-                                                    ring + i * D::STAGE);
+                if (j < upto) mask[i] = loads.issue(t0 + j, ring + i * D::STAGE);
             }
             int slot = 0;
             for (int j = pos + wave; j < upto; j += DEC_WAVES) {
@@ -683,8 +768,7 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void attn_decode_kernel(AttnArgs a)
                 mask[D::NST - 1] = 0;
                 wait_lds();      // the last tile's reads of that stage have come back
                 if (ahead < upto) {
-                    mask[D::NST - 1] = dec_issue<E, KV8, DP>(a, kb, vb, pages, first, t0 + ahead, kr.lo, kr.hi,
-                                                             ring + fill * D::STAGE);
+                    mask[D::NST - 1] = loads.issue(t0 + ahead, ring + fill * D::STAGE);
                     wait_vmem<(D::NST - 1) * D::LOADS>();
                 } else {
                     wait_vmem<0>();
