@@ -279,48 +279,57 @@ __device__ __forceinline__ int block_scan(int x, int* red, int& total) {
     return base + s - x;
 }
 
-__global__ __launch_bounds__(1024) void attn_plan_kernel(AttnArgs a, int key_tile) {
-    __shared__ int red[16];
+template <int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void attn_plan_kernel(AttnArgs a, int key_tile) {
+    constexpr int NT = 64 * WAVES;
+    __shared__ int red[WAVES], first_near[NT];
+    __shared__ Seq seq_near[NT];
+    // (up to NT sequences their numbers stay in LDS: a second round trip to
+    // memory costs more than the rest of the plan)
+    const bool near = a.sv.seqs <= NT;
     Plan p;
     plan_layout(a.ws, a.entries, a.sv.seqs, a.workers, a.tile_rows, 0, &p);
     int run = 0;
-    for (int b0 = 0; b0 < a.sv.seqs; b0 += 1024) {
+    for (int b0 = 0; b0 < a.sv.seqs; b0 += NT) {
         const int b = b0 + threadIdx.x;
         int c = 0;
         if (b < a.sv.seqs) {
             const Seq s = seq_of(a.sv, a.kv.page_size, b);
             c = (int)(((int64_t)s.nq * a.group + a.tile_rows - 1) / a.tile_rows);
+            if (near) seq_near[b] = s;
         }
         int total;
-        const int at = run + block_scan<16>(c, red, total);
-        if (b < a.sv.seqs) p.first[b] = at;
+        const int at = run + block_scan<WAVES>(c, red, total);
+        if (b < a.sv.seqs) {
+            if (near) first_near[b] = at;
+            else p.first[b] = at;
+        }
         run += total;
     }
     const int entries = min(run, a.entries);
-    if (threadIdx.x == 0) p.first[a.sv.seqs] = run;
     if (threadIdx.x < 4) reinterpret_cast<int32_t*>(p.zeros)[threadIdx.x] = 0;
     __syncthreads();
     int tiles = 0;
-    for (int e0 = 0; e0 < entries; e0 += 1024) {
+    for (int e0 = 0; e0 < entries; e0 += NT) {
         const int e = e0 + threadIdx.x;
         int c = 0;
         i32x4 ent{0, 0, 0, 0};
         if (e < entries) {
-            int lo = 0, hi = a.sv.seqs;      // first[lo] <= e < first[hi]
+            int lo = 0, hi = a.sv.seqs;      // the last sequence whose first row tile is at most e
             while (hi - lo > 1) {
                 const int mid = (lo + hi) / 2;
-                if (p.first[mid] <= e) lo = mid;
+                if ((near ? first_near[mid] : p.first[mid]) <= e) lo = mid;
                 else hi = mid;
             }
-            const Seq s = seq_of(a.sv, a.kv.page_size, lo);
-            const int r0 = (e - p.first[lo]) * a.tile_rows;
+            const Seq s = near ? seq_near[lo] : seq_of(a.sv, a.kv.page_size, lo);
+            const int r0 = (e - (near ? first_near[lo] : p.first[lo])) * a.tile_rows;
             const Span32 k = keys_of(s, a.group, a.window, r0, min(r0 + a.tile_rows, s.nq * a.group));
             const int t0 = k.lo / key_tile;
             c = max((k.hi + key_tile - 1) / key_tile - t0, 1);
             ent = i32x4{lo, r0, t0, c};
         }
         int total;
-        const int at = tiles + block_scan<16>(c, red, total);
+        const int at = tiles + block_scan<WAVES>(c, red, total);
         if (e < entries) {
             p.entry[e] = ent;
             p.before[e] = at;
@@ -349,14 +358,16 @@ __device__ __forceinline__ int worker_id() {
 // Row tile `e` of a batch without a plan: all threads of the workgroup look
 // for the sequence that holds it (-1: none) and the tile's first row.
 template <int WAVES>
-__device__ __forceinline__ void find_entry(const AttnArgs& a, int e, int* red, int* box, int& b, int& r0) {
+__device__ __forceinline__ void find_entry(const AttnArgs& a, int e, int* red, int* box, int& b, int& r0,
+                                           Seq& s) {
     if (a.sv.seqs <= 64) {
         // every wave for itself: one sequence a lane
         const int lane = threadIdx.x & 63;
         int c = 0;
+        Seq mine{0, 0, 0};
         if (lane < a.sv.seqs) {
-            const Seq s = seq_of(a.sv, a.kv.page_size, lane);
-            c = (int)(((int64_t)s.nq * a.group + a.tile_rows - 1) / a.tile_rows);
+            mine = seq_of(a.sv, a.kv.page_size, lane);
+            c = (int)(((int64_t)mine.nq * a.group + a.tile_rows - 1) / a.tile_rows);
         }
         int upto = c;
 #pragma unroll
@@ -366,7 +377,10 @@ __device__ __forceinline__ void find_entry(const AttnArgs& a, int e, int* red, i
         }
         const uint64_t in = __ballot(e >= upto - c && e < upto);
         b = in ? __builtin_ctzll(in) : -1;
-        r0 = in ? (e - __builtin_amdgcn_readlane(upto - c, b)) * a.tile_rows : 0;
+        if (!in) return;
+        r0 = (e - __builtin_amdgcn_readlane(upto - c, b)) * a.tile_rows;
+        s = Seq{__builtin_amdgcn_readlane(mine.start, b), __builtin_amdgcn_readlane(mine.nq, b),
+                __builtin_amdgcn_readlane(mine.n, b)};
         return;
     }
     if (threadIdx.x == 0) box[0] = -1;
@@ -391,6 +405,7 @@ __device__ __forceinline__ void find_entry(const AttnArgs& a, int e, int* red, i
     __syncthreads();
     b = uni(box[0]);
     r0 = uni(box[1]);
+    if (b >= 0) s = uniform_seq(a.sv, a.kv.page_size, b);
 }
 
 // The byte offsets of the pages that hold the keys from key tile `tile` on,
@@ -485,14 +500,16 @@ __device__ __forceinline__ float lse_of(float ref, float sum) {
 
 // ---- few rows: 16 rows by 32 keys a wave ----------------------------------------
 
-constexpr int DEC_WAVES = 4, DEC_ROWS = 16, DEC_KEYS = 32;
+constexpr int DEC_ROWS = 16, DEC_KEYS = 32;
+constexpr int DEC_LDS = 128 * 1024;       // rings of a workgroup
 
-template <class E, bool KV8, int DP>
+// WAVES: 4, or 8 for a workgroup that has a unit to itself.
+template <bool KV8, int DP, int WAVES>
 struct Dec {
     using R = Rows<DP, KV8, 16>;
     static constexpr int HALF = DEC_KEYS * R::BYTES;         // K rows, then V rows
     static constexpr int STAGE = 2 * HALF;
-    static constexpr int NST = KV8 && DP <= 64 ? 4 : (KV8 || DP <= 64 ? 3 : 2);
+    static constexpr int FIT = DEC_LDS / (WAVES * STAGE), NST = FIT > 4 ? 4 : FIT;
     static constexpr int LOADS = 2 * DEC_KEYS * R::CH / 64;  // direct loads of a stage
     static constexpr int RING = NST * STAGE;
     static constexpr int OROW = DP * 4 + 16;                 // bytes of a row of outputs in LDS
@@ -501,9 +518,9 @@ struct Dec {
 };
 
 // A wave's loads of its key tiles.
-template <class E, bool KV8, int DP>
+template <bool KV8, int DP, int WAVES>
 struct DecLoads {
-    using D = Dec<E, KV8, DP>;
+    using D = Dec<KV8, DP, WAVES>;
     using R = typename D::R;
     static constexpr int PER16 = R::CH / 4;      // loads of 16 keys, K or V
     const AttnArgs& a;
@@ -569,11 +586,11 @@ struct DecLoads {
     }
 };
 
-template <class E, class EP, bool KV8, int DP, bool CAP>
+template <class E, class EP, bool KV8, int DP, bool CAP, int WAVES>
 __device__ __forceinline__ void dec_tile(const MPDT_LDS char* st, const u32x4 (&qf)[DP / 32], const Score& sc,
                                          uint32_t mask, bool edge, int key0, int qpos, int qlow, float& ref,
                                          float& sum, f32x4 (&o)[DP / 16]) {
-    using D = Dec<E, KV8, DP>;
+    using D = Dec<KV8, DP, WAVES>;
     using R = typename D::R;
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     // All of K's operands are asked for before the first MFMA, and all of V's
@@ -657,12 +674,13 @@ __device__ __forceinline__ void dec_tile(const MPDT_LDS char* st, const u32x4 (&
 
 // DIRECT: one workgroup to a unit, no plan and no joining.
 template <class E, class EP, bool KV8, int DP, bool CAP, bool DIRECT>
-__global__ __launch_bounds__(64 * DEC_WAVES) void attn_decode_kernel(AttnArgs a) {
-    using D = Dec<E, KV8, DP>;
-    __shared__ __attribute__((aligned(1024))) char smem[DEC_WAVES * D::RING];
+__global__ __launch_bounds__(64 * (DIRECT ? 8 : 4)) void attn_decode_kernel(AttnArgs a) {
+    constexpr int WAVES = DIRECT ? 8 : 4;
+    using D = Dec<KV8, DP, WAVES>;
+    __shared__ __attribute__((aligned(1024))) char smem[WAVES * D::RING];
     __shared__ int64_t pages[PAGES_LDS];
-    __shared__ float ml[2][DEC_WAVES][DEC_ROWS];
-    __shared__ int red[DEC_WAVES], box[2];
+    __shared__ float ml[2][WAVES][DEC_ROWS];
+    __shared__ int red[WAVES], box[2];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 15, g = lane >> 4;
     MPDT_LDS char* ring = lds_cast(smem) + wave * D::RING;
@@ -671,8 +689,9 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void attn_decode_kernel(AttnArgs a)
     int64_t at = 0, stop = 0, share = 1;
     int worker = 0, line = 0, entries = 0, e = 0, h = 0;
     int b, r0, t0, tiles;
+    Seq s;
     if constexpr (DIRECT) {
-        find_entry<DEC_WAVES>(a, blockIdx.x, red, box, b, r0);
+        find_entry<WAVES>(a, blockIdx.x, red, box, b, r0, s);
         h = blockIdx.y;
         if (b < 0) return;
         at = 0;
@@ -712,7 +731,7 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void attn_decode_kernel(AttnArgs a)
             seg_e = (int)min((int64_t)tiles, stop - u0);
             whole = seg_a == 0 && seg_e == tiles;
         }
-        const Seq s = uniform_seq(a.sv, a.kv.page_size, b);
+        if constexpr (!DIRECT) s = uniform_seq(a.sv, a.kv.page_size, b);
         const int rows = s.nq * a.group, r1 = min(r0 + DEC_ROWS, rows);
         const Span32 kr = keys_of(s, a.group, a.window, r0, r1);
         if constexpr (DIRECT) {
@@ -740,7 +759,7 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void attn_decode_kernel(AttnArgs a)
         // rows of this tile see every key below `all_hi` and from `all_lo` on
         const int all_hi = s.n - s.nq + r0 / a.group + 1;
         const int all_lo = a.window > 0 ? s.n - s.nq + (r1 - 1) / a.group - a.window + 1 : 0;
-        DecLoads<E, KV8, DP> loads(a, kb, vb, pages);
+        DecLoads<KV8, DP, WAVES> loads(a, kb, vb, pages);
         loads.lo = kr.lo;
         loads.hi = kr.hi;
         float ref = NO_MAX, sum = 0.0f;
@@ -750,20 +769,20 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void attn_decode_kernel(AttnArgs a)
 
         for (int pos = seg_a; pos < seg_e;) {
             bool clean;
-            const int upto = fetch_pages<64 * DEC_WAVES, DEC_KEYS>(a, b, t0 + pos, t0 + seg_e, pages, loads.first,
+            const int upto = fetch_pages<64 * WAVES, DEC_KEYS>(a, b, t0 + pos, t0 + seg_e, pages, loads.first,
                                                                    &clean) - t0;
             loads.fast = clean && a.kv.page_size % 16 == 0;
             uint32_t mask[D::NST];
 #pragma unroll
             for (int i = 0; i < D::NST - 1; ++i) {
-                const int j = pos + wave + i * DEC_WAVES;
+                const int j = pos + wave + i * WAVES;
                 mask[i] = 0;
                 if (j < upto) mask[i] = loads.issue(t0 + j, ring + i * D::STAGE);
             }
             int slot = 0;
-            for (int j = pos + wave; j < upto; j += DEC_WAVES) {
+            for (int j = pos + wave; j < upto; j += WAVES) {
                 // the stage freed by the last tile takes the loads of the one NST - 1 on
-                const int ahead = j + (D::NST - 1) * DEC_WAVES;
+                const int ahead = j + (D::NST - 1) * WAVES;
                 const int fill = slot == 0 ? D::NST - 1 : slot - 1;
                 mask[D::NST - 1] = 0;
                 wait_lds();      // the last tile's reads of that stage have come back
@@ -778,7 +797,7 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void attn_decode_kernel(AttnArgs a)
                 const int key0 = (t0 + j) * DEC_KEYS;
                 if (mask[0]) {
                     const bool edge = mask[0] != 0xffffffffu || key0 + DEC_KEYS > all_hi || key0 < all_lo;
-                    dec_tile<E, EP, KV8, DP, CAP>(ring + slot * D::STAGE, qf, sc, mask[0], edge, key0, qpos, qlow,
+                    dec_tile<E, EP, KV8, DP, CAP, WAVES>(ring + slot * D::STAGE, qf, sc, mask[0], edge, key0, qpos, qlow,
                                                   ref, sum, o);
                 }
                 __atomic_signal_fence(__ATOMIC_SEQ_CST);
@@ -803,13 +822,13 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void attn_decode_kernel(AttnArgs a)
             ml[1][wave][n] = sum;
         }
         __syncthreads();
-        {
+        if (tid < 16 * DEC_ROWS) {
             const int rr = tid >> 4, dc = tid & 15;
-            float top = NO_MAX, den = 0.0f, w[DEC_WAVES];
+            float top = NO_MAX, den = 0.0f, w[WAVES];
 #pragma unroll
-            for (int i = 0; i < DEC_WAVES; ++i) top = fmaxf(top, ml[0][i][rr]);
+            for (int i = 0; i < WAVES; ++i) top = fmaxf(top, ml[0][i][rr]);
 #pragma unroll
-            for (int i = 0; i < DEC_WAVES; ++i) {
+            for (int i = 0; i < WAVES; ++i) {
                 w[i] = __builtin_amdgcn_exp2f(ml[0][i][rr] - top);
                 den += w[i] * ml[1][i][rr];
             }
@@ -822,7 +841,7 @@ __global__ __launch_bounds__(64 * DEC_WAVES) void attn_decode_kernel(AttnArgs a)
                 if (d >= DP) break;
                 f32x4 v{0, 0, 0, 0};
 #pragma unroll
-                for (int i = 0; i < DEC_WAVES; ++i)
+                for (int i = 0; i < WAVES; ++i)
                     v += w[i] * __builtin_bit_cast(f32x4, lds_load16(lds_cast(smem) + i * D::RING,
                                                                      rr * D::OROW + d * 4));
                 if (whole) {
@@ -895,6 +914,65 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
     for (int k = 0; k < (DP + 63) / 64; ++k)
         if (4 * dc + 64 * k < a.kv.dim) store_out4(a, orow, 4 * dc + 64 * k, v[k] * inv);
     if (dc == 0 && a.lse) a.lse[(int64_t)(s.start + tok) * a.lse_tok + qh] = lse_of(top, den);
+}
+
+// The same for units of few rows over many workers: one workgroup to a row,
+// eight groups of 32 threads take every eighth worker, and the eight sums are
+// joined in order.
+template <int DP>
+__global__ __launch_bounds__(256) void attn_join_few_kernel(AttnArgs a) {
+    __shared__ f32x4 part[8][DP / 4];
+    __shared__ float sums[8], tops[8];
+    Plan p;
+    plan_layout(a.ws, a.entries, a.sv.seqs, a.workers, a.tile_rows, DP, &p);
+    const int e = blockIdx.x, h = blockIdx.y, rr = blockIdx.z, grp = threadIdx.x >> 5, dc = threadIdx.x & 31;
+    if (e >= p.head[0]) return;
+    const int line = p.head[1];
+    const i32x4 ent = p.entry[e];
+    const int64_t u0 = (int64_t)h * line + p.before[e], u1 = u0 + ent[3];
+    const int64_t share = share_of(a, (int64_t)line * a.kv.kv_heads);
+    const int w0 = (int)(u0 / share), w1 = (int)((u1 - 1) / share);
+    if (w0 == w1) return;
+    const Seq s = seq_of(a.sv, a.kv.page_size, ent[0]);
+    const int row = ent[1] + rr;
+    if (row >= s.nq * a.group) return;
+    float top = NO_MAX, den = 0.0f;
+    f32x4 v{0, 0, 0, 0};
+#pragma unroll 4
+    for (int w = w0 + grp; w <= w1; w += 8) {
+        const int64_t sr = ((int64_t)w * 2 + (w * share >= u0 ? 0 : 1)) * a.tile_rows + rr;
+        const f32x2 ml = p.part_ml[sr];
+        f32x4 x{0, 0, 0, 0};
+        if (4 * dc < DP) x = *reinterpret_cast<const f32x4*>(p.part_o + sr * DP + 4 * dc);
+        const float to = fmaxf(top, ml[0]), f0 = __builtin_amdgcn_exp2f(top - to), f1 = __builtin_amdgcn_exp2f(ml[0] - to);
+        v = v * f0 + x * f1;
+        den = den * f0 + ml[1] * f1;
+        top = to;
+    }
+    if (4 * dc < DP) part[grp][dc] = v;
+    if (dc == 0) {
+        tops[grp] = top;
+        sums[grp] = den;
+    }
+    __syncthreads();
+    if (grp != 0) return;
+    float all = tops[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) all = fmaxf(all, tops[i]);
+    den = 0.0f;
+    v = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float f = __builtin_amdgcn_exp2f(tops[i] - all);
+        den += f * sums[i];
+        if (4 * dc < DP) v += part[i][dc] * f;
+    }
+    const int tok = row / a.group, qh = h * a.group + row % a.group;
+    const float inv = (den > 0.0f || den != den ? 1.0f / den : 0.0f) *
+                      (a.kv.type == DT_E4M3 ? a.kv.v_scale[h] : 1.0f);
+    if (4 * dc < a.kv.dim)
+        store_out4(a, a.out + (int64_t)(s.start + tok) * a.o_tok_b + qh * a.o_head_b, 4 * dc, v * inv);
+    if (dc == 0 && a.lse) a.lse[(int64_t)(s.start + tok) * a.lse_tok + qh] = lse_of(all, den);
 }
 
 // ---- many rows: 256 rows by 64 keys a workgroup ------------------------------------
@@ -1456,14 +1534,19 @@ hipError_t launch_as(const AttnArgs& a, const Shape& s, hipStream_t stream) {
     hipError_t err;
     if (s.direct) {
         hipLaunchKernelGGL((attn_decode_kernel<E, EP, KV8, DP, CAP, true>),
-                           dim3((unsigned)s.entries, (unsigned)a.kv.kv_heads), dim3(64 * DEC_WAVES), 0, stream, a);
+                           dim3((unsigned)s.entries, (unsigned)a.kv.kv_heads), dim3(512), 0, stream, a);
         return hipGetLastError();
     }
-    hipLaunchKernelGGL(attn_plan_kernel, dim3(1), dim3(1024), 0, stream, a, s.key_tile);
+    // (one wave's scans need no barrier to wait at)
+    if (s.entries <= 64 && a.sv.seqs <= 64) {
+        hipLaunchKernelGGL(attn_plan_kernel<1>, dim3(1), dim3(64), 0, stream, a, s.key_tile);
+    } else {
+        hipLaunchKernelGGL(attn_plan_kernel<16>, dim3(1), dim3(1024), 0, stream, a, s.key_tile);
+    }
     if ((err = hipGetLastError()) != hipSuccess) return err;
     if (s.few) {
         hipLaunchKernelGGL((attn_decode_kernel<E, EP, KV8, DP, CAP, false>), dim3((unsigned)s.workers),
-                           dim3(64 * DEC_WAVES), 0, stream, a);
+                           dim3(256), 0, stream, a);
     } else if (a.kv.page_size % 16 == 0) {
         hipLaunchKernelGGL((attn_chunk_kernel<E, EP, KV8, DP, CAP, true>), dim3((unsigned)s.workers),
                            dim3(64 * CHK_WAVES), 0, stream, a);
@@ -1472,6 +1555,14 @@ hipError_t launch_as(const AttnArgs& a, const Shape& s, hipStream_t stream) {
                            dim3(64 * CHK_WAVES), 0, stream, a);
     }
     if ((err = hipGetLastError()) != hipSuccess) return err;
+    // a workgroup to a row only where units are cut into several pieces: 64
+    // sequences of 8 heads (0.4 pieces a unit) 9.7 us, 16 rows to a workgroup
+    // 5.5; 8 long sequences (32 pieces) 4.3 us against 8.7
+    if (s.few && s.workers >= 2 * (int64_t)s.entries * a.kv.kv_heads) {
+        hipLaunchKernelGGL((attn_join_few_kernel<DP>), dim3((unsigned)s.entries, (unsigned)a.kv.kv_heads, DEC_ROWS),
+                           dim3(256), 0, stream, a);
+        return hipGetLastError();
+    }
     hipLaunchKernelGGL((attn_join_kernel<DP>), dim3((unsigned)s.entries, (unsigned)a.kv.kv_heads, s.tile_rows / 16),
                        dim3(256), 0, stream, a);
     return hipGetLastError();
