@@ -230,6 +230,7 @@ struct Plan {
     int32_t* before;
     int32_t* first;     // row tiles before a sequence
     char* zeros;        // 16 bytes
+    int32_t* cut;       // per worker: entry and head of the unit that it begins and leaves to others, or -1
     float* part_o;      // partial outputs, two slots to a worker
     f32x2* part_ml;     // their reference and sum
 };
@@ -248,6 +249,8 @@ __host__ __device__ inline int64_t plan_layout(char* ws, int entries, int seqs, 
     at += up256(((int64_t)entries + 1) * 4);
     p->first = (int32_t*)(ws + at);
     at += up256(((int64_t)seqs + 1) * 4);
+    p->cut = (int32_t*)(ws + at);
+    at += up256((int64_t)workers * 8);
     p->part_ml = (f32x2*)(ws + at);
     at += up256((int64_t)workers * 2 * tile_rows * 8);
     p->part_o = (float*)(ws + at);
@@ -705,7 +708,10 @@ __global__ __launch_bounds__(64 * (DIRECT ? 8 : 4)) void attn_decode_kernel(Attn
         worker = worker_id();
         at = worker * share;
         stop = min(at + share, total);
-        if (at >= stop) return;
+        if (at >= stop) {
+            if (tid == 0) p.cut[2 * worker] = -1;
+            return;
+        }
         h = (int)(at / line);
         const int rem = (int)(at - (int64_t)h * line);
         int lo = 0, hi = entries;
@@ -863,6 +869,10 @@ __global__ __launch_bounds__(64 * (DIRECT ? 8 : 4)) void attn_decode_kernel(Attn
         if constexpr (DIRECT) return;
         at += seg_e - seg_a;
         lead = false;
+        if (at >= stop && tid == 0) {
+            p.cut[2 * worker] = seg_a == 0 && seg_e < tiles ? e : -1;
+            p.cut[2 * worker + 1] = h;
+        }
         if (++e == entries) {
             e = 0;
             ++h;
@@ -871,19 +881,19 @@ __global__ __launch_bounds__(64 * (DIRECT ? 8 : 4)) void attn_decode_kernel(Attn
 }
 
 // Units that several workers share: their partial sums joined in the order of
-// the keys.  One workgroup to 16 rows of a unit.
+// the keys.  One workgroup to 16 rows of the unit that a worker leaves to others.
 template <int DP>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
     Plan p;
     plan_layout(a.ws, a.entries, a.sv.seqs, a.workers, a.tile_rows, DP, &p);
-    const int e = blockIdx.x, h = blockIdx.y, rr = blockIdx.z * 16 + (threadIdx.x >> 4), dc = threadIdx.x & 15;
-    if (e >= p.head[0]) return;
+    const int e = p.cut[2 * blockIdx.x], h = p.cut[2 * blockIdx.x + 1];
+    const int rr = blockIdx.y * 16 + (threadIdx.x >> 4), dc = threadIdx.x & 15;
+    if (e < 0) return;
     const int line = p.head[1];
     const i32x4 ent = p.entry[e];
     const int64_t u0 = (int64_t)h * line + p.before[e], u1 = u0 + ent[3];
     const int64_t share = share_of(a, (int64_t)line * a.kv.kv_heads);
-    const int w0 = (int)(u0 / share), w1 = (int)((u1 - 1) / share);
-    if (w0 == w1) return;
+    const int w0 = blockIdx.x, w1 = (int)((u1 - 1) / share);
     const Seq s = seq_of(a.sv, a.kv.page_size, ent[0]);
     const int row = ent[1] + rr;
     if (row >= s.nq * a.group) return;
@@ -925,14 +935,14 @@ __global__ __launch_bounds__(256) void attn_join_few_kernel(AttnArgs a) {
     __shared__ float sums[8], tops[8];
     Plan p;
     plan_layout(a.ws, a.entries, a.sv.seqs, a.workers, a.tile_rows, DP, &p);
-    const int e = blockIdx.x, h = blockIdx.y, rr = blockIdx.z, grp = threadIdx.x >> 5, dc = threadIdx.x & 31;
-    if (e >= p.head[0]) return;
+    const int e = p.cut[2 * blockIdx.x], h = p.cut[2 * blockIdx.x + 1];
+    const int rr = blockIdx.y, grp = threadIdx.x >> 5, dc = threadIdx.x & 31;
+    if (e < 0) return;
     const int line = p.head[1];
     const i32x4 ent = p.entry[e];
     const int64_t u0 = (int64_t)h * line + p.before[e], u1 = u0 + ent[3];
     const int64_t share = share_of(a, (int64_t)line * a.kv.kv_heads);
-    const int w0 = (int)(u0 / share), w1 = (int)((u1 - 1) / share);
-    if (w0 == w1) return;
+    const int w0 = blockIdx.x, w1 = (int)((u1 - 1) / share);
     const Seq s = seq_of(a.sv, a.kv.page_size, ent[0]);
     const int row = ent[1] + rr;
     if (row >= s.nq * a.group) return;
@@ -1289,7 +1299,10 @@ __global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(
     const int worker = worker_id();
     int64_t at = worker * share;
     const int64_t stop = min(at + share, total);
-    if (at >= stop) return;
+    if (at >= stop) {
+        if (tid == 0) p.cut[2 * worker] = -1;
+        return;
+    }
     int h = (int)(at / line), e;
     {
         const int rem = (int)(at - (int64_t)h * line);
@@ -1496,6 +1509,10 @@ __global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(
         }
         at += seg_e - seg_a;
         lead = false;
+        if (at >= stop && tid == 0) {
+            p.cut[2 * worker] = seg_a == 0 && seg_e < tiles ? e : -1;
+            p.cut[2 * worker + 1] = h;
+        }
         if (++e == entries) {
             e = 0;
             ++h;
@@ -1555,16 +1572,14 @@ hipError_t launch_as(const AttnArgs& a, const Shape& s, hipStream_t stream) {
                            dim3(64 * CHK_WAVES), 0, stream, a);
     }
     if ((err = hipGetLastError()) != hipSuccess) return err;
-    // a workgroup to a row only where units are cut into several pieces: 64
-    // sequences of 8 heads (0.4 pieces a unit) 9.7 us, 16 rows to a workgroup
-    // 5.5; 8 long sequences (32 pieces) 4.3 us against 8.7
+    // a workgroup to a row only where units are cut into several pieces: 8 long
+    // sequences of 8 heads (4 pieces a unit) 4.3 us, 16 rows to a workgroup 8.7;
+    // 64 sequences (0.5 pieces a unit) 9.7 us against 5.5
     if (s.few && s.workers >= 2 * (int64_t)s.entries * a.kv.kv_heads) {
-        hipLaunchKernelGGL((attn_join_few_kernel<DP>), dim3((unsigned)s.entries, (unsigned)a.kv.kv_heads, DEC_ROWS),
-                           dim3(256), 0, stream, a);
-        return hipGetLastError();
+        hipLaunchKernelGGL((attn_join_few_kernel<DP>), dim3((unsigned)s.workers, DEC_ROWS), dim3(256), 0, stream, a);
+    } else {
+        hipLaunchKernelGGL((attn_join_kernel<DP>), dim3((unsigned)s.workers, s.tile_rows / 16), dim3(256), 0, stream, a);
     }
-    hipLaunchKernelGGL((attn_join_kernel<DP>), dim3((unsigned)s.entries, (unsigned)a.kv.kv_heads, s.tile_rows / 16),
-                       dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 
