@@ -2,6 +2,8 @@
 shapes, types and strides before anything native is called, and the C ABI
 refuses wrong arguments on the host (or reports that there is no device)."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -266,9 +268,8 @@ def test_logprobs_abi():
 
 
 def test_every_declared_entry_point_is_exported():
-    import os
-    import re
-    text = open(os.path.join(os.path.dirname(mp.lib_path()), "..", "include", "mpdt_serving.h")).read()
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "include", "mpdt_serving.h")).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     names = set(re.findall(r"\b([a-z_][a-z0-9_]*)\s*\(", text))
     assert len(names) == 11
