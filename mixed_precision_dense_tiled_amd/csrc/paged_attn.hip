@@ -10,8 +10,9 @@
 // The work is cut into units (a tile of rows of one KV head; a row is one
 // token and one of the query heads that share the KV head) and each unit's
 // keys into tiles.  All tiles of all units stand in one line, which the
-// workgroups share evenly: a plan kernel writes the line down (lengths are
-// known on the device only), each workgroup walks its stretch with a running
+// workgroups share evenly: each works out the line for itself, or in large
+// batches a plan kernel writes it down (lengths are known on the device only),
+// each workgroup walks its stretch with a running
 // maximum and sum per row, and units that several workgroups share are joined
 // by a last kernel.  Batches whose cache rows are short run in one launch,
 // one workgroup to a unit.
@@ -226,6 +227,13 @@ __device__ __forceinline__ Span32 keys_of(const Seq& s, int group, int window, i
     return k;
 }
 
+// The unit that a worker begins and leaves to others (b < 0: none): what the
+// joining launch has to know.
+struct Cut {
+    int32_t b, h, r0, tiles;
+    int64_t u0, share;      // the unit's first tile in the line; tiles to a worker
+};
+
 // The plan in the workspace: head[0] entries (row tiles), head[1] key tiles
 // of all entries, then per entry {sequence, first row, first key tile, key
 // tiles} and the key tiles before it.  A KV head repeats the line once more.
@@ -235,7 +243,7 @@ struct Plan {
     int32_t* before;
     int32_t* first;     // row tiles before a sequence
     char* zeros;        // 16 bytes
-    int32_t* cut;       // per worker: entry and head of the unit that it begins and leaves to others, or -1
+    Cut* cut;           // per worker
     float* part_o;      // partial outputs, two slots to a worker
     f32x2* part_ml;     // their reference and sum
 };
@@ -254,8 +262,8 @@ __host__ __device__ inline int64_t plan_layout(char* ws, int entries, int seqs, 
     at += up256(((int64_t)entries + 1) * 4);
     p->first = (int32_t*)(ws + at);
     at += up256(((int64_t)seqs + 1) * 4);
-    p->cut = (int32_t*)(ws + at);
-    at += up256((int64_t)workers * 8);
+    p->cut = (Cut*)(ws + at);
+    at += up256((int64_t)workers * (int64_t)sizeof(Cut));
     p->part_ml = (f32x2*)(ws + at);
     at += up256((int64_t)workers * 2 * tile_rows * 8);
     p->part_o = (float*)(ws + at);
@@ -287,57 +295,48 @@ __device__ __forceinline__ int block_scan(int x, int* red, int& total) {
     return base + s - x;
 }
 
-template <int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void attn_plan_kernel(AttnArgs a, int key_tile) {
-    constexpr int NT = 64 * WAVES;
-    __shared__ int red[WAVES], first_near[NT];
-    __shared__ Seq seq_near[NT];
-    // (up to NT sequences their numbers stay in LDS: a second round trip to
-    // memory costs more than the rest of the plan)
-    const bool near = a.sv.seqs <= NT;
+// Entry e of sequence b, its first key tile and key tiles.
+__device__ __forceinline__ i32x4 entry_of(const AttnArgs& a, const Seq& s, int b, int r0, int key_tile) {
+    const Span32 k = keys_of(s, a.group, a.window, r0, min(r0 + a.tile_rows, s.nq * a.group));
+    const int t0 = k.lo / key_tile;
+    return i32x4{b, r0, t0, max((k.hi + key_tile - 1) / key_tile - t0, 1)};
+}
+
+__global__ __launch_bounds__(1024) void attn_plan_kernel(AttnArgs a, int key_tile) {
+    __shared__ int red[16];
     Plan p;
     plan_layout(a.ws, a.entries, a.sv.seqs, a.workers, a.tile_rows, 0, &p);
     int run = 0;
-    for (int b0 = 0; b0 < a.sv.seqs; b0 += NT) {
+    for (int b0 = 0; b0 < a.sv.seqs; b0 += 1024) {
         const int b = b0 + threadIdx.x;
         int c = 0;
         if (b < a.sv.seqs) {
             const Seq s = seq_of(a.sv, a.kv.page_size, b);
             c = (int)(((int64_t)s.nq * a.group + a.tile_rows - 1) / a.tile_rows);
-            if (near) seq_near[b] = s;
         }
         int total;
-        const int at = run + block_scan<WAVES>(c, red, total);
-        if (b < a.sv.seqs) {
-            if (near) first_near[b] = at;
-            else p.first[b] = at;
-        }
+        const int at = run + block_scan<16>(c, red, total);
+        if (b < a.sv.seqs) p.first[b] = at;
         run += total;
     }
     const int entries = min(run, a.entries);
-    if (threadIdx.x < 4) reinterpret_cast<int32_t*>(p.zeros)[threadIdx.x] = 0;
     __syncthreads();
     int tiles = 0;
-    for (int e0 = 0; e0 < entries; e0 += NT) {
+    for (int e0 = 0; e0 < entries; e0 += 1024) {
         const int e = e0 + threadIdx.x;
-        int c = 0;
         i32x4 ent{0, 0, 0, 0};
         if (e < entries) {
             int lo = 0, hi = a.sv.seqs;      // the last sequence whose first row tile is at most e
             while (hi - lo > 1) {
                 const int mid = (lo + hi) / 2;
-                if ((near ? first_near[mid] : p.first[mid]) <= e) lo = mid;
+                if (p.first[mid] <= e) lo = mid;
                 else hi = mid;
             }
-            const Seq s = near ? seq_near[lo] : seq_of(a.sv, a.kv.page_size, lo);
-            const int r0 = (e - (near ? first_near[lo] : p.first[lo])) * a.tile_rows;
-            const Span32 k = keys_of(s, a.group, a.window, r0, min(r0 + a.tile_rows, s.nq * a.group));
-            const int t0 = k.lo / key_tile;
-            c = max((k.hi + key_tile - 1) / key_tile - t0, 1);
-            ent = i32x4{lo, r0, t0, c};
+            const Seq s = seq_of(a.sv, a.kv.page_size, lo);
+            ent = entry_of(a, s, lo, (e - p.first[lo]) * a.tile_rows, key_tile);
         }
         int total;
-        const int at = tiles + block_scan<WAVES>(c, red, total);
+        const int at = tiles + block_scan<16>(ent[3], red, total);
         if (e < entries) {
             p.entry[e] = ent;
             p.before[e] = at;
@@ -349,6 +348,74 @@ __global__ __launch_bounds__(64 * WAVES) void attn_plan_kernel(AttnArgs a, int k
         p.head[0] = entries;
         p.head[1] = tiles;
     }
+}
+
+// The plan of a small batch, which every workgroup works out for itself in LDS
+// (at most NEAR sequences and entries): a launch of its own and the way of its
+// numbers through memory cost about 9 us before the first key is read.
+constexpr int NEAR = 256;
+struct NearPlan {
+    i32x4 entry[NEAR];
+    Seq seq[NEAR];
+    int before[NEAR + 1], first[NEAR];
+};
+
+// Plan as the workers see it.
+struct Line {
+    const NearPlan& near;
+    const Plan& far;
+    bool is_near;
+    int entries, tiles;
+    __device__ __forceinline__ i32x4 entry(int e) const {
+        const i32x4 x = is_near ? near.entry[e] : far.entry[e];
+        return i32x4{uni(x[0]), uni(x[1]), uni(x[2]), uni(x[3])};
+    }
+    __device__ __forceinline__ int before(int e) const { return uni(is_near ? near.before[e] : far.before[e]); }
+    // The entry that holds a tile.
+    __device__ __forceinline__ int find(int tile) const {
+        int lo = 0, hi = entries;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (before(mid) <= tile) lo = mid;
+            else hi = mid;
+        }
+        return lo;
+    }
+};
+
+template <int WAVES>
+__device__ __forceinline__ void make_line(const AttnArgs& a, int key_tile, NearPlan& n, int* red, Line& line) {
+    if (!line.is_near) {
+        line.entries = uni(line.far.head[0]);
+        line.tiles = uni(line.far.head[1]);
+        return;
+    }
+    const int t = threadIdx.x;
+    int c = 0, run, tiles;
+    if (t < a.sv.seqs) {
+        n.seq[t] = seq_of(a.sv, a.kv.page_size, t);
+        c = (int)(((int64_t)n.seq[t].nq * a.group + a.tile_rows - 1) / a.tile_rows);
+    }
+    const int at = block_scan<WAVES>(c, red, run);
+    if (t < a.sv.seqs) n.first[t] = at;
+    const int entries = min(run, a.entries);
+    __syncthreads();
+    i32x4 ent{0, 0, 0, 0};
+    if (t < entries) {
+        int lo = 0, hi = a.sv.seqs;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (n.first[mid] <= t) lo = mid;
+            else hi = mid;
+        }
+        ent = entry_of(a, n.seq[lo], lo, (t - n.first[lo]) * a.tile_rows, key_tile);
+        n.entry[t] = ent;
+    }
+    const int before = block_scan<WAVES>(ent[3], red, tiles);
+    if (t < entries) n.before[t] = before;
+    __syncthreads();
+    line.entries = uni(entries);
+    line.tiles = uni(tiles);
 }
 
 // Key tiles to a worker.
@@ -698,15 +765,17 @@ __global__ __launch_bounds__(64 * (DIRECT ? 8 : 4)) void attn_decode_kernel(Attn
     __shared__ int64_t pages[PAGES_LDS];
     __shared__ float ml[2][WAVES][DEC_ROWS];
     __shared__ int red[WAVES], box[2];
+    __shared__ NearPlan near;      // (not touched where DIRECT: no LDS then)
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 15, g = lane >> 4;
     MPDT_LDS char* ring = lds_cast(smem) + wave * D::RING;
 
     Plan p;
     int64_t at = 0, stop = 0, share = 1;
-    int worker = 0, line = 0, entries = 0, e = 0, h = 0;
+    int worker = 0, e = 0, h = 0;
     int b, r0, t0, tiles;
     Seq s;
+    Line line{near, p, a.near != 0, 0, 0};
     if constexpr (DIRECT) {
         find_entry<WAVES>(a, blockIdx.x, red, box, b, r0, s);
         h = blockIdx.y;
@@ -715,38 +784,31 @@ __global__ __launch_bounds__(64 * (DIRECT ? 8 : 4)) void attn_decode_kernel(Attn
         stop = 1;
     } else {
         plan_layout(a.ws, a.entries, a.sv.seqs, a.workers, a.tile_rows, DP, &p);
-        line = uni(p.head[1]);
-        entries = uni(p.head[0]);
-        const int64_t total = (int64_t)line * a.kv.kv_heads;
+        make_line<WAVES>(a, DEC_KEYS, near, red, line);
+        const int64_t total = (int64_t)line.tiles * a.kv.kv_heads;
         share = share_of(a, total);
         worker = worker_id();
         at = worker * share;
         stop = min(at + share, total);
         if (at >= stop) {
-            if (tid == 0) p.cut[2 * worker] = -1;
+            if (tid == 0) p.cut[worker].b = -1;
             return;
         }
-        h = (int)(at / line);
-        const int rem = (int)(at - (int64_t)h * line);
-        int lo = 0, hi = entries;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (uni(p.before[mid]) <= rem) lo = mid;
-            else hi = mid;
-        }
-        e = lo;
+        h = (int)(at / line.tiles);
+        e = line.find((int)(at - (int64_t)h * line.tiles));
     }
     bool lead = true;    // the first stretch of this workgroup
     while (at < stop) {
         int seg_a, seg_e;      // key tiles of this stretch within the unit
+        int64_t u0 = 0;
         bool whole = true;
         if constexpr (!DIRECT) {
-            const i32x4 ent = p.entry[e];
-            b = uni(ent[0]);
-            r0 = uni(ent[1]);
-            t0 = uni(ent[2]);
-            tiles = uni(ent[3]);
-            const int64_t u0 = (int64_t)h * line + uni(p.before[e]);
+            const i32x4 ent = line.entry(e);
+            b = ent[0];
+            r0 = ent[1];
+            t0 = ent[2];
+            tiles = ent[3];
+            u0 = (int64_t)h * line.tiles + line.before(e);
             seg_a = (int)(at - u0);
             seg_e = (int)min((int64_t)tiles, stop - u0);
             whole = seg_a == 0 && seg_e == tiles;
@@ -883,11 +945,8 @@ __global__ __launch_bounds__(64 * (DIRECT ? 8 : 4)) void attn_decode_kernel(Attn
         if constexpr (DIRECT) return;
         at += seg_e - seg_a;
         lead = false;
-        if (at >= stop && tid == 0) {
-            p.cut[2 * worker] = seg_a == 0 && seg_e < tiles ? e : -1;
-            p.cut[2 * worker + 1] = h;
-        }
-        if (++e == entries) {
+        if (at >= stop && tid == 0) p.cut[worker] = Cut{seg_a == 0 && seg_e < tiles ? b : -1, h, r0, tiles, u0, share};
+        if (++e == line.entries) {
             e = 0;
             ++h;
         }
@@ -900,16 +959,13 @@ template <int DP>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
     Plan p;
     plan_layout(a.ws, a.entries, a.sv.seqs, a.workers, a.tile_rows, DP, &p);
-    const int e = p.cut[2 * blockIdx.x], h = p.cut[2 * blockIdx.x + 1];
+    const Cut c = p.cut[blockIdx.x];
     const int rr = blockIdx.y * 16 + (threadIdx.x >> 4), dc = threadIdx.x & 15;
-    if (e < 0) return;
-    const int line = p.head[1];
-    const i32x4 ent = p.entry[e];
-    const int64_t u0 = (int64_t)h * line + p.before[e], u1 = u0 + ent[3];
-    const int64_t share = share_of(a, (int64_t)line * a.kv.kv_heads);
-    const int w0 = blockIdx.x, w1 = (int)((u1 - 1) / share);
-    const Seq s = seq_of(a.sv, a.kv.page_size, ent[0]);
-    const int row = ent[1] + rr;
+    if (c.b < 0) return;
+    const int h = c.h, w0 = blockIdx.x, w1 = (int)((c.u0 + c.tiles - 1) / c.share);
+    const int64_t u0 = c.u0, share = c.share;
+    const Seq s = seq_of(a.sv, a.kv.page_size, c.b);
+    const int row = c.r0 + rr;
     if (row >= s.nq * a.group) return;
     float top = NO_MAX;
     for (int w = w0; w <= w1; ++w) {
@@ -949,16 +1005,13 @@ __global__ __launch_bounds__(256) void attn_join_few_kernel(AttnArgs a) {
     __shared__ float sums[8], tops[8];
     Plan p;
     plan_layout(a.ws, a.entries, a.sv.seqs, a.workers, a.tile_rows, DP, &p);
-    const int e = p.cut[2 * blockIdx.x], h = p.cut[2 * blockIdx.x + 1];
+    const Cut c = p.cut[blockIdx.x];
     const int rr = blockIdx.y, grp = threadIdx.x >> 5, dc = threadIdx.x & 31;
-    if (e < 0) return;
-    const int line = p.head[1];
-    const i32x4 ent = p.entry[e];
-    const int64_t u0 = (int64_t)h * line + p.before[e], u1 = u0 + ent[3];
-    const int64_t share = share_of(a, (int64_t)line * a.kv.kv_heads);
-    const int w0 = blockIdx.x, w1 = (int)((u1 - 1) / share);
-    const Seq s = seq_of(a.sv, a.kv.page_size, ent[0]);
-    const int row = ent[1] + rr;
+    if (c.b < 0) return;
+    const int h = c.h, w0 = blockIdx.x, w1 = (int)((c.u0 + c.tiles - 1) / c.share);
+    const int64_t u0 = c.u0, share = c.share;
+    const Seq s = seq_of(a.sv, a.kv.page_size, c.b);
+    const int row = c.r0 + rr;
     if (row >= s.nq * a.group) return;
     float top = NO_MAX, den = 0.0f;
     f32x4 v{0, 0, 0, 0};
@@ -1302,37 +1355,33 @@ __global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(
     constexpr int DT = (DP + 31) / 32, NST = D::NST;
     __shared__ __attribute__((aligned(1024))) char smem[NST * D::STAGE];
     __shared__ int64_t pages[PAGES_LDS];
+    __shared__ int red[CHK_WAVES];
+    __shared__ NearPlan near;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 31, half = lane >> 5;
     const bool second = wave >= CHK_WAVES / 2;     // waves w and w + 4 share a SIMD
     MPDT_LDS char* lds = lds_cast(smem);
     Plan p;
     plan_layout(a.ws, a.entries, a.sv.seqs, a.workers, a.tile_rows, DP, &p);
-    const int line = uni(p.head[1]), entries = uni(p.head[0]);
-    const int64_t total = (int64_t)line * a.kv.kv_heads, share = share_of(a, total);
+    Line line{near, p, a.near != 0, 0, 0};
+    make_line<CHK_WAVES>(a, CHK_KEYS, near, red, line);
+    const int64_t total = (int64_t)line.tiles * a.kv.kv_heads, share = share_of(a, total);
     const int worker = worker_id();
     int64_t at = worker * share;
     const int64_t stop = min(at + share, total);
     if (at >= stop) {
-        if (tid == 0) p.cut[2 * worker] = -1;
+        if (tid == 0) p.cut[worker].b = -1;
         return;
     }
-    int h = (int)(at / line), e;
-    {
-        const int rem = (int)(at - (int64_t)h * line);
-        int lo = 0, hi = entries;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (uni(p.before[mid]) <= rem) lo = mid;
-            else hi = mid;
-        }
-        e = lo;
-    }
+    // 16 bytes of zeros for keys that do not exist (every worker writes the same)
+    if (tid < 4) reinterpret_cast<int32_t*>(p.zeros)[tid] = 0;
+    __syncthreads();
+    int h = (int)(at / line.tiles), e = line.find((int)(at - (int64_t)h * line.tiles));
     bool lead = true;
     while (at < stop) {
-        const i32x4 ent = p.entry[e];
-        const int b = uni(ent[0]), r0 = uni(ent[1]), t0 = uni(ent[2]), tiles = uni(ent[3]);
-        const int64_t u0 = (int64_t)h * line + uni(p.before[e]);
+        const i32x4 ent = line.entry(e);
+        const int b = ent[0], r0 = ent[1], t0 = ent[2], tiles = ent[3];
+        const int64_t u0 = (int64_t)h * line.tiles + line.before(e);
         const int seg_a = (int)(at - u0), seg_e = (int)min((int64_t)tiles, stop - u0);
         const bool whole = seg_a == 0 && seg_e == tiles;
         const Seq s = uniform_seq(a.sv, a.kv.page_size, b);
@@ -1523,11 +1572,8 @@ __global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(
         }
         at += seg_e - seg_a;
         lead = false;
-        if (at >= stop && tid == 0) {
-            p.cut[2 * worker] = seg_a == 0 && seg_e < tiles ? e : -1;
-            p.cut[2 * worker + 1] = h;
-        }
-        if (++e == entries) {
+        if (at >= stop && tid == 0) p.cut[worker] = Cut{seg_a == 0 && seg_e < tiles ? b : -1, h, r0, tiles, u0, share};
+        if (++e == line.entries) {
             e = 0;
             ++h;
         }
@@ -1568,12 +1614,7 @@ hipError_t launch_as(const AttnArgs& a, const Shape& s, hipStream_t stream) {
                            dim3((unsigned)s.entries, (unsigned)a.kv.kv_heads), dim3(512), 0, stream, a);
         return hipGetLastError();
     }
-    // (one wave's scans need no barrier to wait at)
-    if (s.entries <= 64 && a.sv.seqs <= 64) {
-        hipLaunchKernelGGL(attn_plan_kernel<1>, dim3(1), dim3(64), 0, stream, a, s.key_tile);
-    } else {
-        hipLaunchKernelGGL(attn_plan_kernel<16>, dim3(1), dim3(1024), 0, stream, a, s.key_tile);
-    }
+    if (!a.near) hipLaunchKernelGGL(attn_plan_kernel, dim3(1), dim3(1024), 0, stream, a, s.key_tile);
     if ((err = hipGetLastError()) != hipSuccess) return err;
     if (s.few) {
         hipLaunchKernelGGL((attn_decode_kernel<E, EP, KV8, DP, CAP, false>), dim3((unsigned)s.workers),
@@ -1628,6 +1669,7 @@ hipError_t launch_paged_attention(const AttnArgs& in, hipStream_t stream) {
     a.entries = s.entries;
     a.workers = s.workers;
     a.min_tiles = s.min_tiles;
+    a.near = a.sv.seqs <= NEAR && s.entries <= NEAR;
     const bool kv8 = a.kv.type == DT_E4M3;
     if (a.q_type == DT_BF16) {
         return kv8 ? launch_dim<Bf16, F16, true>(a, s, stream) : launch_dim<Bf16, Bf16, false>(a, s, stream);

@@ -60,6 +60,7 @@ struct AttnArgs {
     int entries;            // upper bound of the row tiles over all sequences
     int workers;            // workgroups that share the key tiles
     int min_tiles;          // fewest key tiles for a workgroup
+    int near;               // every workgroup plans for itself
 };
 int64_t attn_workspace(const AttnArgs& a);
 hipError_t launch_paged_attention(const AttnArgs& a, hipStream_t stream);

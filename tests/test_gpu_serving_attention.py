@@ -192,6 +192,24 @@ def test_cache_past_four_gib(gpu_ok):
     close(lse, z, tol_z, "lse")
 
 
+@pytest.mark.parametrize("kind", ["short", "long", "chunks"])
+def test_many_sequences(gpu_ok, kind):
+    """More sequences than a wave, a workgroup and a planning pass hold."""
+    if kind == "short":          # one launch
+        seqs, heads = [(1, i % 50) for i in range(1500)], 2
+    elif kind == "long":         # shared out over the card
+        seqs, heads = [(i % 2, i % 40) for i in range(1500)] + [(1, 3000), (1, 5)], 2
+    else:                        # 40 rows a sequence
+        seqs, heads = [(1, i % 40) for i in range(1100)] + [(9, 100)], 40
+    check(Batch(seqs, heads, 1, 16, 16, bf16, seed=31), kind)
+
+
+@pytest.mark.parametrize("n", [63, 64, 65, 255, 256, 257])
+def test_batches_around_the_plan_sizes(gpu_ok, n):
+    check(Batch([(1, 1 + 37 * i % 90) for i in range(n - 1)] + [(1, 2000)], 2, 1, 16, 16, f16, seed=n))
+    check(Batch([(3, 1 + 37 * i % 90) for i in range(n - 1)] + [(40, 700)], 16, 1, 16, 16, bf16, seed=n))
+
+
 def test_empty_batches(gpu_ok):
     b = Batch([(0, 5), (0, 0)], 4, 2, 64, 16)
     out, lse = mp.paged_attention(**b.gpu(), return_lse=True)
