@@ -530,6 +530,17 @@ __device__ __forceinline__ int64_t shfl64(int64_t v, int lane) {
     return (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo);
 }
 
+// The larger of this lane's value and that of the lane 32 (16) on: a swap of
+// register halves instead of a way through LDS.
+__device__ __forceinline__ float across32(float m) {
+    const u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(__float_as_uint(m), __float_as_uint(m), false, false));
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float across16(float m) {
+    const u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(__float_as_uint(m), __float_as_uint(m), false, false));
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
 // Bits first to last (both may lie outside 0 to 63) of a 64-bit word.
 __device__ __forceinline__ uint64_t from_to(int first, int last) {
     const uint64_t upto = last >= 63 ? ~0ull : last < 0 ? 0 : (2ull << last) - 1;
@@ -723,8 +734,7 @@ __device__ __forceinline__ void dec_tile(const MPDT_LDS char* st, const u32x4 (&
     float m = x[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) m = fmaxf(m, x[i]);
-    m = fmaxf(m, __shfl_xor(m, 16));
-    m = fmaxf(m, __shfl_xor(m, 32)) - EP::P_SHIFT;
+    m = across32(across16(m)) - EP::P_SHIFT;
     if (__ballot(m > ref + RESCALE)) {
         const float to = fmaxf(m, ref), f = __builtin_amdgcn_exp2f(ref - to);
         ref = to;
@@ -1192,12 +1202,13 @@ __device__ __forceinline__ void chk_weights(f32x16 (&s)[2], const Score& sc, uin
             }
     }
     const float mul = CAP ? 1.0f : sc.mul;       // positive
-    float m = s[0][0];
+    float m = s[0][0], m1 = s[1][0];            // (two chains)
 #pragma unroll
-    for (int i = 1; i < 16; ++i) m = fmaxf(m, s[0][i]);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) m = fmaxf(m, s[1][i]);
-    m = fmaxf(m, __shfl_xor(m, 32)) * mul - EP::P_SHIFT;
+    for (int i = 1; i < 16; ++i) {
+        m = fmaxf(m, s[0][i]);
+        m1 = fmaxf(m1, s[1][i]);
+    }
+    m = across32(fmaxf(m, m1)) * mul - EP::P_SHIFT;
     if (__ballot(m > ref + RESCALE)) {
         const float to = fmaxf(m, ref), f = __builtin_amdgcn_exp2f(ref - to);
         ref = to;
