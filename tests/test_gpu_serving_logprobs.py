@@ -31,8 +31,8 @@ def bounds(x):
     return base, rel
 
 
-def check(x, t, top=0):
-    r = mp.token_logprobs(x, t, top_k=top)
+def check(x, t, top=0, r=None):
+    r = mp.token_logprobs(x, t, top_k=top) if r is None else r
     lp, lse, ent, tv, ti = logprobs(x, t, top)
     base, rel = bounds(x)
     close(r.lse, lse, base, "lse")
@@ -47,8 +47,8 @@ def check(x, t, top=0):
     return r
 
 
-def check_grad(x, t, r, gl, ge, out=None):
-    got = mp.token_logprobs_backward(x, t, r.lse, r.entropy, gl, ge, out=out)
+def check_grad(x, t, r, gl, ge, out=None, got=None):
+    got = mp.token_logprobs_backward(x, t, r.lse, r.entropy, gl, ge, out=out) if got is None else got
     zero = torch.zeros(x.shape[0], device="cuda")
     gl, ge = zero if gl is None else gl, zero if ge is None else ge
     want = logprobs_grad(x, t, gl, ge)
@@ -178,6 +178,20 @@ def test_gradient_against_differences(gpu_ok):
     got = mp.token_logprobs_backward(xf, t.cuda(), r.lse, r.entropy, gl.cuda(), ge.cuda())
     # differences: h^2 times a third derivative of order 1, and 1e-16 / h; the kernel: FP32
     assert (got.cpu().double() - want).abs().max() < 1e-8 + 2e-6
+
+
+def test_more_logits_than_the_cache_holds(gpu_ok):
+    """Over 256 MB the gradient reads and writes past the caches."""
+    rows, vocab = 2200, 65001
+    g = torch.Generator("cuda").manual_seed(12)
+    x = (torch.randn(rows, vocab, device="cuda", generator=g) * 2.5).to(bf16)
+    t = torch.arange(rows, device="cuda") * 29 - 5
+    gl, ge = torch.randn(rows, device="cuda", generator=g), torch.randn(rows, device="cuda", generator=g)
+    r = mp.token_logprobs(x, t, top_k=5)
+    got = mp.token_logprobs_backward(x, t, r.lse, r.entropy, gl, ge)
+    some = [0, 1, 1000, rows - 2, rows - 1]
+    check(x[some], t[some], 5, mp.TokenLogprobs(*(v[some] for v in r)))
+    check_grad(x[some], t[some], r, gl[some], ge[some], got=got[some])
 
 
 def test_same_bits_again_and_on_another_stream(gpu_ok):
