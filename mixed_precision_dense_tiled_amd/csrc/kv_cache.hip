@@ -22,8 +22,8 @@ namespace {
 
 // Tokens to a workgroup: one thread each finds where its token belongs, then
 // all threads move the rows, 8 elements at a time.  8800 tokens of 8 heads of 128
-// in BF16 (72 MB): 14.3 us, 5.0 TB/s, a copy's rate; 4801 tokens into FP8 (30 MB):
-// 16 us, of which the bytes are 6.
+// in BF16 (72 MB): 13.0 us, 5.5 TB/s (14.3 with a load and a store in turn); 4801
+// tokens into FP8 (30 MB): 14.5 us, of which the bytes are 6.
 constexpr int APPEND_TOKENS = 8;
 
 __device__ __forceinline__ float widen(uint16_t x, bool bf16) {
@@ -37,56 +37,85 @@ template <bool TO8>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
     __shared__ int64_t dst[APPEND_TOKENS];
     const int t0 = blockIdx.x * APPEND_TOKENS;
-    if (threadIdx.x < APPEND_TOKENS) {
-        const int t = t0 + threadIdx.x;
-        int64_t off = -1;
-        if (t < a.sv.tokens) {
-            int lo = 0, hi = a.sv.seqs;     // the last sequence that starts at or before t
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) / 2;
-                if (a.sv.cu_q[mid] <= t) lo = mid;
+    if (threadIdx.x < 64) {
+        // one wave finds each token's sequence, the last that starts at or before
+        // it: among up to 64 in one look (a lane each), else by halves
+        const int lane = threadIdx.x, t = t0 + lane;
+        int seq = 0;
+        if (a.sv.seqs <= 64) {
+            const int start = lane < a.sv.seqs ? a.sv.cu_q[lane] : 0x7fffffff;
+#pragma unroll
+            for (int k = 0; k < APPEND_TOKENS; ++k) {
+                const int upto = __popcll(__ballot(start <= t0 + k));
+                if (lane == k) seq = upto > 0 ? upto - 1 : 0;
+            }
+        } else if (lane < APPEND_TOKENS) {
+            int hi = a.sv.seqs;
+            while (hi - seq > 1) {
+                const int mid = (seq + hi) / 2;
+                if (a.sv.cu_q[mid] <= t) seq = mid;
                 else hi = mid;
             }
-            const int end = a.sv.cu_q[lo + 1];
-            if (t >= a.sv.cu_q[lo] && t < end) {
-                const int64_t pos = (int64_t)a.sv.lens[lo] - (end - t);
+        }
+        if (lane < APPEND_TOKENS) {
+            int64_t off = -1;
+            const int begin = a.sv.cu_q[seq], end = a.sv.cu_q[seq + 1], len = a.sv.lens[seq];
+            if (t < a.sv.tokens && t >= begin && t < end) {
+                const int64_t pos = (int64_t)len - (end - t);
                 const int64_t pi = pos / a.kv.page_size;
                 if (pos >= 0 && pi < a.sv.width) {
-                    const int pg = a.sv.table[(int64_t)lo * a.sv.ld_table + pi];
+                    const int pg = a.sv.table[(int64_t)seq * a.sv.ld_table + pi];
                     if (pg >= 0 && pg < a.kv.pages)
                         off = pg * a.kv.page_b + (pos - pi * a.kv.page_size) * a.kv.slot_b;
                 }
             }
+            dst[lane] = off;
         }
-        dst[threadIdx.x] = off;
     }
     __syncthreads();
     const int per_row = a.kv.dim / 8, per_tok = a.kv.kv_heads * per_row;
     const bool bf16 = a.type == DT_BF16;
-    for (int i = threadIdx.x; i < 2 * APPEND_TOKENS * per_tok; i += 256) {
-        const int k = i / per_tok, c = i - k * per_tok, t = k >> 1, h = c / per_row, e = c - h * per_row;
-        const int64_t off = dst[t];
-        if (off < 0) continue;
-        const bool is_v = k & 1;
-        const char* src = is_v ? a.v_new + (t0 + t) * a.v_tok_b + h * a.v_head_b
-                               : a.k_new + (t0 + t) * a.k_tok_b + h * a.k_head_b;
-        char* to = (is_v ? a.kv.v : a.kv.k) + off + h * a.kv.head_b;
-        const u32x4 x = *reinterpret_cast<const u32x4*>(src + 16 * e);
-        if constexpr (TO8) {
-            const float s = (is_v ? a.kv.v_scale : a.kv.k_scale)[h];
-            float f[8];
+    const int n = 2 * APPEND_TOKENS * per_tok;
+    // eight loads of a thread at a time, then their stores
+    constexpr int U = 8;
+    for (int i0 = threadIdx.x; i0 < n; i0 += 256 * U) {
+        u32x4 x[U];
+        char* to[U];
+        float scale[U];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = cut448(widen((uint16_t)(x[j >> 1] >> (16 * (j & 1))), bf16) / s);
-            u32x2 w;
+        for (int u = 0; u < U; ++u) {
+            const int i = min(i0 + u * 256, n - 1);
+            const int k = i / per_tok, c = i - k * per_tok, h = c / per_row, e = c - h * per_row;
+            const bool is_v = k & 1;
+            // (a token past the last reads the last one's row, which is there)
+            const int t = min(t0 + (k >> 1), a.sv.tokens - 1);
+            const char* src = is_v ? a.v_new + t * a.v_tok_b + h * a.v_head_b : a.k_new + t * a.k_tok_b + h * a.k_head_b;
+            x[u] = *reinterpret_cast<const u32x4*>(src + 16 * e);
+            const int64_t off = dst[k >> 1];
+            to[u] = off < 0 || i0 + u * 256 >= n
+                        ? nullptr
+                        : (is_v ? a.kv.v : a.kv.k) + off + h * a.kv.head_b + (TO8 ? 8 : 16) * e;
+            if constexpr (TO8) scale[u] = (is_v ? a.kv.v_scale : a.kv.k_scale)[h];
+        }
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                int q = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * j], f[4 * j + 1], 0, false);
-                q = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * j + 2], f[4 * j + 3], q, true);
-                w[j] = (uint32_t)q;
+        for (int u = 0; u < U; ++u) {
+            if (!to[u]) continue;
+            if constexpr (TO8) {
+                float f[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    f[j] = cut448(widen((uint16_t)(x[u][j >> 1] >> (16 * (j & 1))), bf16) / scale[u]);
+                u32x2 w;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    int q = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * j], f[4 * j + 1], 0, false);
+                    q = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * j + 2], f[4 * j + 3], q, true);
+                    w[j] = (uint32_t)q;
+                }
+                *reinterpret_cast<u32x2*>(to[u]) = w;
+            } else {
+                *reinterpret_cast<u32x4*>(to[u]) = x[u];
             }
-            *reinterpret_cast<u32x2*>(to + 8 * e) = w;
-        } else {
-            *reinterpret_cast<u32x4*>(to + 16 * e) = x;
         }
     }
 }
