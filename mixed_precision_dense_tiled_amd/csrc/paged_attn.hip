@@ -587,17 +587,23 @@ __device__ __forceinline__ float lse_of(float ref, float sum) {
 // ---- few rows: 16 rows by 32 keys a wave ----------------------------------------
 //
 // Bound by the cache's bytes: 64 sequences of 700 to 8000 keys, 8 KV heads of 128
-// in BF16 (1.14 GB): 198 us of kernel, 5.8 TB/s; 8 of 9000 to 65000 keys in FP8
-// (0.61 GB): 104 us, 5.8 TB/s; a plain stream of 1 GiB reads at 6.7.  Each wave
+// in BF16 (1.14 GB): 203 us a pass, 5.6 TB/s; 8 of 9000 to 65000 keys in FP8
+// (0.61 GB): 116 us, 5.2 TB/s; a plain stream of 1 GiB reads at 6.7.  Each wave
 // keeps a ring of its own, so nothing but its own loads holds it up: 64 to 128 KB
-// a CU are in flight.  Non-temporal loads took these two from 220 and 116 us.
+// a CU are in flight.  Non-temporal loads took the kernels from 220 to 200 and from
+// 116 to 103 us.
 // One sequence of 517 keys and 8 KV heads is eight workgroups on one memory round
 // trip after another (numbers, page table, keys): 9 us.
 
 constexpr int DEC_ROWS = 16, DEC_KEYS = 32;
 constexpr int DEC_LDS = 128 * 1024;       // rings of a workgroup
 
-// WAVES: 4, or 8 for a workgroup that has a unit to itself.
+// Waves of a workgroup: eight with one or two stages each over 16-bit caches (64
+// sequences of dim 128: 203 us against 215 of four waves with twice the stages;
+// dim 64: 122 against 133) and where a workgroup has a unit to itself; four over
+// FP8 (two stages more a wave: 116 us against 122).
+constexpr int dec_waves(bool kv8, bool direct) { return direct || !kv8 ? 8 : 4; }
+
 template <bool KV8, int DP, int WAVES>
 struct Dec {
     using R = Rows<DP, KV8, 16>;
@@ -776,8 +782,8 @@ __device__ __forceinline__ void dec_tile(const MPDT_LDS char* st, const u32x4 (&
 
 // DIRECT: one workgroup to a unit, no plan and no joining.
 template <class E, class EP, bool KV8, int DP, bool CAP, bool DIRECT>
-__global__ __launch_bounds__(64 * (DIRECT ? 8 : 4)) void attn_decode_kernel(AttnArgs a) {
-    constexpr int WAVES = DIRECT ? 8 : 4;
+__global__ __launch_bounds__(64 * dec_waves(KV8, DIRECT)) void attn_decode_kernel(AttnArgs a) {
+    constexpr int WAVES = dec_waves(KV8, DIRECT);
     using D = Dec<KV8, DP, WAVES>;
     __shared__ __attribute__((aligned(1024))) char smem[WAVES * D::RING];
     __shared__ int64_t pages[PAGES_LDS];
@@ -1639,14 +1645,15 @@ hipError_t launch_as(const AttnArgs& a, const Shape& s, hipStream_t stream) {
     hipError_t err;
     if (s.direct) {
         hipLaunchKernelGGL((attn_decode_kernel<E, EP, KV8, DP, CAP, true>),
-                           dim3((unsigned)s.entries, (unsigned)a.kv.kv_heads), dim3(512), 0, stream, a);
+                           dim3((unsigned)s.entries, (unsigned)a.kv.kv_heads),
+                           dim3(64 * dec_waves(KV8, true)), 0, stream, a);
         return hipGetLastError();
     }
     if (!a.near) hipLaunchKernelGGL(attn_plan_kernel, dim3(1), dim3(1024), 0, stream, a, s.key_tile);
     if ((err = hipGetLastError()) != hipSuccess) return err;
     if (s.few) {
         hipLaunchKernelGGL((attn_decode_kernel<E, EP, KV8, DP, CAP, false>), dim3((unsigned)s.workers),
-                           dim3(256), 0, stream, a);
+                           dim3(64 * dec_waves(KV8, false)), 0, stream, a);
     } else if (a.kv.page_size % 16 == 0) {
         hipLaunchKernelGGL((attn_chunk_kernel<E, EP, KV8, DP, CAP, true>), dim3((unsigned)s.workers),
                            dim3(64 * CHK_WAVES), 0, stream, a);
