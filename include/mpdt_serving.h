@@ -76,7 +76,9 @@ mpdt_status paged_kv_append(const mpdt_paged_kv* kv, const mpdt_sequences* seq, 
  * stands at position p = n - nq + t and sees the keys j <= p; with window > 0
  * only those with j > p - window.  Query head h reads KV head
  * h / (heads / kv_heads).  s = scale * (q . k), then softcap * tanh(s /
- * softcap) where softcap > 0; out = sum softmax(s) v, lse = log sum exp(s).
+ * softcap) where softcap > 0 (any finite one: a large cap lets the score through;
+ * the cap adds a few roundings of the capped score, in chunks up to 2^-22 of a
+ * softcap of at most 64); out = sum softmax(s) v, lse = log sum exp(s).
  * A token that sees no key gets out = 0 and lse = -inf.  Keys and values past a
  * sequence's end or on pages that do not exist are never looked at; a value that
  * is no number or infinite, hidden from one token but seen by another of the same

@@ -548,25 +548,67 @@ __device__ __forceinline__ uint64_t from_to(int first, int last) {
     return upto & ~below;
 }
 
-// Score in base-2 logarithms: s * c, or capped.
+// Score in base-2 logarithms: s * mul, or capped: cap tanh(y), y = s * scale / cap.
 struct Score {
     float mul, cap2, inner;   // inner: 2 * log2(e) * scale / cap
 };
 __device__ __forceinline__ Score score_of(const AttnArgs& a, float k_scale) {
     Score s;
     s.mul = a.scale * k_scale * LOG2E;
-    s.cap2 = a.softcap * LOG2E;
-    s.inner = a.softcap > 0.0f ? 2.0f * LOG2E * a.scale * k_scale / a.softcap : 0.0f;
+    // (held finite: a product of zero stays a score of zero)
+    s.cap2 = fminf(a.softcap * LOG2E, 3e38f);
+    s.inner = a.softcap > 0.0f ? fminf(fmaxf(2.0f * LOG2E * a.scale * k_scale / a.softcap, -3e38f), 3e38f) : 0.0f;
     return s;
 }
-// cap * tanh(x / cap), tanh(y) = 1 - 2 / (exp(2 y) + 1); both ends saturate.
-template <bool CAP>
-__device__ __forceinline__ float score(const Score& c, float s) {
-    if constexpr (CAP) {
-        const float e = __builtin_amdgcn_exp2f(s * c.inner);
-        return c.cap2 - 2.0f * c.cap2 * __builtin_amdgcn_rcpf(e + 1.0f);
+// How scores are capped.  CAP_ANY, right for every cap: from |y| = 1/2 on tanh(y) = 1 -
+// 2 / (exp(2 y) + 1), both ends of which saturate; below, where that difference
+// would leave an error of the cap's size in a score near zero, y T(y^2), T of degree 4
+// in z^2 with z = 2 log2(e) y, fitted at Chebyshev nodes over |y| <= 1/2 (off by
+// 2^-25), times the score itself, so that a cap however large only lets the score
+// through.  CAP_NEAR: the first form alone, whose error of up to 2^-22 of the cap is, up
+// to CAP_NEAR_MOST, 2^-16 of a weight, 1/16 of its rounding to FP16.  The kernel of
+// few rows waits for memory and takes CAP_ANY throughout (64 sequences: 198 us with
+// either); the kernel of many rows is bound by its vector operations (17 sequences in
+// FP16, dim 64: CAP_NEAR 126 us, CAP_ANY 148 under a cap of 100, 179 where every
+// score passes 1/2).
+enum : int { CAP_NONE = 0, CAP_NEAR = 1, CAP_ANY = 2 };
+constexpr float CAP_NEAR_MOST = 64.0f;
+constexpr float CAP_SMALL = LOG2E;     // |z| at |y| = 1/2
+__device__ __forceinline__ float score_exp(const Score& c, float z) {
+    return fmaf(-2.0f * c.cap2, __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(z) + 1.0f), c.cap2);
+}
+__device__ __forceinline__ float score_small(const Score& c, float s, float z) {
+    const float x = z * z;
+    float t = fmaf(x, 3.565785164028057e-06f, -9.181624045595527e-05f);
+    t = fmaf(x, t, 0.001922387513332069f);
+    t = fmaf(x, t, -0.040037430822849274f);
+    t = fmaf(x, t, 1.0f);
+    return s * c.mul * t;
+}
+// N scores of a lane, capped in place; CAP_ANY four at a time (all side by side would
+// hold several registers a score), the exponentials only where one of the wave's
+// four reaches 1/2.
+template <int CAP, int N>
+__device__ __forceinline__ void cap_scores(const Score& c, float (&s)[N]) {
+    if constexpr (CAP == CAP_NEAR) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i] = score_exp(c, s[i] * c.inner);
+        return;
     }
-    return s * c.mul;
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        float z[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            z[j] = s[i + j] * c.inner;
+            s[i + j] = score_small(c, s[i + j], z[j]);
+        }
+        const float most = fmaxf(fmaxf(fabsf(z[0]), fabsf(z[1])), fmaxf(fabsf(z[2]), fabsf(z[3])));
+        if (__ballot(most >= CAP_SMALL)) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i + j] = fabsf(z[j]) >= CAP_SMALL ? score_exp(c, z[j]) : s[i + j];
+        }
+    }
 }
 
 // Four outputs of a row from d on, rounded once to the type of q.
@@ -686,7 +728,7 @@ struct DecLoads {
     }
 };
 
-template <class E, class EP, bool KV8, int DP, bool CAP, int WAVES>
+template <class E, class EP, bool KV8, int DP, int CAP, int WAVES>
 __device__ __forceinline__ void dec_tile(const MPDT_LDS char* st, const u32x4 (&qf)[DP / 32], const Score& sc,
                                          uint32_t mask, bool edge, int key0, int qpos, int qlow, float& ref,
                                          float& sum, f32x4 (&o)[DP / 16]) {
@@ -737,7 +779,8 @@ __device__ __forceinline__ void dec_tile(const MPDT_LDS char* st, const u32x4 (&
         }
     float x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = score<CAP>(sc, s[i >> 2][i & 3]);
+    for (int i = 0; i < 8; ++i) x[i] = CAP != CAP_NONE ? s[i >> 2][i & 3] : s[i >> 2][i & 3] * sc.mul;
+    if constexpr (CAP != CAP_NONE) cap_scores<CAP>(sc, x);
     if (edge) {
         const uint32_t seen = (mask & (uint32_t)from_to(qlow + 1 - key0, qpos - key0)) >> (4 * g);
 #pragma unroll
@@ -781,7 +824,7 @@ __device__ __forceinline__ void dec_tile(const MPDT_LDS char* st, const u32x4 (&
 }
 
 // DIRECT: one workgroup to a unit, no plan and no joining.
-template <class E, class EP, bool KV8, int DP, bool CAP, bool DIRECT>
+template <class E, class EP, bool KV8, int DP, int CAP, bool DIRECT>
 __global__ __launch_bounds__(64 * dec_waves(KV8, DIRECT)) void attn_decode_kernel(AttnArgs a) {
     constexpr int WAVES = dec_waves(KV8, DIRECT);
     using D = Dec<KV8, DP, WAVES>;
@@ -1198,16 +1241,18 @@ struct ChkRefill {
 };
 
 // Weights of a tile from its scores, with the running maximum and sum.
-template <class EP, int DP, bool CAP>
+template <class EP, int DP, int CAP>
 __device__ __forceinline__ void chk_weights(f32x16 (&s)[2], const Score& sc, uint64_t mask, bool edge, int key0,
                                             int qpos, int qlow, float& ref, float& sum,
                                             f32x16 (&o)[(DP + 31) / 32], u32x4 (&p)[4]) {
     const int h = (threadIdx.x & 63) >> 5;
-    if constexpr (CAP) {
+    if constexpr (CAP != CAP_NONE) {
+        float c[32];
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
+        for (int i = 0; i < 32; ++i) c[i] = s[i >> 4][i & 15];
+        cap_scores<CAP>(sc, c);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[ks][i] = score<true>(sc, s[ks][i]);
+        for (int i = 0; i < 32; ++i) s[i >> 4][i & 15] = c[i];
     }
     if (edge) {
         // the keys of this half of the wave that the row sees, in the order of
@@ -1221,7 +1266,7 @@ __device__ __forceinline__ void chk_weights(f32x16 (&s)[2], const Score& sc, uin
                 s[ks][i] = w & (1u << (8 * (i >> 2) + (i & 3))) ? s[ks][i] : -__builtin_inff();
             }
     }
-    const float mul = CAP ? 1.0f : sc.mul;       // positive
+    const float mul = CAP != CAP_NONE ? 1.0f : sc.mul;       // positive
     float m = s[0][0], m1 = s[1][0];            // (two chains)
 #pragma unroll
     for (int i = 1; i < 16; ++i) {
@@ -1378,7 +1423,7 @@ struct ChkMma {
     }
 };
 
-template <class E, class EP, bool KV8, int DP, bool CAP, bool PAGE16>
+template <class E, class EP, bool KV8, int DP, int CAP, bool PAGE16>
 __global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(2, 2))) void attn_chunk_kernel(
     AttnArgs a) {
     using D = Chk<KV8, DP>;
@@ -1432,7 +1477,7 @@ __global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(
         // the largest score is the factor times the largest product where the
         // factor is positive: a negative one goes to q's signs, a zero to q
         uint32_t keep = 0xffffffffu, flip = 0;
-        if constexpr (!CAP) {
+        if constexpr (CAP == CAP_NONE) {
             if (sc.mul < 0.0f) flip = 0x80008000u;
             if (sc.mul == 0.0f) keep = 0;
             sc.mul = sc.mul == 0.0f ? 1.0f : fabsf(sc.mul);
@@ -1640,11 +1685,12 @@ Shape shape_of(const AttnArgs& a) {
     return s;
 }
 
-template <class E, class EP, bool KV8, int DP, bool CAP>
+template <class E, class EP, bool KV8, int DP, int CAP>
 hipError_t launch_as(const AttnArgs& a, const Shape& s, hipStream_t stream) {
     hipError_t err;
+    constexpr int FEW_CAP = CAP == CAP_NONE ? CAP_NONE : CAP_ANY;
     if (s.direct) {
-        hipLaunchKernelGGL((attn_decode_kernel<E, EP, KV8, DP, CAP, true>),
+        hipLaunchKernelGGL((attn_decode_kernel<E, EP, KV8, DP, FEW_CAP, true>),
                            dim3((unsigned)s.entries, (unsigned)a.kv.kv_heads),
                            dim3(64 * dec_waves(KV8, true)), 0, stream, a);
         return hipGetLastError();
@@ -1652,7 +1698,7 @@ hipError_t launch_as(const AttnArgs& a, const Shape& s, hipStream_t stream) {
     if (!a.near) hipLaunchKernelGGL(attn_plan_kernel, dim3(1), dim3(1024), 0, stream, a, s.key_tile);
     if ((err = hipGetLastError()) != hipSuccess) return err;
     if (s.few) {
-        hipLaunchKernelGGL((attn_decode_kernel<E, EP, KV8, DP, CAP, false>), dim3((unsigned)s.workers),
+        hipLaunchKernelGGL((attn_decode_kernel<E, EP, KV8, DP, FEW_CAP, false>), dim3((unsigned)s.workers),
                            dim3(64 * dec_waves(KV8, false)), 0, stream, a);
     } else if (a.kv.page_size % 16 == 0) {
         hipLaunchKernelGGL((attn_chunk_kernel<E, EP, KV8, DP, CAP, true>), dim3((unsigned)s.workers),
@@ -1675,8 +1721,9 @@ hipError_t launch_as(const AttnArgs& a, const Shape& s, hipStream_t stream) {
 
 template <class E, class EP, bool KV8, int DP>
 hipError_t launch_cap(const AttnArgs& a, const Shape& s, hipStream_t stream) {
-    return a.softcap > 0.0f ? launch_as<E, EP, KV8, DP, true>(a, s, stream)
-                            : launch_as<E, EP, KV8, DP, false>(a, s, stream);
+    if (a.softcap == 0.0f) return launch_as<E, EP, KV8, DP, CAP_NONE>(a, s, stream);
+    return a.softcap <= CAP_NEAR_MOST ? launch_as<E, EP, KV8, DP, CAP_NEAR>(a, s, stream)
+                                      : launch_as<E, EP, KV8, DP, CAP_ANY>(a, s, stream);
 }
 
 template <class E, class EP, bool KV8>
