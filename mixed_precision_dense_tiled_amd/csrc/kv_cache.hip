@@ -59,15 +59,12 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
         }
         if (lane < APPEND_TOKENS) {
             int64_t off = -1;
-            const int begin = a.sv.cu_q[seq], end = a.sv.cu_q[seq + 1], len = a.sv.lens[seq];
-            if (t < a.sv.tokens && t >= begin && t < end) {
-                const int64_t pos = (int64_t)len - (end - t);
-                const int64_t pi = pos / a.kv.page_size;
-                if (pos >= 0 && pi < a.sv.width) {
-                    const int pg = a.sv.table[(int64_t)seq * a.sv.ld_table + pi];
-                    if (pg >= 0 && pg < a.kv.pages)
-                        off = pg * a.kv.page_b + (pos - pi * a.kv.page_size) * a.kv.slot_b;
-                }
+            const Seq s = seq_of(a.sv, a.kv.page_size, seq);
+            const int pos = s.n - (s.start + s.nq - t);
+            if (t >= s.start && t < s.start + s.nq && pos >= 0) {
+                const int pi = a.kv.page_of(pos);
+                const int pg = a.sv.table[(int64_t)seq * a.sv.ld_table + pi];
+                if (pg >= 0 && pg < a.kv.pages) off = pg * a.kv.page_b + (pos - pi * a.kv.page_size) * a.kv.slot_b;
             }
             dst[lane] = off;
         }

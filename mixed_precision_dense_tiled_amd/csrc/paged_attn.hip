@@ -193,22 +193,7 @@ __device__ __forceinline__ float uni(float x) {
 
 // ---- sequences, units and the plan --------------------------------------------
 
-struct Seq {
-    int start, nq, n;   // first row of q, new tokens, keys
-};
-
-// Numbers that point outside the batch are cut to it.
-__device__ __forceinline__ Seq seq_of(const SeqView& v, int64_t page_size, int b) {
-    Seq s;
-    const int c0 = v.cu_q[b], c1 = v.cu_q[b + 1];
-    s.start = min(max(c0, 0), v.tokens);
-    s.nq = min(max(c1, s.start), v.tokens) - s.start;
-    const int64_t most = page_size * v.width;
-    s.n = (int)min((int64_t)max(v.lens[b], 0), most);
-    return s;
-}
-
-// The same for a sequence that the whole wave works on.
+// A sequence that the whole wave works on.
 __device__ __forceinline__ Seq uniform_seq(const SeqView& v, int64_t page_size, int b) {
     const Seq s = seq_of(v, page_size, b);
     return Seq{uni(s.start), uni(s.nq), uni(s.n)};

@@ -41,6 +41,21 @@ struct SeqView {
     int tokens;             // rows of q / of the new keys
 };
 
+// A sequence as every operator sees it: numbers that point outside the batch are
+// cut to it.  Its last nq of n tokens are the rows from `start` on.
+struct Seq {
+    int start, nq, n;
+};
+__device__ __forceinline__ Seq seq_of(const SeqView& v, int64_t page_size, int b) {
+    Seq s;
+    const int c0 = v.cu_q[b], c1 = v.cu_q[b + 1];
+    s.start = min(max(c0, 0), v.tokens);
+    s.nq = min(max(c1, s.start), v.tokens) - s.start;
+    const int64_t most = page_size * v.width;
+    s.n = (int)min((int64_t)max(v.lens[b], 0), most);
+    return s;
+}
+
 struct AttnArgs {
     PagedKV kv;
     SeqView sv;
