@@ -111,11 +111,11 @@ typedef struct {
 /* Bytes of workspace for each of the four below (cache_free needs none). */
 int64_t cache_pages_workspace(int64_t pages, int64_t rows);
 
-/* Row r becomes a copy of row parent[r] (< 0: it stays): whole pages are
- * shared and their counters raised, a part-filled last page is copied in every
+/* Row r becomes a copy of row parent[r] (itself or no row: it stays): whole pages
+ * are shared and their counters raised, a part-filled last page is copied in every
  * plane to a free page of its own, the lowest free pages going to the rows in
- * ascending order.  What row r held before is forgotten.  A parent that is
- * itself forked into by the same call is no parent.  Where pages are missing,
+ * ascending order.  What row r held before is forgotten.  A row that names
+ * another one in the same call is no parent.  Where pages are missing,
  * nothing changes and *shortfall says how many (0 otherwise). */
 mpdt_status cache_fork(const mpdt_pages* c, const int32_t* parent, int32_t* shortfall, void* workspace,
                        int64_t workspace_bytes, void* stream);

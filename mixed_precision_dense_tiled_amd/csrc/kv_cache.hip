@@ -181,11 +181,15 @@ __host__ __device__ inline PagesWs pages_ws(int32_t* ws, int pages) {
     return PagesWs{ws, ws + 16, ws + 16 + 2 * (int64_t)pages};
 }
 
-// Parent of a row, or -1.  A parent that is itself a child of this call has
-// no settled contents; rows that name one are left as they are.
-__device__ __forceinline__ int parent_of(const PagesArgs& a, int row) {
+// Whether a row names another one, so that this call may write it.
+__device__ __forceinline__ bool names_another(const PagesArgs& a, int row) {
     const int p = a.which[row];
-    return p >= 0 && p < a.rows && p != row && a.which[p] < 0 ? p : -1;
+    return p >= 0 && p < a.rows && p != row;
+}
+// Parent of a row, or -1.  A parent that may be written by this call has no settled
+// contents; rows that name one are left as they are.
+__device__ __forceinline__ int parent_of(const PagesArgs& a, int row) {
+    return names_another(a, row) && !names_another(a, a.which[row]) ? a.which[row] : -1;
 }
 
 // Fork, first launch: part-filled pages wanted, free ones found for them in

@@ -282,11 +282,11 @@ def cache_fork(kv, refs, table, lens, parent, page_size):
     kv [planes, pages, page_size, ...]: every plane (layer; K and V) of the
     cache, any type, each page contiguous; refs INT32 [pages]: how many rows
     hold a page (0: free); table INT32 [rows, width]; lens INT32 [rows].  Row r
-    becomes a copy of row parent[r] (INT32 [rows]; negative: it stays): whole
+    becomes a copy of row parent[r] (INT32 [rows]; itself or no row: it stays): whole
     pages are shared and their refs raised, a part-filled last page is copied
     to a free page of its own, the lowest free pages going to the rows in
     ascending order.  What row r held before is forgotten (cache_free it
-    first); a parent that is itself forked into by this call is no parent.
+    first); a row that names another one in this call is no parent.
 
     Returns an INT32 tensor of one number: pages that were missing.  Where it
     is not 0, nothing was changed."""
