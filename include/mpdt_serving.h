@@ -122,8 +122,8 @@ mpdt_status cache_fork(const mpdt_pages* c, const int32_t* parent, int32_t* shor
 
 /* Room for add[r] (>= 0) more tokens in row r: the pages that its new length
  * needs, the lowest free ones in ascending order of rows.  Where pages are
- * missing or a row of the table is full, nothing changes and *shortfall says
- * how many pages could not be had. */
+ * missing, nothing changes and *shortfall says how many; where a row of the table
+ * is full, nothing changes and it says how many pages were asked for. */
 mpdt_status cache_extend(const mpdt_pages* c, const int32_t* add, int32_t* shortfall, void* workspace,
                          int64_t workspace_bytes, void* stream);
 

@@ -207,13 +207,13 @@ __global__ __launch_bounds__(PLAN_THREADS) void fork_plan_kernel(PagesArgs a) {
         if (r < a.rows) w.row_at[r] = part ? at : -1;
         need += total;
     }
-    const int got = need > a.pages ? 0 : free_pages(a.refs, a.pages, need, w.list, red);
+    const int got = free_pages(a.refs, a.pages, need, w.list, red);
     const bool go = got == need;
     if (go)
         for (int i = threadIdx.x; i < need; i += PLAN_THREADS) a.refs[w.list[i]] = 1;
     if (threadIdx.x == 0) {
         w.head[1] = go;
-        if (a.shortfall) a.shortfall[0] = go ? 0 : need - min(got, need);
+        if (a.shortfall) a.shortfall[0] = need - got;
     }
 }
 
@@ -268,35 +268,31 @@ __global__ __launch_bounds__(256) void fork_move_kernel(PagesArgs a) {
 // Extend every row by which[row] tokens: one workgroup, one launch.
 __global__ __launch_bounds__(PLAN_THREADS) void extend_kernel(PagesArgs a) {
     __shared__ int red[PLAN_THREADS / 64];
-    __shared__ int64_t wide[2];     // pages wanted, pages past the table's width
+    __shared__ int64_t past;        // pages past the table's width
     const PagesWs w = pages_ws(a.ws, a.pages);
-    if (threadIdx.x < 2) wide[threadIdx.x] = 0;
+    if (threadIdx.x == 0) past = 0;
     __syncthreads();
-    int need = 0;
+    int need = 0;                   // (at most rows * width)
     for (int r0 = 0; r0 < a.rows; r0 += PLAN_THREADS) {
         const int r = r0 + threadIdx.x;
-        int more = 0, past = 0;
+        int more = 0, over = 0;
         if (r < a.rows) {
             const int len = max(a.lens[r], 0), add = max(a.which[r], 0), have = held_pages(len, a.page_size);
             const int64_t want = ((int64_t)len + add + a.page_size - 1) / a.page_size;
             more = (int)(min(want, (int64_t)a.width) - min(have, a.width));
-            past = (int)min(want - a.width, (int64_t)1 << 30);
-            if (past < 0) past = 0;
+            over = (int)max((int64_t)0, min(want - a.width, (int64_t)1 << 30));
         }
-        if (more) atomicAdd((unsigned long long*)&wide[0], (unsigned long long)more);
-        if (past) atomicAdd((unsigned long long*)&wide[1], (unsigned long long)past);
+        if (over) atomicAdd((unsigned long long*)&past, (unsigned long long)over);
         int total;
         const int at = need + plan_scan(more, red, total);
         if (r < a.rows) w.row_at[r] = at;
         need += total;
     }
     __syncthreads();
-    const int64_t wanted = wide[0], past = wide[1];
-    const bool fits = wanted <= a.pages && past == 0;
-    const int got = fits ? free_pages(a.refs, a.pages, need, w.list, red) : 0;
-    const bool go = fits && got == need;
-    if (threadIdx.x == 0 && a.shortfall)
-        a.shortfall[0] = go ? 0 : (int)min(wanted + past - got, (int64_t)0x7fffffff);
+    // (where a row is full no page is taken for any)
+    const int got = past == 0 ? free_pages(a.refs, a.pages, need, w.list, red) : 0;
+    const bool go = past == 0 && got == need;
+    if (threadIdx.x == 0 && a.shortfall) a.shortfall[0] = (int)min(need + past - got, (int64_t)0x7fffffff);
     if (!go) return;
     for (int r = threadIdx.x; r < a.rows; r += PLAN_THREADS) {
         const int len = max(a.lens[r], 0), add = max(a.which[r], 0), have = held_pages(len, a.page_size);

@@ -298,8 +298,9 @@ def cache_extend(refs, table, lens, add, page_size):
     place: lens grows, and the pages that the new lengths need are the lowest
     free ones in ascending order of rows.  refs, table, lens as in cache_fork.
 
-    Returns an INT32 tensor of one number: pages that could not be had (none
-    free, or a row of the table full).  Where it is not 0, nothing was changed."""
+    Returns an INT32 tensor of one number: pages that were missing, or where a
+    row of the table is full all that were asked for.  Where it is not 0, nothing
+    was changed."""
     return _pages_call("cache_extend", None, refs, table, lens, add, "add", page_size, True)
 
 

@@ -1,4 +1,5 @@
-"""cache_fork's rule for parents, written out from its documentation."""
+"""cache_fork's rule for parents, and what cache_fork and cache_extend say is
+missing, written out from their documentation."""
 import pytest
 import torch
 
@@ -57,3 +58,27 @@ def test_a_row_that_is_written_is_no_parent(gpu_ok):
         assert torch.equal(a, b)
     assert mp.cache_fork(kv, refs, table, lens, ints([-1, -1, -1, 2, 3]), PAGE).item() == 0
     assert lens.tolist() == [6, 7, 3, 3, 0] and table[3].tolist() == [5, -1, -1, -1] and refs.sum().item() == 6
+
+
+@pytest.mark.parametrize("pages, missing", [(9, 0), (8, 1), (4, 5), (3, 6)])
+def test_fork_says_how_many_pages_are_missing(gpu_ok, pages, missing):
+    """Six copies of a part-filled page; also where they are more than the cache has."""
+    kv, refs, table, lens = state([10] + [0] * 6, pages)
+    before = [t.clone() for t in (kv, refs, table, lens)]
+    assert mp.cache_fork(kv, refs, table, lens, ints([-1] + [0] * 6), PAGE).item() == missing
+    if missing:
+        for a, b in zip(before, (kv, refs, table, lens)):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("pages, missing", [(13, 0), (12, 1), (9, 4), (8, 5), (3, 10), (1, 12)])
+def test_extend_says_how_many_pages_are_missing(gpu_ok, pages, missing):
+    """Four rows of which one holds a page, each to three or four pages: 12 more."""
+    kv, refs, table, lens = state([4, 0, 0, 0], pages)
+    before = [t.clone() for t in (refs, table, lens)]
+    assert mp.cache_extend(refs, table, lens, ints([12, 12, 9, 11]), PAGE).item() == missing
+    if missing:
+        for a, b in zip(before, (refs, table, lens)):
+            assert torch.equal(a, b)
+    else:
+        assert lens.tolist() == [16, 12, 9, 11] and refs.tolist() == [1] * 13
