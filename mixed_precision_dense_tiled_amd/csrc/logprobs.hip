@@ -561,7 +561,9 @@ __global__ __launch_bounds__(NT) void logprob_grad_kernel(LogprobArgs a) {
         float d[P];
 #pragma unroll
         for (int j = 0; j < P; ++j) {
-            const float z = fmaxf(E::get(v[c], j) - shift, -1e30f);       // log p, finite where p = 0
+            // log p, finite where p = 0 (at -1e4 it is, and a factor of up to 1e34 leaves
+            // the product finite)
+            const float z = fmaxf(E::get(v[c], j) - shift, -1e4f);
             const float p = __builtin_amdgcn_exp2f(z * LOG2E);
             float g = p * fmaf(-ge, z, c0);
             if (i + j == target) g += gl;
