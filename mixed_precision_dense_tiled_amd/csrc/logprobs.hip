@@ -134,17 +134,19 @@ __device__ __forceinline__ float wave_sorted(float v, int lane) {
     return v;
 }
 
-// Order of (value, index): larger first, NaN above all, then the lower index.
+// Order of (value, index): larger first, NaN above all, then the lower index.  No
+// key is ~0, which stands above all of them where the largest is looked for.
+constexpr uint32_t NAN_KEY = 0xfffffffeu;
 __device__ __forceinline__ uint64_t order_key(float x, int index) {
     const uint32_t b = __float_as_uint(x + 0.0f);
-    const uint32_t k = x != x ? 0xffffffffu : (b >> 31) ? ~b : b | 0x80000000u;
+    const uint32_t k = x != x ? NAN_KEY : (b >> 31) ? ~b : b | 0x80000000u;
     return ((uint64_t)k << 32) | (uint32_t)~index;
 }
 
 __device__ __forceinline__ int key_index(uint64_t key) { return (int)~(uint32_t)key; }
 __device__ __forceinline__ float key_value(uint64_t key) {
     const uint32_t k = (uint32_t)(key >> 32);
-    return k == 0xffffffffu ? __builtin_nanf("") : __uint_as_float((k >> 31) ? k ^ 0x80000000u : ~k);
+    return k == NAN_KEY ? __builtin_nanf("") : __uint_as_float((k >> 31) ? k ^ 0x80000000u : ~k);
 }
 
 struct TopShared {
