@@ -715,8 +715,8 @@ struct DecLoads {
 
 template <class E, class EP, bool KV8, int DP, int CAP, int WAVES>
 __device__ __forceinline__ void dec_tile(const MPDT_LDS char* st, const u32x4 (&qf)[DP / 32], const Score& sc,
-                                         uint32_t mask, bool edge, int key0, int qpos, int qlow, float& ref,
-                                         float& sum, f32x4 (&o)[DP / 16]) {
+                                         int dim, uint32_t mask, bool edge, int key0, int qpos, int qlow,
+                                         float& ref, float& sum, f32x4 (&o)[DP / 16]) {
     using D = Dec<KV8, DP, WAVES>;
     using R = typename D::R;
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
@@ -755,6 +755,15 @@ __device__ __forceinline__ void dec_tile(const MPDT_LDS char* st, const u32x4 (&
         }
     }
     __builtin_amdgcn_sched_barrier(0);
+    if constexpr (!KV8) {
+        // past dim stand other bytes of the row: q is zero there, but zero times an
+        // infinite one would be no number (an E4M3 code that is not finite is NaN, there and in its place)
+        if (dim < DP) {
+#pragma unroll
+            for (int d = 0; d < DP / 32; ++d)
+                if (32 * d + 8 * g >= dim) kf[0][d] = kf[1][d] = u32x4{0, 0, 0, 0};
+        }
+    }
 #pragma unroll
     for (int d = 0; d < DP / 32; ++d)
 #pragma unroll
@@ -931,8 +940,8 @@ __global__ __launch_bounds__(64 * dec_waves(KV8, DIRECT)) void attn_decode_kerne
                 const int key0 = (t0 + j) * DEC_KEYS;
                 if (mask[0]) {
                     const bool edge = mask[0] != 0xffffffffu || key0 + DEC_KEYS > all_hi || key0 < all_lo;
-                    dec_tile<E, EP, KV8, DP, CAP, WAVES>(ring + slot * D::STAGE, qf, sc, mask[0], edge, key0, qpos, qlow,
-                                                  ref, sum, o);
+                    dec_tile<E, EP, KV8, DP, CAP, WAVES>(ring + slot * D::STAGE, qf, sc, a.kv.dim, mask[0], edge, key0,
+                                                                  qpos, qlow, ref, sum, o);
                 }
                 __atomic_signal_fence(__ATOMIC_SEQ_CST);
                 __builtin_amdgcn_sched_barrier(0);
@@ -1135,7 +1144,10 @@ struct Chk {
 // between MFMAs.  PAGE16: pages hold a multiple of 16 tokens, so that a wave's
 // keys lie in one page and its address is scalar; a lane's own offset then is
 // the same for every tile.  Keys that do not exist are staged as zeros (from
-// the workspace): a weight of zero times their value is zero.
+// the workspace): a weight of zero times their value is zero.  So is what lies
+// past dim in rows of 16-bit values: q is zero there, but zero times another
+// value's infinity would be no number.  (FP8: other bytes of the row; a code
+// that is not finite is NaN, there and in its place.)
 template <bool KV8, int DP, bool PAGE16>
 struct ChkRefill {
     using D = Chk<KV8, DP>;
@@ -1145,7 +1157,8 @@ struct ChkRefill {
     const char *base, *zeros;    // K or V of the head
     const int64_t* pages;
     int first, lo, hi, key16;    // key16: this wave's first key in a tile
-    bool is_v, clean;
+    static constexpr uint32_t PAD = ~0u;         // a lane's offset past dim
+    bool is_v, clean, padded;
     int lane, key0;
     uint64_t mask;
     int64_t page[PAGE16 ? 1 : D::LOADS];
@@ -1157,11 +1170,13 @@ struct ChkRefill {
         is_v = wave >= CHK_WAVES / 2;
         base = is_v ? vb : kb;
         key16 = wave % (CHK_WAVES / 2) * 16;
+        padded = !KV8 && a.kv.dim < DP;
         lane = threadIdx.x & 63;
         if constexpr (PAGE16)
             static_for<0, D::LOADS>([&](auto i) {
                 constexpr int I = decltype(i)::value;
-                own[I] = (uint32_t)(row_of<I>() * a.kv.slot_b) + chunk_of<I>();
+                const uint32_t c = chunk_of<I>();
+                own[I] = c == PAD ? PAD : (uint32_t)(row_of<I>() * a.kv.slot_b) + c;
             });
     }
     template <int I>
@@ -1172,7 +1187,7 @@ struct ChkRefill {
     __device__ __forceinline__ uint32_t chunk_of() const {
         const int r = key16 + row_of<I>(), pos = (I * 64 + lane) % R::CH;
         const int from = (pos ^ (is_v ? R::swz_v(r) : R::swz_k(r))) * 16;
-        return from >= a.kv.dim * (KV8 ? 1 : 2) ? 0 : from;      // (dim below DP: any bytes of the row)
+        return from < a.kv.dim * (KV8 ? 1 : 2) ? from : KV8 ? 0 : PAD;
     }
 
     // Returns which of the tile's 64 keys exist.
@@ -1208,16 +1223,17 @@ struct ChkRefill {
     __device__ __forceinline__ void step(MPDT_LDS char* dst) {
         MPDT_LDS char* d = dst + (is_v ? D::HALF : 0) + (key16 * R::CH / 64 + I) * 1024;
         if constexpr (PAGE16) {
-            if (~mask) {
+            if (~mask || padded) {
                 const char* src = from + own[I];
-                global_to_lds16((mask >> (key16 + row_of<I>())) & 1 ? src : zeros, d);
+                global_to_lds16((mask >> (key16 + row_of<I>())) & 1 && own[I] != PAD ? src : zeros, d);
             } else {
                 global_to_lds16(from, own[I], d);
             }
         } else {
             const int slot = place_of(a.kv, first, key0 + key16 + row_of<I>()).slot;
-            const char* src = base + (page[I] + slot * a.kv.slot_b + chunk_of<I>());
-            global_to_lds16((mask >> (key16 + row_of<I>())) & 1 ? src : zeros, d);
+            const uint32_t c = chunk_of<I>();
+            const char* src = base + (page[I] + slot * a.kv.slot_b + c);
+            global_to_lds16((mask >> (key16 + row_of<I>())) & 1 && c != PAD ? src : zeros, d);
         }
     }
     __device__ __forceinline__ void steps(MPDT_LDS char* dst) {
