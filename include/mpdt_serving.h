@@ -15,6 +15,10 @@
  * read or written out of range: a page number outside [0, pages) holds no
  * keys, a length past width * page_size counts as that, an offset outside the
  * tokens is moved to their border.
+ *
+ * One call takes fewer than 2^24 rows of logits or of a page table (the gradient:
+ * of pieces of rows, 8192 values of 16 bits or 4096 of 32), and fewer than 2^27 new
+ * tokens to append.
  */
 #ifndef MPDT_SERVING_H
 #define MPDT_SERVING_H

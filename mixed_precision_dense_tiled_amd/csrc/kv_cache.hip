@@ -20,12 +20,6 @@ namespace {
 
 // ---- new keys and values into their pages ----------------------------------------
 
-// Tokens to a workgroup: one thread each finds where its token belongs, then
-// all threads move the rows, 8 elements at a time.  8800 tokens of 8 heads of 128
-// in BF16 (72 MB): 13.0 us, 5.5 TB/s (14.3 with a load and a store in turn); 4801
-// tokens into FP8 (30 MB): 14.5 us, of which the bytes are 6.
-constexpr int APPEND_TOKENS = 8;
-
 __device__ __forceinline__ float widen(uint16_t x, bool bf16) {
     return bf16 ? __uint_as_float((uint32_t)x << 16) : (float)__builtin_bit_cast(_Float16, x);
 }
@@ -33,6 +27,10 @@ __device__ __forceinline__ float widen(uint16_t x, bool bf16) {
 // x / scale, cut to the format's range (NaN stays), rounded to nearest even.
 __device__ __forceinline__ float cut448(float x) { return x > 448.0f ? 448.0f : x < -448.0f ? -448.0f : x; }
 
+// APPEND_TOKENS tokens to a workgroup: one lane each finds where its token belongs,
+// then all threads move the rows, 8 elements at a time.  8800 tokens of 8 heads of
+// 128 in BF16 (72 MB): 13.0 us, 5.5 TB/s (14.3 with a load and a store in turn); 4801
+// tokens into FP8 (30 MB): 14.5 us, of which the bytes are 6.
 template <bool TO8>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
     __shared__ int64_t dst[APPEND_TOKENS];

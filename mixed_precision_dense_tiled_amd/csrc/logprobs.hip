@@ -642,7 +642,7 @@ hipError_t backward(LogprobArgs a, hipStream_t stream) {
 }  // namespace
 
 bool logprob_fits(int type, int64_t rows, int64_t vocab) {
-    return rows * cut_of(type, rows, vocab).chunks <= 0x7fffffff;
+    return rows * cut_of(type, rows, vocab).chunks <= MAX_GROUPS;
 }
 
 int64_t logprob_workspace(int type, int64_t rows, int64_t vocab, int top) {

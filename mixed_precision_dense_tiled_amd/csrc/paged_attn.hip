@@ -1677,12 +1677,13 @@ Shape shape_of(const AttnArgs& a) {
     Shape s;
     const int64_t rows = (int64_t)a.sv.tokens * a.group;
     s.few = rows <= (int64_t)32 * a.sv.seqs;
-    s.direct = s.few && (int64_t)a.sv.width * a.kv.page_size <= DIRECT_KEYS;
     s.tile_rows = s.few ? DEC_ROWS : CHK_ROWS;
     s.key_tile = s.few ? DEC_KEYS : CHK_KEYS;
     s.workers = CUS;
     s.min_tiles = 4;
     s.entries = (int)(rows / s.tile_rows + std::min<int64_t>(a.sv.seqs, a.sv.tokens));
+    s.direct = s.few && (int64_t)a.sv.width * a.kv.page_size <= DIRECT_KEYS &&
+               s.entries <= LAUNCH_THREADS / (64 * dec_waves(true, true));
     return s;
 }
 

@@ -11,6 +11,10 @@ namespace mpdt {
 // Element types (the values of the C ABI's mpdt_dtype).
 enum : int { DT_BF16 = 0, DT_F16 = 1, DT_F32 = 2, DT_E4M3 = 3 };
 
+// A launch holds fewer than 2^32 threads along x.
+constexpr int64_t LAUNCH_THREADS = 0xffffffffll;
+constexpr int64_t MAX_GROUPS = LAUNCH_THREADS / 256;     // workgroups of 256 threads
+
 // One layer's paged cache.  Strides in BYTES, the same for K and V; a row is
 // dim elements side by side.
 struct PagedKV {
@@ -80,6 +84,7 @@ struct AttnArgs {
 int64_t attn_workspace(const AttnArgs& a);
 hipError_t launch_paged_attention(const AttnArgs& a, hipStream_t stream);
 
+constexpr int APPEND_TOKENS = 8;    // new tokens to a workgroup
 struct AppendArgs {
     PagedKV kv;
     SeqView sv;
@@ -134,7 +139,7 @@ struct LogprobArgs {
     int64_t ld_grad_b;
 };
 constexpr int LOGPROB_MAX_TOP = 64;
-bool logprob_fits(int type, int64_t rows, int64_t vocab);   // the launch's size
+bool logprob_fits(int type, int64_t rows, int64_t vocab);   // the gradient's launch
 int64_t logprob_workspace(int type, int64_t rows, int64_t vocab, int top);
 hipError_t launch_token_logprobs(const LogprobArgs& a, hipStream_t stream);
 hipError_t launch_token_logprobs_backward(const LogprobArgs& a, hipStream_t stream);

@@ -137,6 +137,7 @@ MPDT_EXPORT mpdt_status paged_kv_append(const mpdt_paged_kv* kv, const mpdt_sequ
     if ((dtype != MPDT_BF16 && dtype != MPDT_F16) || (kv->dtype != MPDT_E4M3 && dtype != kv->dtype))
         return invalid(fn, "new keys must have the cache's type, or a 16-bit one for an E4M3 cache");
     if (sq->tokens == 0 || sq->seqs == 0) return MPDT_SUCCESS;
+    if (sq->tokens > mpdt::MAX_GROUPS * mpdt::APPEND_TOKENS) return invalid(fn, "too many tokens");
     if (!k_new || !v_new) return invalid(fn, "NULL pointer");
     if (off(k_new, 16) || off(v_new, 16) || k_token % 8 || k_head % 8 || v_token % 8 || v_head % 8)
         return misaligned(fn, "new rows must start on 16-byte boundaries");
@@ -226,7 +227,7 @@ mpdt_status check_pages(const char* fn, const mpdt_pages* c, bool moves, const i
                         int32_t* shortfall, void* ws, int64_t ws_bytes, bool needs_ws, mpdt::PagesArgs* a) {
     if (!c) return invalid(fn, "cache NULL");
     if (!in_dims(c->pages, 0) || !in_dims(c->page_size, 1) || !in_dims(c->rows, 0) || !in_dims(c->width, 1) ||
-        !in_dims(c->planes, 0) || c->planes > 65534)
+        !in_dims(c->planes, 0) || c->planes > 65534 || c->rows > mpdt::MAX_GROUPS)
         return invalid(fn, "planes, pages, page_size, rows or width out of range");
     if (c->width > kMaxDim / c->page_size || c->width > kMaxDim / std::max<int64_t>(c->rows, 1))
         return invalid(fn, "width * page_size and rows * width must be at most 2^30");
@@ -337,7 +338,7 @@ mpdt_status check_logits(const char* fn, int dtype, int64_t rows, int64_t vocab,
         return misaligned(fn, "pointer not aligned to its element size");
     if (!span(logits, {{rows, ld * size_of(dtype)}}, vocab * size_of(dtype), b))
         return invalid(fn, "operand too large");
-    if (!mpdt::logprob_fits(dtype, rows, vocab)) return invalid(fn, "too many rows");
+    if (rows > mpdt::MAX_GROUPS) return invalid(fn, "too many rows");
     return MPDT_SUCCESS;
 }
 
@@ -408,6 +409,7 @@ MPDT_EXPORT mpdt_status token_logprobs_backward(int dtype, int64_t rows, int64_t
     mpdt_status s = check_logits(fn, dtype, rows, vocab, logits, ld, targets, &bx);
     if (s != MPDT_SUCCESS) return s;
     if (rows == 0) return MPDT_SUCCESS;
+    if (!mpdt::logprob_fits(dtype, rows, vocab)) return invalid(fn, "too many rows");
     if (!lse || !entropy || !grad) return invalid(fn, "lse, entropy or grad is NULL");
     if (ld_grad < vocab) return invalid(fn, "ld_grad < vocab");
     if (off(lse, 4) || off(entropy, 4) || off(g_logprob, 4) || off(g_entropy, 4) || off(grad, size_of(dtype)))
