@@ -6,7 +6,8 @@
  * The conventions of mpdt.h hold (device pointers, arguments checked on the
  * host before anything is launched, no allocation, no synchronisation, no
  * state between calls, stream order, mpdt_last_error()), with two additions:
- *   - Strides are in ELEMENTS and named in the structures below.
+ *   - Strides are in ELEMENTS and named in the structures below.  Rows that are
+ *     written (of out, of a cache that is appended to) share no bytes.
  *   - An operator that needs device scratch takes a workspace of the size that
  *     its *_workspace function names; it may be shared by calls on one stream.
  *

@@ -53,6 +53,22 @@ bool span(const void* p, std::initializer_list<Axis> axes, int64_t inner, Bytes*
     return true;
 }
 
+// Whether no two elements share a byte, for rows of `inner` bytes laid out by
+// strides that nest (in any order of the axes).
+bool apart(std::initializer_list<Axis> axes, int64_t inner) {
+    Axis by[3];
+    int n = 0;
+    for (const Axis& a : axes)
+        if (a.n > 1) by[n++] = a;
+    std::sort(by, by + n, [](const Axis& x, const Axis& y) { return x.stride < y.stride; });
+    int64_t reach = inner;
+    for (int i = 0; i < n; ++i) {
+        if (by[i].stride < reach) return false;
+        reach += (by[i].n - 1) * by[i].stride;
+    }
+    return true;
+}
+
 int size_of(int dtype) { return dtype == MPDT_F32 ? 4 : dtype == MPDT_E4M3 ? 1 : 2; }
 
 // The cache and the batch, checked and in the kernels' form; k and v: their bytes.
@@ -146,6 +162,9 @@ MPDT_EXPORT mpdt_status paged_kv_append(const mpdt_paged_kv* kv, const mpdt_sequ
         return invalid(fn, "operand too large, or a negative stride");
     if (nk.meets(bk) || nk.meets(bv) || nv.meets(bk) || nv.meets(bv))
         return abi_fail(MPDT_ERROR_ALIASING, fn, "new rows overlap the cache");
+    if (!apart({{kv->pages, a.kv.page_b}, {kv->page_size, a.kv.slot_b}, {kv->kv_heads, a.kv.head_b}},
+               kv->dim * size_of(kv->dtype)))
+        return abi_fail(MPDT_ERROR_ALIASING, fn, "rows of the cache overlap each other");
     if ((s = abi_check_device(fn)) != MPDT_SUCCESS) return s;
     a.k_new = (const char*)k_new;
     a.v_new = (const char*)v_new;
@@ -201,6 +220,8 @@ MPDT_EXPORT mpdt_status paged_attention(const mpdt_paged_kv* kv, const mpdt_sequ
     if (workspace_bytes < need || (need > 0 && !workspace)) return invalid(fn, "workspace too small");
     if (need > 0 && off(workspace, 256)) return misaligned(fn, "workspace must start on a 256-byte boundary");
     (void)span(workspace, {{need > 0, 0}}, need, &bw);
+    if (!apart({{sq->tokens, out_token * 2}, {heads, out_head * 2}}, kv->dim * 2))
+        return abi_fail(MPDT_ERROR_ALIASING, fn, "rows of out overlap each other");
     if (bo.meets(bq) || bo.meets(bk) || bo.meets(bv) || bl.meets(bq) || bl.meets(bk) || bl.meets(bv) || bl.meets(bo) ||
         bw.meets(bq) || bw.meets(bk) || bw.meets(bv) || bw.meets(bo) || bw.meets(bl))
         return abi_fail(MPDT_ERROR_ALIASING, fn, "an output or the workspace overlaps another operand");
