@@ -28,10 +28,11 @@
 // reads take any order of rows).
 //
 // Scores, maxima, sums and outputs are FP32.  P is rounded to the type that
-// the second MFMA takes (FP16 for FP16 and FP8 caches, BF16 for BF16; single
-// tokens over BF16 in two parts, 16 bits of it): one rounding per weight,
-// independent from key to key, where the sum of the weights keeps them
-// unrounded.  FP8 keys and values are widened exactly;
+// the second MFMA takes (FP16 for FP16 and FP8 caches, BF16 for BF16): single tokens
+// in two parts, 16 bits of it and more, which costs no time there; chunks once, as the
+// second part would be half again as many MFMAs where these are the bound: one
+// rounding per weight, independent from key to key, where the sum of the weights
+// keeps them unrounded.  FP8 keys and values are widened exactly;
 // their scales are per head and join the score's scale and the output.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -60,7 +61,6 @@ typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
 struct Bf16 {
     using vec8 = bf16x8;
     static constexpr float P_SHIFT = 0.0f;
-    static constexpr bool TWICE = true;
     static __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
     static __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
     static __device__ __forceinline__ uint32_t pack(float a, float b) {
@@ -90,7 +90,8 @@ struct F16 {
     // that small ones stay clear of the subnormals; the sum carries the same
     // factor and it cancels.
     static constexpr float P_SHIFT = 7.0f;
-    static constexpr bool TWICE = false;
+    static __device__ __forceinline__ float low(uint32_t w) { return (float)__builtin_bit_cast(f16x2, w)[0]; }
+    static __device__ __forceinline__ float high(uint32_t w) { return (float)__builtin_bit_cast(f16x2, w)[1]; }
     static __device__ __forceinline__ uint32_t pack(float a, float b) {
         f16x2 r;
         r[0] = (_Float16)a;
@@ -802,19 +803,18 @@ __device__ __forceinline__ void dec_tile(const MPDT_LDS char* st, const u32x4 (&
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         p[i] = EP::pack(x[2 * i], x[2 * i + 1]);
-        // BF16: what its 8 bits leave over goes through the MFMA as well (this
+        // what its 8 (FP16: 11) bits leave over goes through the MFMA as well (this
         // kernel waits for memory either way)
-        if constexpr (EP::TWICE) rest[i] = EP::pack(x[2 * i] - EP::low(p[i]), x[2 * i + 1] - EP::high(p[i]));
+        rest[i] = EP::pack(x[2 * i] - EP::low(p[i]), x[2 * i + 1] - EP::high(p[i]));
+    }
+    if constexpr (KV8) {
+#pragma unroll
+        for (int t = 0; t < DP / 16; ++t) vf[t] = widen8<EP>(u32x2{vf[t][0], vf[t][1]});
     }
 #pragma unroll
-    for (int t = 0; t < DP / 16; ++t) {
-        if constexpr (KV8) o[t] = EP::mma16(widen8<EP>(u32x2{vf[t][0], vf[t][1]}), p, o[t]);
-        else o[t] = EP::mma16(vf[t], p, o[t]);
-    }
-    if constexpr (EP::TWICE) {
+    for (int t = 0; t < DP / 16; ++t) o[t] = EP::mma16(vf[t], p, o[t]);
 #pragma unroll
-        for (int t = 0; t < DP / 16; ++t) o[t] = EP::mma16(vf[t], rest, o[t]);
-    }
+    for (int t = 0; t < DP / 16; ++t) o[t] = EP::mma16(vf[t], rest, o[t]);
 }
 
 // DIRECT: one workgroup to a unit, no plan and no joining.
@@ -953,7 +953,7 @@ __global__ __launch_bounds__(64 * dec_waves(KV8, DIRECT)) void attn_decode_kerne
             __syncthreads();
         }
 
-        // join the four waves: each writes its rows over its own ring
+        // join the waves: each writes its rows over its own ring
         sum += __shfl_xor(sum, 16);
         sum += __shfl_xor(sum, 32);
         wait_lds();
