@@ -110,7 +110,7 @@ typedef struct {
     int32_t* table;         /* [rows, width] */
     int64_t ld_table;
     int32_t* lens;          /* [rows] */
-    int64_t rows, width;
+    int64_t rows, width;    /* no rows: the four calls below do nothing */
 } mpdt_pages;
 
 /* Bytes of workspace for each of the four below (cache_free needs none). */

@@ -71,7 +71,9 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
     const int per_row = a.kv.dim / 8, per_tok = a.kv.kv_heads * per_row;
     const bool bf16 = a.type == DT_BF16;
     const int n = 2 * APPEND_TOKENS * per_tok;
-    // eight loads of a thread at a time, then their stores
+    // eight loads of a thread at a time, then their stores: all of a workgroup's where
+    // a token is 8 heads of 128 (smaller rows leave slots empty, which read the last
+    // piece again)
     constexpr int U = 8;
     for (int i0 = threadIdx.x; i0 < n; i0 += 256 * U) {
         u32x4 x[U];

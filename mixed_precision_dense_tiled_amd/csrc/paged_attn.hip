@@ -168,7 +168,7 @@ __device__ __forceinline__ void global_to_lds16(const char* src, MPDT_LDS char* 
 }
 
 // The same from a scalar base and a 32-bit offset per lane.  ONCE: the bytes
-// are read once (non-temporal).
+// are read once (non-temporal), by all but sequences of more than 16 rows.
 template <bool ONCE = false>
 __device__ __forceinline__ void global_to_lds16(const char* base, uint32_t off, MPDT_LDS char* dst) {
     if constexpr (ONCE)

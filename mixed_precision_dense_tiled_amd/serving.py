@@ -5,7 +5,9 @@ pages, and log probabilities of given tokens with their gradient.
 As for the rest of the package, these functions marshal arguments, allocate
 outputs and workspaces with torch, and run on torch's current stream without
 synchronising.  Numbers that live on the device (page numbers, lengths,
-offsets) are not read here; the kernels cut them to the buffers.
+offsets) are not read here; the kernels cut them to the buffers.  None of them
+takes part in torch's autograd: results are detached from logits, q or caches that
+require a gradient, and token_logprobs_backward is a call of its own.
 """
 from __future__ import annotations
 
@@ -195,7 +197,8 @@ def paged_attention(q, k_cache, v_cache, table, cu_q, lens, scale=None, softcap=
     softcap > 0 softcap * tanh(score / softcap).  Returns out [tokens, heads,
     dim] in q's type, with return_lse (or an lse buffer) also the FP32
     [tokens, heads] log of the sum of exp(scores).  A token that sees no key
-    gets 0 and -inf; rows of q that belong to no sequence are not written."""
+    gets 0 and -inf; rows of q that belong to no sequence are not written.  There
+    is no gradient: the outputs are detached from q and the cache."""
     if q.dim() != 3:
         raise ValueError("q must be [tokens, heads, dim]")
     tokens, heads, dim = q.shape
@@ -341,7 +344,9 @@ def token_logprobs(logits, targets, top_k=0):
     [rows] = -sum p log p, all FP32, and with top_k (at most 64 and vocab)
     top_logprobs FP32 and top_indices INT64 [rows, top_k], largest first, ties
     to the lower index (None otherwise).  -inf logits have p = 0; a row of
-    nothing else has lse = -inf, entropy 0 and log probabilities -inf."""
+    nothing else has lse = -inf, entropy 0 and log probabilities -inf.  Results
+    are detached from logits that require a gradient: token_logprobs_backward
+    gives it."""
     rows, vocab, code, ld, pt = _logits(logits, targets)
     if not 0 <= top_k <= min(64, vocab):
         raise ValueError("top_k must be at most 64 and at most the vocabulary")
