@@ -549,9 +549,10 @@ struct Score {
 __device__ __forceinline__ Score score_of(const AttnArgs& a, float k_scale) {
     Score s;
     s.mul = a.scale * k_scale * LOG2E;
-    // (held finite: a product of zero stays a score of zero)
     s.cap2 = fminf(a.softcap * LOG2E, 3e38f);
-    s.inner = a.softcap > 0.0f ? fminf(fmaxf(2.0f * LOG2E * a.scale * k_scale / a.softcap, -3e38f), 3e38f) : 0.0f;
+    s.inner = a.softcap > 0.0f ? 2.0f * LOG2E * a.scale * k_scale / a.softcap : 0.0f;
+    // (held finite, so that a product of zero stays a score of zero; NaN stays)
+    s.inner = s.inner > 3e38f ? 3e38f : s.inner < -3e38f ? -3e38f : s.inner;
     return s;
 }
 // How scores are capped.  CAP_ANY, right for every cap: from |y| = 1/2 on tanh(y) = 1 -
@@ -562,8 +563,8 @@ __device__ __forceinline__ Score score_of(const AttnArgs& a, float k_scale) {
 // through.  CAP_NEAR: the first form alone, whose error of up to 2^-22 of the cap is, up
 // to CAP_NEAR_MOST, 2^-16 of a weight, 1/16 of its rounding to FP16.  The kernel of
 // few rows waits for memory and takes CAP_ANY throughout (64 sequences: 198 us with
-// either); the kernel of many rows is bound by its vector operations (17 sequences in
-// FP16, dim 64: CAP_NEAR 126 us, CAP_ANY 148 under a cap of 100, 179 where every
+// either); the kernel of many rows waits for its softmax (17 sequences in FP16,
+// dim 64: CAP_NEAR 126 us, CAP_ANY 148 under a cap of 100, 179 where every
 // score passes 1/2).
 enum : int { CAP_NONE = 0, CAP_NEAR = 1, CAP_ANY = 2 };
 constexpr float CAP_NEAR_MOST = 64.0f;
@@ -1500,12 +1501,14 @@ __global__ __launch_bounds__(64 * CHK_WAVES) __attribute__((amdgpu_waves_per_eu(
         const int qpos = past + tok, qlow = a.window > 0 ? qpos - a.window : -1;
         Score sc = score_of(a, KV8 ? uni(a.kv.k_scale[h]) : 1.0f);
         // the largest score is the factor times the largest product where the
-        // factor is positive: a negative one goes to q's signs, a zero to q
+        // factor is positive: a negative one goes to q's signs, a zero to q, and one
+        // that is no number too (hidden keys keep their -inf)
         uint32_t keep = 0xffffffffu, flip = 0;
         if constexpr (CAP == CAP_NONE) {
             if (sc.mul < 0.0f) flip = 0x80008000u;
-            if (sc.mul == 0.0f) keep = 0;
-            sc.mul = sc.mul == 0.0f ? 1.0f : fabsf(sc.mul);
+            if (!(fabsf(sc.mul) > 0.0f)) keep = 0;
+            if (sc.mul != sc.mul) flip = 0x7fff7fffu;
+            sc.mul = fabsf(sc.mul) > 0.0f ? fabsf(sc.mul) : 1.0f;
         }
         u32x4 qf[DP / 16];
 #pragma unroll

@@ -97,3 +97,18 @@ def test_caps_over_wide_heads(gpu_ok, dim, dtype, fp8, seqs):
     out, lse, tol, tol_lse = capped(b, 4.0, 0.2, window=250)
     close(got[1], lse, tol_lse, "lse")
     close(got[0], out, tol, "out")
+
+
+@pytest.mark.parametrize("softcap", [0.0, 5.0, 1e4])
+@pytest.mark.parametrize("seqs", [ONE_LAUNCH, SHARED_OUT, CHUNKS], ids=["one_launch", "shared_out", "chunks"])
+def test_a_head_whose_scale_is_no_number(gpu_ok, softcap, seqs):
+    """Its outputs are none, with a cap as without one; the other head's are as ever."""
+    b = Batch(seqs, 4, 2, 64, 16, bf16, True, seed=43)
+    some = torch.cat([torch.arange(n - nq, n) >= 0 for nq, n in seqs if nq])
+    g = b.gpu()
+    want = mp.paged_attention(**g, return_lse=True, softcap=softcap)
+    g["k_scale"][1] = math.nan
+    out, lse = mp.paged_attention(**g, return_lse=True, softcap=softcap)
+    assert torch.equal(out[:, :2], want[0][:, :2]) and torch.equal(lse[:, :2], want[1][:, :2])
+    assert out[some][:, 2:].isnan().all() and lse[some][:, 2:].isnan().all()
+    assert (out[~some] == 0).all() and (lse[~some] == -math.inf).all()
