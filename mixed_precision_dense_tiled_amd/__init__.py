@@ -25,6 +25,8 @@ __all__ = ["gemm_f16", "gemm_bf16", "gemm_f16_f16out", "gemm_bf16_bf16out", "gem
            "quantize_fp8_blocks", "quantize_fp8",
            "paged_kv_append", "paged_attention", "cache_fork", "cache_extend", "cache_free",
            "cache_compact", "token_logprobs", "token_logprobs_backward", "TokenLogprobs",
+           "rms_norm", "rms_norm_backward", "RmsNorm", "paged_kv_append_rope", "gemm_grouped",
+           "gemm_grouped_wgrad", "gemm_grouped_w8a8",
            "MpdtError", "lib", "lib_path", "version"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -547,3 +549,5 @@ def quantize_fp8(X, fmt, block_rows, block_cols, q_out=None, scales_out=None):
 
 from .serving import (TokenLogprobs, cache_compact, cache_extend, cache_fork, cache_free,  # noqa: E402
                       paged_attention, paged_kv_append, token_logprobs, token_logprobs_backward)
+from .layers import (RmsNorm, gemm_grouped, gemm_grouped_w8a8, gemm_grouped_wgrad,  # noqa: E402
+                     paged_kv_append_rope, rms_norm, rms_norm_backward)

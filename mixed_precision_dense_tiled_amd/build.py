@@ -24,6 +24,9 @@ HIP_SOURCES = ["abi.hip", "gemm.hip", "gemm_epi.hip", "gemm_fp8.hip", "gemm_fp8_
 # The serving operators (include/mpdt_serving.h), in libmpdt.so beside the above.
 SERVING_SOURCES = ["serving_abi.hip", "paged_attn.hip", "kv_cache.hip", "logprobs.hip"]
 
+# A decoder layer's operators (include/mpdt_layers.h), in libmpdt.so as well.
+LAYER_SOURCES = ["layers_abi.hip", "rms_norm.hip", "rotary.hip", "grouped.hip"]
+
 # Per-source device-compiler options.  The one-wave FP8 GEMM rescales its MFMA
 # block sums with FP32 FMAs every K tile; VALU instructions cannot read AGPRs,
 # so its MFMAs are built in the form that writes VGPRs.
@@ -76,7 +79,7 @@ def _link(out: str, sources, extra_flags=()) -> str:
 
 
 def build_library(extra_flags=()) -> str:
-    return _link(LIB, HIP_SOURCES + SERVING_SOURCES, extra_flags)
+    return _link(LIB, HIP_SOURCES + SERVING_SOURCES + LAYER_SOURCES, extra_flags)
 
 
 CLOCK_LIB = os.path.join(PKG, "libmpdt_clock.so")
@@ -106,7 +109,7 @@ def build_oracle() -> str:
 def build_all():
     build_oracle()
     # the three HIP libraries in one compile pool
-    _build_libs([(LIB, HIP_SOURCES + SERVING_SOURCES, ()), (PROBE_LIB, ["probes.hip"], ()),
+    _build_libs([(LIB, HIP_SOURCES + SERVING_SOURCES + LAYER_SOURCES, ()), (PROBE_LIB, ["probes.hip"], ()),
                  (CLOCK_LIB, HIP_SOURCES, ("-DMPDT_CLOCK_STAMPS",))])
 
 

@@ -13,19 +13,13 @@
 #include <algorithm>
 
 #include "device_common.hpp"
+#include "kv_places.hpp"
 #include "serving.hpp"
 
 namespace mpdt {
 namespace {
 
 // ---- new keys and values into their pages ----------------------------------------
-
-__device__ __forceinline__ float widen(uint16_t x, bool bf16) {
-    return bf16 ? __uint_as_float((uint32_t)x << 16) : (float)__builtin_bit_cast(_Float16, x);
-}
-
-// x / scale, cut to the format's range (NaN stays), rounded to nearest even.
-__device__ __forceinline__ float cut448(float x) { return x > 448.0f ? 448.0f : x < -448.0f ? -448.0f : x; }
 
 // APPEND_TOKENS tokens to a workgroup: one lane each finds where its token belongs,
 // then all threads move the rows, 8 elements at a time.  8800 tokens of 8 heads of
@@ -36,36 +30,9 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
     __shared__ int64_t dst[APPEND_TOKENS];
     const int t0 = blockIdx.x * APPEND_TOKENS;
     if (threadIdx.x < 64) {
-        // one wave finds each token's sequence, the last that starts at or before
-        // it: among up to 64 in one look (a lane each), else by halves
-        const int lane = threadIdx.x, t = t0 + lane;
-        int seq = 0;
-        if (a.sv.seqs <= 64) {
-            const int start = lane < a.sv.seqs ? a.sv.cu_q[lane] : 0x7fffffff;
-#pragma unroll
-            for (int k = 0; k < APPEND_TOKENS; ++k) {
-                const int upto = __popcll(__ballot(start <= t0 + k));
-                if (lane == k) seq = upto > 0 ? upto - 1 : 0;
-            }
-        } else if (lane < APPEND_TOKENS) {
-            int hi = a.sv.seqs;
-            while (hi - seq > 1) {
-                const int mid = (seq + hi) / 2;
-                if (a.sv.cu_q[mid] <= t) seq = mid;
-                else hi = mid;
-            }
-        }
-        if (lane < APPEND_TOKENS) {
-            int64_t off = -1;
-            const Seq s = seq_of(a.sv, a.kv.page_size, seq);
-            const int pos = s.n - (s.start + s.nq - t);
-            if (t >= s.start && t < s.start + s.nq && pos >= 0) {
-                const int pi = a.kv.page_of(pos);
-                const int pg = a.sv.table[(int64_t)seq * a.sv.ld_table + pi];
-                if (pg >= 0 && pg < a.kv.pages) off = pg * a.kv.page_b + (pos - pi * a.kv.page_size) * a.kv.slot_b;
-            }
-            dst[lane] = off;
-        }
+        const int lane = threadIdx.x;
+        const Place p = place_of<APPEND_TOKENS>(a.kv, a.sv, t0, lane);
+        if (lane < APPEND_TOKENS) dst[lane] = p.off;
     }
     __syncthreads();
     const int per_row = a.kv.dim / 8, per_tok = a.kv.kv_heads * per_row;

@@ -1,0 +1,408 @@
+// rms_norm.hip -- root-mean-square norm of rows, with the residual's addition and
+// an output in the rows' type, in INT8 or in E4M3 with scales; and its gradient.
+//
+//   h = x + residual,  rstd = 1 / sqrt(mean h^2 + eps),  y = (h * rstd) * w
+//
+// Bound by the bytes that it moves: each row is read once, kept in registers (a
+// thread holds PIECES pieces of 8 neighbouring elements), reduced once for rstd
+// and once for a scale a row, and written once.  The squares are added in FP64:
+// a square of a 24-bit number is exact there and the sum's order does not show in
+// rstd, so that a code next to a border between two codes does not depend on how
+// many threads share a row.  At two FP64 operations an element that costs a tenth
+// of the time in which the bytes move.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_common.hpp"
+#include "layers.hpp"
+
+namespace mpdt {
+namespace {
+
+// Loads and stores of 8 elements from any element-aligned address.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+
+// 8 elements of a row as they are stored: 4 or 8 registers.
+template <int T> struct Piece {
+    static constexpr int ES = T == DT_F32 ? 4 : 2;
+    static constexpr int W = 2 * ES;
+    uint32_t w[W];
+
+    __device__ __forceinline__ void load(const char* p, int n) {   // n elements of 8, the rest 0
+        if (n >= 8) {
+#pragma unroll
+            for (int i = 0; i < W / 4; ++i) {
+                const u32x4_any v = *reinterpret_cast<const u32x4_any*>(p + 16 * i);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[4 * i + j] = v[j];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i) w[i] = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < n) {
+                    if constexpr (ES == 4) w[e] = reinterpret_cast<const uint32_t*>(p)[e];
+                    else w[e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[e] << (16 * (e & 1));
+                }
+        }
+    }
+    __device__ __forceinline__ void store(char* p, int n) const {
+        if (n >= 8) {
+#pragma unroll
+            for (int i = 0; i < W / 4; ++i)
+                *reinterpret_cast<u32x4_any*>(p + 16 * i) = u32x4_any{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < n) {
+                    if constexpr (ES == 4) reinterpret_cast<uint32_t*>(p)[e] = w[e];
+                    else reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+                }
+        }
+    }
+    __device__ __forceinline__ float get(int e) const {
+        if constexpr (T == DT_F32) return __uint_as_float(w[e]);
+        else if constexpr (T == DT_BF16) return __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
+        else return (float)__builtin_bit_cast(_Float16, (uint16_t)(w[e >> 1] >> (16 * (e & 1))));
+    }
+    __device__ __forceinline__ void put(int e, float x) {   // rounded once to the type
+        if constexpr (T == DT_F32) {
+            w[e] = __float_as_uint(x);
+        } else {
+            // (the FP32 value first: a product that is fused with the conversion to
+            // FP16 is rounded only once)
+            if constexpr (T == DT_F16) asm("" : "+v"(x));
+            const uint32_t b = T == DT_BF16 ? f32_to_bf16_bits(x) : f32_to_f16_bits(x);
+            w[e >> 1] = e & 1 ? (w[e >> 1] & 0xffffu) | b << 16 : (w[e >> 1] & 0xffff0000u) | b;
+        }
+    }
+};
+
+// 8 weights as FP32.
+template <int T>
+__device__ __forceinline__ void load_weight(const char* p, int w_f32, int e0, int n, float (&w)[8]) {
+    if (T == DT_F32 || w_f32) {
+        Piece<DT_F32> v;
+        v.load(p + 4 * (int64_t)e0, n);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = v.get(e);
+    } else {
+        Piece<T> v;
+        v.load(p + 2 * (int64_t)e0, n);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = v.get(e);
+    }
+}
+
+// The larger of two magnitudes; NaN where either is.
+__device__ __forceinline__ float larger(float a, float b) { return a >= b ? a : (b == b ? (a == a ? b : a) : b); }
+
+template <class V, class F>
+__device__ __forceinline__ V over_lanes(V v, int from, F f) {
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1)
+        if (m <= from) v = f(v, __shfl_xor(v, m, 64));
+    return v;
+}
+
+// v of every thread, joined in one order whatever the threads' timing.
+template <int NT, class V, class F>
+__device__ __forceinline__ V over_row(V v, V* red, F f) {
+    v = over_lanes(v, 32, f);
+    if constexpr (NT > 64) {
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = red[0];
+#pragma unroll
+        for (int i = 1; i < NT / 64; ++i) v = f(v, red[i]);
+    }
+    return v;
+}
+
+// The scale of values up to amax; NaN stays.
+__device__ __forceinline__ float scale_of(float amax, float qmax) {
+    const float s = amax / qmax;
+    return s == 0.0f ? 1.0f : s;
+}
+__device__ __forceinline__ float cut(float x, float most) { return x > most ? most : x < -most ? -most : x; }
+
+// NT threads to a row (64: four rows to a workgroup of 256).
+template <int T, int QUANT, int NT, int PIECES>
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(NormArgs a) {
+    __shared__ double red_d[NT / 64];
+    __shared__ float red_f[NT / 64];
+    constexpr int ROWS = NT < 256 ? 256 / NT : 1;
+    const int tid = threadIdx.x % NT;
+    const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / NT;
+    if (row >= a.rows) return;   // (whole waves; rows that share a workgroup share no barrier)
+    const char* x = a.x + row * a.x_b;
+    Piece<T> h[PIECES];
+#pragma unroll
+    for (int u = 0; u < PIECES; ++u) {
+        const int e0 = 8 * (tid + NT * u);
+        h[u].load(x + (int64_t)e0 * Piece<T>::ES, a.dim - e0);
+    }
+    if (a.residual) {
+        const char* r = a.residual + row * a.res_b;
+        Piece<T> p[PIECES];
+#pragma unroll
+        for (int u = 0; u < PIECES; ++u) {
+            const int e0 = 8 * (tid + NT * u);
+            p[u].load(r + (int64_t)e0 * Piece<T>::ES, a.dim - e0);
+        }
+#pragma unroll
+        for (int u = 0; u < PIECES; ++u)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[u].put(e, h[u].get(e) + p[u].get(e));
+        if (a.h) {
+#pragma unroll
+            for (int u = 0; u < PIECES; ++u) {
+                const int e0 = 8 * (tid + NT * u);
+                h[u].store(a.h + row * a.h_b + (int64_t)e0 * Piece<T>::ES, a.dim - e0);
+            }
+        }
+    }
+    double sum = 0;
+#pragma unroll
+    for (int u = 0; u < PIECES; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const double v = h[u].get(e);
+            sum = __builtin_fma(v, v, sum);
+        }
+    sum = over_row<NT>(sum, red_d, [](double p, double q) { return p + q; });
+    const float rstd = (float)(1.0 / sqrt(sum / a.dim + a.eps));
+    if (a.rstd && tid == 0) a.rstd[row] = rstd;
+
+    float y[PIECES][8];
+#pragma unroll
+    for (int u = 0; u < PIECES; ++u) {
+        const int e0 = 8 * (tid + NT * u);
+        float w[8];
+        load_weight<T>(a.weight, a.w_f32, e0, a.dim - e0, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[u][e] = mul_rn(mul_rn(h[u].get(e), rstd), w[e]);
+    }
+    char* out = a.out + row * a.out_b;
+    if constexpr (QUANT == NORM_PLAIN) {
+#pragma unroll
+        for (int u = 0; u < PIECES; ++u) {
+            const int e0 = 8 * (tid + NT * u);
+            Piece<T> o;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o.put(e, y[u][e]);
+            o.store(out + (int64_t)e0 * Piece<T>::ES, a.dim - e0);
+        }
+    } else {
+        constexpr float QMAX = QUANT == NORM_I8_ROWS ? 127.0f : 448.0f;
+        float amax[PIECES], scale = 1.0f;
+        // (past the row's end a piece holds 0 * rstd: an amax of 0, or NaN where rstd
+        // is, as it is in the whole row then)
+#pragma unroll
+        for (int u = 0; u < PIECES; ++u) {
+            amax[u] = fabsf(y[u][0]);
+#pragma unroll
+            for (int e = 1; e < 8; ++e) amax[u] = larger(amax[u], fabsf(y[u][e]));
+        }
+        if constexpr (QUANT != NORM_E4M3_BLOCKS) {
+            float m = amax[0];
+#pragma unroll
+            for (int u = 1; u < PIECES; ++u) m = larger(m, amax[u]);
+            scale = scale_of(over_row<NT>(m, red_f, [](float p, float q) { return larger(p, q); }), QMAX);
+            if (tid == 0) a.scales[row * a.ld_scales] = scale;
+        }
+#pragma unroll
+        for (int u = 0; u < PIECES; ++u) {
+            const int e0 = 8 * (tid + NT * u);
+            const int n = a.dim - e0;
+            if constexpr (QUANT == NORM_E4M3_BLOCKS) {
+                // 16 lanes hold a block of 128
+                scale = scale_of(over_lanes(amax[u], 8, [](float p, float q) { return larger(p, q); }), QMAX);
+                if ((tid & 15) == 0 && n > 0) a.scales[row * a.ld_scales + e0 / 128] = scale;
+            }
+            uint32_t code[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float q[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) q[j] = cut(y[u][4 * i + j] / scale, QMAX);
+                if constexpr (QUANT == NORM_I8_ROWS) {
+                    code[i] = 0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int c = q[j] == q[j] ? (int)__builtin_rintf(q[j]) : 0;
+                        code[i] |= (uint32_t)(c & 0xff) << (8 * j);
+                    }
+                } else {
+                    int p = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+                    code[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], p, true);
+                }
+            }
+            if (n >= 8) {
+                *reinterpret_cast<u32x2_any*>(out + e0) = u32x2_any{code[0], code[1]};
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e < n) out[e0 + e] = (char)(code[e >> 2] >> (8 * (e & 3)));
+            }
+        }
+    }
+}
+
+// f(threads to a row, pieces of a thread) for rows of dim elements.
+template <class F>
+hipError_t by_width(int dim, F f) {
+    using std::integral_constant;
+#define MPDT_W(nt, p) return f(integral_constant<int, nt>{}, integral_constant<int, p>{})
+    if (dim <= 512) MPDT_W(64, 1);
+    if (dim <= 1024) MPDT_W(64, 2);
+    if (dim <= 2048) MPDT_W(256, 1);
+    if (dim <= 4096) MPDT_W(256, 2);
+    if (dim <= 8192) MPDT_W(256, 4);
+    if (dim <= 16384) MPDT_W(1024, 2);
+    MPDT_W(1024, 4);
+#undef MPDT_W
+}
+
+template <int T>
+hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
+    return by_width(a.dim, [&](auto NT, auto P) {
+        constexpr int nt = decltype(NT)::value, p = decltype(P)::value;
+        constexpr int rows = nt < 256 ? 256 / nt : 1;
+        const dim3 grid((unsigned)((a.rows + rows - 1) / rows)), block(nt < 256 ? 256 : nt);
+        switch (a.quant) {
+            case NORM_PLAIN: rms_norm_kernel<T, NORM_PLAIN, nt, p><<<grid, block, 0, stream>>>(a); break;
+            case NORM_I8_ROWS: rms_norm_kernel<T, NORM_I8_ROWS, nt, p><<<grid, block, 0, stream>>>(a); break;
+            case NORM_E4M3_ROWS: rms_norm_kernel<T, NORM_E4M3_ROWS, nt, p><<<grid, block, 0, stream>>>(a); break;
+            default: rms_norm_kernel<T, NORM_E4M3_BLOCKS, nt, p><<<grid, block, 0, stream>>>(a); break;
+        }
+        return hipGetLastError();
+    });
+}
+
+// ---- gradient ------------------------------------------------------------------
+
+// Each workgroup walks rows of its own and keeps its columns' sums of grad * h * rstd
+// in registers; a second launch adds the workgroups' sums in their order.
+constexpr int GRAD_GROUPS = 512;
+int grad_groups(int64_t rows) { return (int)(rows < GRAD_GROUPS ? rows : GRAD_GROUPS); }
+
+template <int T, int NT, int PIECES>
+__global__ __launch_bounds__(NT) void rms_norm_grad_kernel(NormGradArgs a) {
+    __shared__ float red[2][NT / 64];
+    const int tid = threadIdx.x;
+    constexpr int ES = Piece<T>::ES;
+    float dw[PIECES][8];
+#pragma unroll
+    for (int u = 0; u < PIECES; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[u][e] = 0;
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+        Piece<T> g[PIECES], h[PIECES], r[PIECES];
+#pragma unroll
+        for (int u = 0; u < PIECES; ++u) {
+            const int e0 = 8 * (tid + NT * u);
+            g[u].load(a.grad + row * a.grad_b + (int64_t)e0 * ES, a.dim - e0);
+            h[u].load(a.h + row * a.h_b + (int64_t)e0 * ES, a.dim - e0);
+            if (a.grad_res) r[u].load(a.grad_res + row * a.gres_b + (int64_t)e0 * ES, a.dim - e0);
+        }
+        const float rstd = a.rstd[row];
+        float c = 0;
+#pragma unroll
+        for (int u = 0; u < PIECES; ++u) {
+            const int e0 = 8 * (tid + NT * u);
+            float w[8];
+            load_weight<T>(a.weight, a.w_f32, e0, a.dim - e0, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float v = g[u].get(e), x = h[u].get(e);
+                c += v * w[e] * x;
+                dw[u][e] += v * (x * rstd);
+            }
+        }
+        // (two sets of partial sums in turn: one barrier a row)
+        c = over_row<NT>(c, red[turn], [](float p, float q) { return p + q; });
+        c = rstd * rstd * (c / a.dim);
+#pragma unroll
+        for (int u = 0; u < PIECES; ++u) {
+            const int e0 = 8 * (tid + NT * u);
+            float w[8];
+            load_weight<T>(a.weight, a.w_f32, e0, a.dim - e0, w);
+            Piece<T> o;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float d = rstd * (g[u].get(e) * w[e] - h[u].get(e) * c);
+                if (a.grad_res) d += r[u].get(e);
+                o.put(e, d);
+            }
+            o.store(a.grad_h + row * a.gh_b + (int64_t)e0 * ES, a.dim - e0);
+        }
+    }
+    float* to = gridDim.x == 1 ? a.grad_weight : a.ws + (int64_t)blockIdx.x * a.dim;
+#pragma unroll
+    for (int u = 0; u < PIECES; ++u) {
+        const int e0 = 8 * (tid + NT * u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e0 + e < a.dim) to[e0 + e] = dw[u][e];
+    }
+}
+
+// Columns' sums of the workgroups: 64 columns to a workgroup, its four waves a
+// quarter of the rows each, joined in order.
+__global__ __launch_bounds__(256) void rms_norm_grad_sum_kernel(const float* ws, int groups, int dim, float* out) {
+    __shared__ float part[4][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = blockIdx.x * 64 + lane;
+    float s = 0;
+    if (col < dim)
+        for (int i = groups * wave / 4; i < groups * (wave + 1) / 4; ++i) s += ws[(int64_t)i * dim + col];
+    part[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && col < dim) out[col] = ((part[0][lane] + part[1][lane]) + part[2][lane]) + part[3][lane];
+}
+
+template <int T>
+hipError_t launch_grad(const NormGradArgs& a, int groups, hipStream_t stream) {
+    const auto go = [&](auto NT, auto P) {
+        constexpr int nt = decltype(NT)::value, p = decltype(P)::value;
+        rms_norm_grad_kernel<T, nt, p><<<dim3(groups), dim3(nt), 0, stream>>>(a);
+        return hipGetLastError();
+    };
+    using std::integral_constant;
+    if (a.dim <= 512) return go(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+    if (a.dim <= 2048) return go(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+    if (a.dim <= 4096) return go(integral_constant<int, 512>{}, integral_constant<int, 1>{});
+    if (a.dim <= 8192) return go(integral_constant<int, 512>{}, integral_constant<int, 2>{});
+    if (a.dim <= 16384) return go(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+    return go(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm(const NormArgs& a, hipStream_t stream) {
+    return a.type == DT_F32 ? launch_norm<DT_F32>(a, stream)
+           : a.type == DT_BF16 ? launch_norm<DT_BF16>(a, stream) : launch_norm<DT_F16>(a, stream);
+}
+
+int64_t rms_norm_backward_ws(int64_t rows, int64_t dim) {
+    const int g = grad_groups(rows);
+    return g > 1 ? 4 * g * dim : 0;
+}
+
+hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t stream) {
+    const int groups = grad_groups(a.rows);
+    if (groups > 0) {
+        const hipError_t e = a.type == DT_F32 ? launch_grad<DT_F32>(a, groups, stream)
+                             : a.type == DT_BF16 ? launch_grad<DT_BF16>(a, groups, stream)
+                                                 : launch_grad<DT_F16>(a, groups, stream);
+        if (e != hipSuccess || groups == 1) return e;
+    }
+    // (no rows: sums of nothing)
+    rms_norm_grad_sum_kernel<<<dim3((a.dim + 63) / 64), dim3(256), 0, stream>>>(a.ws, groups, a.dim, a.grad_weight);
+    return hipGetLastError();
+}
+
+}  // namespace mpdt

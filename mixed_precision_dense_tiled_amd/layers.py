@@ -1,0 +1,370 @@
+"""The operators of libmpdt.so that a decoder layer has around its linear layers
+and its cache (see include/mpdt_layers.h): the root-mean-square norm with the
+residual's addition and an output in 8 bits, and its gradient; new keys rotated
+on their way into a paged cache with the queries beside them; and products
+grouped by expert, with their gradients and in W8A8.
+
+As for the rest of the package, these functions marshal arguments, allocate
+outputs and workspaces with torch, and run on torch's current stream (of the
+tensors' device) without synchronising.  Numbers that live on the device (page
+numbers, lengths, offsets) are not read here; the kernels cut them to the
+buffers.  None of them takes part in torch's autograd: results are detached from
+inputs that require a gradient, and gradients are calls of their own.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from collections import namedtuple
+
+import torch
+
+from . import MpdtError, _check, _dims2, _same_device, _shape, _stream, lib
+from .serving import _DTYPE, _cache_and_batch, _floats, _ints, _PagedKV, _rows3, _Sequences
+
+__all__ = ["rms_norm", "rms_norm_backward", "RmsNorm", "paged_kv_append_rope", "gemm_grouped",
+           "gemm_grouped_wgrad", "gemm_grouped_w8a8"]
+
+_i64, _vp, _int, _f64 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_double
+
+# what rms_norm writes: the C ABI's mpdt_norm_out
+_NORM_OUT = {None: 0, "int8": 1, "fp8_rows": 2, "fp8_blocks": 3}
+
+RmsNorm = namedtuple("RmsNorm", "out scales residual rstd")
+
+_native = None
+
+
+def _lib():
+    """The native library with these entry points' signatures set."""
+    global _native
+    if _native is None:
+        L = lib()
+        kv, sq = ctypes.POINTER(_PagedKV), ctypes.POINTER(_Sequences)
+        for name, res, args in (
+                ("rms_norm", _int, [_int, _i64, _i64, _vp, _i64, _vp, _i64, _int, _vp, _f64, _int, _vp, _i64, _vp,
+                                    _i64, _vp, _i64, _vp, _vp]),
+                ("rms_norm_backward_workspace", _i64, [_i64, _i64]),
+                ("rms_norm_backward", _int, [_int, _i64, _i64, _vp, _i64, _vp, _i64, _int, _vp, _vp, _vp, _i64, _vp,
+                                             _i64, _vp, _vp, _i64, _vp]),
+                ("paged_kv_append_rope", _int, [kv, sq, _int, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _int,
+                                                _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp]),
+                ("gemm_grouped", _int, [_int, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _int, _vp, _vp,
+                                        _i64, _int, _vp]),
+                ("gemm_grouped_wgrad", _int, [_int, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64,
+                                              _i64, _int, _vp]),
+                ("gemm_grouped_w8a8", _int, [_i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _i64,
+                                             _vp, _i64, _vp, _vp, _i64, _vp])):
+            fn = getattr(L, name)
+            fn.restype, fn.argtypes = res, args
+        _native = L
+    return _native
+
+
+def _mat(t, dtype, name):
+    """(pointer, leading dimension) of a row-major matrix of exactly this type."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    rows, cols = t.shape
+    s0, s1 = t.stride()
+    if cols > 1 and s1 != 1:
+        raise ValueError(f"{name} must have unit stride along its rows")
+    # (a stride over one row says nothing)
+    return t.data_ptr(), s0 if rows > 1 else max(cols, 1)
+
+
+def _stack(t, dtype, name):
+    """(pointer, leading dimension, stride between matrices) of [groups, rows, cols]."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be 3-D")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    groups, rows, cols = t.shape
+    s0, s1, s2 = t.stride()
+    if cols > 1 and s2 != 1:
+        raise ValueError(f"{name} must have unit stride along its rows")
+    return t.data_ptr(), s1 if rows > 1 else max(cols, 1), s0 if groups > 1 else 0
+
+
+def _on(ref, name, *ts):
+    """All on ref's GPU, which is the current device within this context."""
+    _same_device(ref, *ts)
+    if not ref.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return contextlib.nullcontext() if ref.get_device() == torch.cuda.current_device() else \
+        torch.cuda.device(ref.device)
+
+
+def _norm_operands(x, weight, name):
+    rows, dim = _dims2(x, name)
+    code = _DTYPE.get(x.dtype)
+    if code is None or code == 3:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {x.dtype}")
+    if weight.dtype not in (x.dtype, torch.float32):
+        raise TypeError(f"weight must be {x.dtype} or torch.float32, got {weight.dtype}")
+    _shape(weight, (dim,), "weight")
+    if not weight.is_contiguous():
+        raise ValueError("weight must be contiguous")
+    return rows, dim, code, _DTYPE[weight.dtype]
+
+
+def rms_norm(x, weight, eps=1e-6, residual=None, quant=None, return_rstd=False, out=None, scales_out=None,
+             residual_out=None):
+    """Root-mean-square norm of rows, with the residual's addition before it and
+    an output in 8 bits after it.
+
+    x [rows, dim] BF16, FP16 or FP32 (rows may be strided), dim at most 32768;
+    weight [dim] in x's type or FP32; residual like x.  With h = x + residual,
+    rounded once to x's type (x alone without a residual), rstd = 1 /
+    sqrt(mean(h^2) + eps) and y = (h * rstd) * weight in FP32.  Returns RmsNorm:
+      out       y in x's type, or with quant codes of 8 bits: "int8" for
+                gemm_w8a8, "fp8_rows" (E4M3 in uint8) for gemm_fp8_rowscaled,
+                "fp8_blocks" (E4M3, 1 x 128 scales) for gemm_fp8_blockscaled
+      scales    FP32 [rows], with "fp8_blocks" [rows, ceil(dim / 128)]: the
+                largest |y| of the row or block over 127 or 448 (1 where that
+                is 0, NaN where the row or block holds one); None without quant
+      residual  h with a residual, else None
+      rstd      FP32 [rows] with return_rstd, else None.
+    residual_out may be x or residual itself, and out too without quant.  There is
+    no autograd here: rms_norm_backward gives the gradient."""
+    rows, dim, code, w_code = _norm_operands(x, weight, "x")
+    if quant not in _NORM_OUT:
+        raise ValueError(f"quant must be one of None, 'int8', 'fp8_rows', 'fp8_blocks', got {quant!r}")
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    out_type = x.dtype if quant is None else torch.int8 if quant == "int8" else torch.uint8
+    grid = (rows, -(-dim // 128)) if quant == "fp8_blocks" else (rows,)
+    if quant is None and scales_out is not None:
+        raise ValueError("scales_out belongs to an output of 8 bits")
+    for t, shape, name in ((residual, (rows, dim), "residual"), (out, (rows, dim), "out"),
+                           (residual_out, (rows, dim), "residual_out"), (scales_out, grid, "scales_out")):
+        _shape(t, shape, name)
+    where = _on(x, "x", ("weight", weight), ("residual", residual), ("out", out), ("scales_out", scales_out),
+                ("residual_out", residual_out))
+    if dim == 0:
+        raise ValueError("x must have at least one column")
+    px, ldx = _mat(x, x.dtype, "x")
+    pr = ph = ps = pd = None
+    ldr = ldh = lds = dim
+    if residual is not None:
+        pr, ldr = _mat(residual, x.dtype, "residual")
+        if residual_out is None:
+            residual_out = torch.empty((rows, dim), dtype=x.dtype, device=x.device)
+        ph, ldh = _mat(residual_out, x.dtype, "residual_out")
+    if out is None:
+        out = torch.empty((rows, dim), dtype=out_type, device=x.device)
+    po, ldo = _mat(out, out_type, "out")
+    if quant is not None:
+        if scales_out is None:
+            scales_out = torch.empty(grid, dtype=torch.float32, device=x.device)
+        if quant == "fp8_blocks":
+            ps, lds = _mat(scales_out, torch.float32, "scales_out")
+        else:
+            ps, lds = _floats(scales_out, rows, "scales_out"), 1
+    rstd = torch.empty(rows, dtype=torch.float32, device=x.device) if return_rstd else None
+    if rstd is not None:
+        pd = rstd.data_ptr()
+    with where:
+        _check("rms_norm", _lib().rms_norm(code, rows, dim, px, ldx, pr, ldr, w_code, weight.data_ptr(), eps,
+                                           _NORM_OUT[quant], po, ldo, ps, lds, ph, ldh, pd, _stream(x)))
+    return RmsNorm(out, scales_out, residual_out, rstd)
+
+
+def rms_norm_backward(grad, h, weight, rstd, grad_residual=None, out=None):
+    """Gradient of rms_norm (without quant) in its normed rows and its weight.
+
+    grad [rows, dim]: the gradient in rms_norm's out; h: what was normed (its
+    residual field, or x without a residual); rstd FP32 [rows] as it gave it;
+    grad_residual, the gradient in the residual field, is added where given.
+    Returns (grad_h in h's type, which is the gradient in x and in residual
+    alike, and grad_weight FP32 [dim]).  out may be grad or grad_residual."""
+    rows, dim, code, w_code = _norm_operands(h, weight, "h")
+    for t, name in ((grad, "grad"), (grad_residual, "grad_residual"), (out, "out")):
+        _shape(t, (rows, dim), name)
+    where = _on(h, "h", ("grad", grad), ("weight", weight), ("rstd", rstd), ("grad_residual", grad_residual),
+                ("out", out))
+    if dim == 0:
+        raise ValueError("h must have at least one column")
+    pg, ldg = _mat(grad, h.dtype, "grad")
+    ph, ldh = _mat(h, h.dtype, "h")
+    pr, ldr = (None, dim) if grad_residual is None else _mat(grad_residual, h.dtype, "grad_residual")
+    pd = _floats(rstd, rows, "rstd")
+    if out is None:
+        out = torch.empty((rows, dim), dtype=h.dtype, device=h.device)
+    po, ldo = _mat(out, h.dtype, "out")
+    grad_weight = torch.empty(dim, dtype=torch.float32, device=h.device)
+    L = _lib()
+    size = L.rms_norm_backward_workspace(rows, dim)
+    if size < 0:
+        raise MpdtError("rms_norm_backward", 1, L.mpdt_last_error().decode())
+    ws = torch.empty(size, dtype=torch.uint8, device=h.device) if size else None
+    with where:
+        _check("rms_norm_backward",
+               L.rms_norm_backward(code, rows, dim, pg, ldg, ph, ldh, w_code, weight.data_ptr(), pd, pr, ldr, po, ldo,
+                                   grad_weight.data_ptr(), None if ws is None else ws.data_ptr(), size, _stream(h)))
+    return out, grad_weight
+
+
+def paged_kv_append_rope(q, k, v, k_cache, v_cache, table, cu_q, lens, inv_freq, interleaved=False, k_scale=None,
+                         v_scale=None, out=None):
+    """paged_kv_append with the keys rotated by their positions on the way, and
+    the queries beside them.
+
+    k, v, the cache, table, cu_q and lens as in paged_kv_append; inv_freq FP32
+    [pairs], 2 * pairs <= dim: pair i of a row at position p is turned by p *
+    inv_freq[i] (formed in FP64, so far positions keep their angle).  Pair i is
+    the elements (i, i + pairs), or with interleaved (2 i, 2 i + 1); elements
+    from 2 * pairs on stay.  The position of new token t of a sequence with n
+    tokens, nq of them new, is n - nq + t.  q [tokens, heads, dim] in k's type, or
+    None.  Returns the turned q (in out, which may be q itself; None without q):
+    rows that belong to no sequence are not written."""
+    if k.dim() != 3:
+        raise ValueError("k must be [tokens, kv_heads, dim]")
+    tokens = k.shape[0]
+    kv, sq = _cache_and_batch(k_cache, v_cache, table, cu_q, lens, tokens, k_scale, v_scale)
+    dtype = k.dtype
+    if dtype not in (torch.bfloat16, torch.float16) or (kv.dtype != 3 and dtype != k_cache.dtype):
+        raise TypeError(f"new keys of {dtype} do not go into a cache of {k_cache.dtype}")
+    shape = (tokens, kv.kv_heads, kv.dim)
+    pk, kt, kh = _rows3(k, shape, dtype, "k")
+    pv, vt, vh = _rows3(v, shape, dtype, "v")
+    if inv_freq.dim() != 1 or not 1 <= inv_freq.shape[0] <= kv.dim // 2:
+        raise ValueError(f"inv_freq must be 1-D with 1 to {kv.dim // 2} values")
+    pf = _floats(inv_freq, inv_freq.shape[0], "inv_freq")
+    heads, pq, qt, qh, po, ot, oh = 0, None, 0, 0, None, 0, 0
+    if q is None:
+        if out is not None:
+            raise ValueError("out belongs to q")
+    else:
+        if q.dim() != 3 or q.shape[1] == 0:
+            raise ValueError("q must be [tokens, heads, dim] with at least one head")
+        heads = q.shape[1]
+        pq, qt, qh = _rows3(q, (tokens, heads, kv.dim), dtype, "q")
+    where = _on(k, "k", ("q", q), ("v", v), ("k_cache", k_cache), ("v_cache", v_cache), ("table", table),
+                ("cu_q", cu_q), ("lens", lens), ("inv_freq", inv_freq), ("k_scale", k_scale), ("v_scale", v_scale),
+                ("out", out))
+    if q is not None:
+        if out is None:
+            out = torch.empty((tokens, heads, kv.dim), dtype=dtype, device=q.device)
+        po, ot, oh = _rows3(out, (tokens, heads, kv.dim), dtype, "out")
+    if tokens == 0:
+        return out      # (an empty tensor has no address)
+    with where:
+        _check("paged_kv_append_rope",
+               _lib().paged_kv_append_rope(kv, sq, _DTYPE[dtype], pk, kt, kh, pv, vt, vh, pf, inv_freq.shape[0],
+                                           int(bool(interleaved)), heads, pq, qt, qh, po, ot, oh, _stream(k)))
+    return out
+
+
+def _offsets(offsets):
+    """(pointer, groups) of the groups' borders."""
+    if offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError("offsets must be 1-D with groups + 1 values")
+    groups = offsets.shape[0] - 1
+    return _ints(offsets, (groups + 1,), "offsets"), groups
+
+
+def _half(t, name):
+    if t.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    return _DTYPE[t.dtype]
+
+
+def _out_type(out, dtype, d16):
+    """An output's type: the given buffer's, or by d16."""
+    kind = out.dtype if out is not None else dtype if d16 else torch.float32
+    if kind not in (dtype, torch.float32):
+        raise TypeError(f"out must be {dtype} or torch.float32, got {kind}")
+    return kind
+
+
+def gemm_grouped(A, B, offsets, trans_b=False, out=None, d16=False):
+    """Products grouped by expert: D[i] = A[i] . B[e] for the rows i of group e.
+
+    A [rows, K] BF16 or FP16, sorted by group: group e has the rows offsets[e] to
+    offsets[e + 1] (INT32 [groups + 1], ascending; empty groups are fine).  B
+    [groups, K, N] in A's type, or with trans_b [groups, N, K]; the matrices may
+    be strided.  Returns D [rows, N]: FP32, or A's type with d16 (or an out of
+    that type); sums are FP32 and rounded once.  Rows that belong to no group are
+    not written.
+
+    The gradient in A from the one in D, G, is gemm_grouped(G, B, offsets,
+    trans_b=not trans_b); the one in B is gemm_grouped_wgrad's."""
+    rows, K = _dims2(A, "A")
+    code = _half(A, "A")
+    poff, groups = _offsets(offsets)
+    pb, ldb, sb = _stack(B, A.dtype, "B")
+    N = B.shape[1 if trans_b else 2]
+    _shape(B, (groups, N, K) if trans_b else (groups, K, N), "B")
+    _shape(out, (rows, N), "out")
+    kind = _out_type(out, A.dtype, d16)
+    pa, lda = _mat(A, A.dtype, "A")
+    where = _on(A, "A", ("B", B), ("offsets", offsets), ("out", out))
+    if out is None:
+        out = torch.empty((rows, N), dtype=kind, device=A.device)
+    pd, ldd = _mat(out, kind, "out")
+    with where:
+        _check("gemm_grouped", _lib().gemm_grouped(code, groups, rows, N, K, pa, lda, pb, ldb, sb,
+                                                   int(bool(trans_b)), poff, pd, ldd, int(kind != torch.float32),
+                                                   _stream(A)))
+    return out
+
+
+def gemm_grouped_wgrad(A, G, offsets, out=None, d16=False):
+    """The gradient of gemm_grouped in its matrices: D[e] = A_e^T . G_e over the
+    rows of group e.
+
+    A [rows, K], G [rows, N], the gradient in gemm_grouped's D; offsets as there.
+    Returns D [groups, K, N], FP32 or A's type with d16 (or an out of that type);
+    0 for a group without rows.  For matrices kept as [groups, N, K] (trans_b)
+    the gradient is gemm_grouped_wgrad(G, A, offsets)."""
+    rows, K = _dims2(A, "A")
+    code = _half(A, "A")
+    rows_g, N = _dims2(G, "G")
+    if rows_g != rows:
+        raise ValueError("A and G must have the same rows")
+    poff, groups = _offsets(offsets)
+    _shape(out, (groups, K, N), "out")
+    kind = _out_type(out, A.dtype, d16)
+    pa, lda = _mat(A, A.dtype, "A")
+    pg, ldg = _mat(G, A.dtype, "G")
+    where = _on(A, "A", ("G", G), ("offsets", offsets), ("out", out))
+    if out is None:
+        out = torch.empty((groups, K, N), dtype=kind, device=A.device)
+    pd, ldd, sd = _stack(out, kind, "out")
+    with where:
+        _check("gemm_grouped_wgrad", _lib().gemm_grouped_wgrad(code, groups, rows, N, K, pa, lda, pg, ldg, poff, pd,
+                                                               ldd, sd, int(kind != torch.float32), _stream(A)))
+    return out
+
+
+def gemm_grouped_w8a8(X, x_scale, W, w_scale, offsets, bias=None, out=None):
+    """The W8A8 layer of gemm_w8a8 by groups of rows.
+
+    X INT8 [rows, K] with x_scale FP32 [rows] (as rms_norm or quantize_i8_rows
+    give them), sorted by group as in gemm_grouped; W INT8 [groups, N, K] (one
+    output channel per row) with w_scale FP32 [groups, N]; bias FP32 [groups, N] or
+    None.  Returns Y BF16 [rows, N], each value bit for bit gemm_w8a8's."""
+    rows, K = _dims2(X, "X")
+    poff, groups = _offsets(offsets)
+    pw, ldw, sw = _stack(W, torch.int8, "W")
+    N = W.shape[1]
+    _shape(W, (groups, N, K), "W")
+    _shape(w_scale, (groups, N), "w_scale")
+    _shape(bias, (groups, N), "bias")
+    _shape(out, (rows, N), "out")
+    px, ldx = _mat(X, torch.int8, "X")
+    psx = _floats(x_scale, rows, "x_scale")
+    psw, ldsw = _mat(w_scale, torch.float32, "w_scale")
+    pb, ldb = (None, N) if bias is None else _mat(bias, torch.float32, "bias")
+    where = _on(X, "X", ("x_scale", x_scale), ("W", W), ("w_scale", w_scale), ("offsets", offsets), ("bias", bias),
+                ("out", out))
+    if out is None:
+        out = torch.empty((rows, N), dtype=torch.bfloat16, device=X.device)
+    py, ldy = _mat(out, torch.bfloat16, "out")
+    with where:
+        _check("gemm_grouped_w8a8", _lib().gemm_grouped_w8a8(groups, rows, N, K, px, ldx, psx, pw, ldw, sw, psw,
+                                                             ldsw, pb, ldb, poff, py, ldy, _stream(X)))
+    return out
