@@ -44,7 +44,7 @@ struct Rows {
 __device__ __forceinline__ Rows rows_of(const GroupedArgs& g, int e, int lane) {
     int lo = 0;
     for (int i = lane; i <= e; i += 64) lo = max(lo, g.offsets[i]);
-    lo = __shfl(lanes_max(lo, lane), 63);
+    lo = __builtin_amdgcn_readlane(lanes_max(lo, lane), 63);
     lo = min(lo, g.rows);
     return {lo, min(max(lo, g.offsets[e + 1]), g.rows)};
 }
@@ -61,12 +61,11 @@ __device__ __forceinline__ RowTile row_tile(const GroupedArgs& g, int t, int lan
     for (int e0 = 0; e0 < g.groups; e0 += 64) {
         const int e = e0 + lane;
         int end = e < g.groups ? g.offsets[e + 1] : 0;
-        int lo = e < g.groups ? g.offsets[e] : 0;
-        // (offsets[e] is offsets[e - 1 + 1], so one running maximum gives both ends)
-        end = max(max(most, __shfl(lo, 0)), lanes_max(end, lane));
-        lo = __shfl_up(end, 1);
+        // (a group begins where the one before it ends: one running maximum gives both)
+        end = max(max(most, g.offsets[e0]), lanes_max(end, lane));
+        int lo = __shfl_up(end, 1);
         if (lane == 0) lo = max(most, g.offsets[e0]);
-        most = __shfl(end, 63);
+        most = __builtin_amdgcn_readlane(end, 63);
         lo = min(max(lo, 0), g.rows);
         end = min(max(end, lo), g.rows);
         const int tiles = (end - lo + BM - 1) / BM;
@@ -74,12 +73,31 @@ __device__ __forceinline__ RowTile row_tile(const GroupedArgs& g, int t, int lan
         const uint64_t here = __ballot(t < upto);
         if (here) {
             const int l = __ffsll((unsigned long long)here) - 1;
-            const int n = __shfl(tiles, l);
-            return {e0 + l, __shfl(lo, l), __shfl(end, l), t - (__shfl(upto, l) - n), n};
+            const int n = __builtin_amdgcn_readlane(tiles, l);
+            return {e0 + l, __builtin_amdgcn_readlane(lo, l), __builtin_amdgcn_readlane(end, l),
+                    t - (__builtin_amdgcn_readlane(upto, l) - n), n};
         }
-        base = __shfl(upto, 63);
+        base = __builtin_amdgcn_readlane(upto, 63);
     }
     return {-1, 0, 0, 0, 0};
+}
+
+// All groups' row tiles.
+template <int BM>
+__device__ __forceinline__ int all_row_tiles(const GroupedArgs& g, int lane) {
+    int most = 0, sum = 0;
+    for (int e0 = 0; e0 < g.groups; e0 += 64) {
+        const int e = e0 + lane;
+        int end = e < g.groups ? g.offsets[e + 1] : 0;
+        end = max(max(most, g.offsets[e0]), lanes_max(end, lane));
+        int lo = __shfl_up(end, 1);
+        if (lane == 0) lo = max(most, g.offsets[e0]);
+        most = __builtin_amdgcn_readlane(end, 63);
+        lo = min(max(lo, 0), g.rows);
+        end = min(max(end, lo), g.rows);
+        sum += __builtin_amdgcn_readlane(lanes_sum((end - lo + BM - 1) / BM, lane), 63);
+    }
+    return sum;
 }
 
 // ---- any problem --------------------------------------------------------------------
@@ -250,6 +268,368 @@ __global__ __launch_bounds__(256) void grouped_any_kernel(GroupedArgs g) {
     }
 }
 
+// ---- large problems -------------------------------------------------------------------
+
+// A tile of the kernel below.
+struct Tile {
+    int group;          // -1: none
+    int m0, m_end;      // rows of D (TN: of D[group])
+    int n0;
+    int k0, k1;         // along the summed axis
+};
+
+// Workgroup b's tile.  Workgroups go to the eight XCDs in turn; the first 8 * (tiles / 8)
+// are renumbered so that an XCD has neighbouring tiles, which share rows of A and columns
+// of B in its L2: up to GROUP_M row tiles of a group beside each other, then the next
+// column tile.
+template <int MODE>
+__device__ __forceinline__ Tile tile_at(const GroupedArgs& g, int lane) {
+    constexpr int BM = 256, BN = 256;
+    const int tiles_n = (g.N + BN - 1) / BN;
+    Tile t{-1, 0, 0, 0, 0, 0};
+    int total;
+    if constexpr (MODE == GROUPED_TN) total = (g.M + BM - 1) / BM * tiles_n * g.groups;
+    else total = all_row_tiles<BM>(g, lane) * tiles_n;
+    int b = blockIdx.x;
+    if (b >= total) return t;
+    const int per = total / NUM_XCD;
+    if (b < per * NUM_XCD) b = b % NUM_XCD * per + b / NUM_XCD;
+    int tiles_m, local;
+    if constexpr (MODE == GROUPED_TN) {
+        tiles_m = (g.M + BM - 1) / BM;
+        t.group = b / (tiles_m * tiles_n);
+        local = b - t.group * tiles_m * tiles_n;
+        const Rows r = rows_of(g, t.group, lane);
+        t.k0 = r.lo;
+        t.k1 = r.hi;
+    } else {
+        const RowTile r = row_tile<BM>(g, b / tiles_n, lane);
+        t.group = r.group;
+        tiles_m = r.tiles;
+        local = r.tile * tiles_n + b % tiles_n;
+        t.m0 = r.lo;
+        t.m_end = r.hi;
+        t.k1 = g.K;
+    }
+    const int strip = local / (GROUP_M * tiles_n), first = strip * GROUP_M;
+    const int high = min(tiles_m - first, GROUP_M), in = local - strip * GROUP_M * tiles_n;
+    t.m0 += (first + in % high) * BM;
+    t.n0 = in / high * BN;
+    if constexpr (MODE == GROUPED_TN) t.m_end = g.M;
+    // (out of vector divisions: back to scalar registers)
+    t.group = __builtin_amdgcn_readfirstlane(t.group);
+    t.m0 = __builtin_amdgcn_readfirstlane(t.m0);
+    t.m_end = __builtin_amdgcn_readfirstlane(t.m_end);
+    t.n0 = __builtin_amdgcn_readfirstlane(t.n0);
+    t.k0 = __builtin_amdgcn_readfirstlane(t.k0);
+    t.k1 = __builtin_amdgcn_readfirstlane(t.k1);
+    return t;
+}
+
+constexpr uint32_t NOWHERE = 0x80000000u;   // a lane offset past every buffer range: the load gives zeros
+
+// One operand of a tile: 64 * TT rows (KC), or columns of KS rows, by 64 bytes of the
+// summed axis to a stage.  Direct loads move 1 KiB an instruction: 16 rows of 64 bytes
+// (KC), or 2 rows of 512 (KS, always 256 columns).  The swizzle is on the global side:
+// the lane that fills a chunk of LDS reads the chunk that belongs there.
+template <bool KS, int TT, int ES>
+struct Operand {
+    static constexpr int PIECES = KS ? 4 : TT;      // a wave's
+    static constexpr int BYTES = PIECES * 4096;
+    static constexpr int ROW = KS ? 512 : 64;
+    static constexpr int KROWS = 64 / ES;
+    uint32_t voff[PIECES];  // from the K tile's first byte; NOWHERE for rows or columns past the end
+    int idx[PIECES];        // KC: the chunk's byte along the summed axis; KS: its row
+    uint64_t base;          // of K tile 0
+    int64_t step;           // bytes to the next K tile
+    uint32_t read0;         // LDS offset of this lane's operand of step 0, 32-row tile 0
+
+    // rows (columns) [r0, end) of the operand at p, summed from k0 on
+    __device__ __forceinline__ void init(const char* p, int64_t ld, int r0, int end, int k0, int wave, int lane,
+                                         int w_half) {
+        if constexpr (KS) {
+            base = (uint64_t)(uintptr_t)p + (uint64_t)((int64_t)k0 * ld + (int64_t)r0 * ES);
+            step = (int64_t)KROWS * ld;
+        } else {
+            base = (uint64_t)(uintptr_t)p + (uint64_t)((int64_t)r0 * ld + (int64_t)k0 * ES);
+            step = 64;
+        }
+#pragma unroll
+        for (int u = 0; u < PIECES; ++u) {
+            if constexpr (KS) {
+                const int row = (wave * PIECES + u) * 2 + (lane >> 5);
+                const uint32_t c = (uint32_t)(lane & 31) ^ swz_b<2>(row);
+                idx[u] = row;
+                voff[u] = r0 + (int)c * 8 < end ? (uint32_t)row * (uint32_t)ld + c * 16u : NOWHERE;
+            } else {
+                const int row = (wave * PIECES + u) * 16 + (lane >> 2);
+                const uint32_t c = (uint32_t)(lane & 3) ^ swz_a<4>(row);
+                idx[u] = (int)c * 16;
+                voff[u] = r0 + row < end ? (uint32_t)row * (uint32_t)ld + c * 16u : NOWHERE;
+            }
+        }
+        const uint32_t lrow = lane & 31, lhalf = lane >> 5, grp = lane >> 4, gp = lane & 15;
+        const int first = w_half * 32 * TT;     // this wave's first row (column)
+        if constexpr (KS) {
+            const uint32_t col = first + 16 * (grp & 1), k = 8 * (grp >> 1) + (gp >> 2);
+            read0 = k * 512 + ((((col >> 3) + ((gp & 3) >> 1)) ^ swz_b<2>(k)) << 4) + 8 * (gp & 1);
+        } else {
+            const uint32_t r = first + lrow;
+            read0 = r * 64 + ((lhalf ^ swz_a<4>(r)) << 4);
+        }
+    }
+    // piece u of K tile t; `left`: what the tile holds along the summed axis (KC: bytes)
+    __device__ __forceinline__ void load(int u, i32x4 rsrc, MPDT_LDS char* stage, int wave, int left) const {
+        const uint32_t v = idx[u] < left ? voff[u] : NOWHERE;
+        lds_dma16<0, true>(rsrc, stage + (wave * PIECES + u) * 1024, v, 0u);
+    }
+    __device__ __forceinline__ i32x4 rsrc(int t, bool live) const {
+        return rsrc_words(base + (uint64_t)((int64_t)t * step), live ? 0x7fffffffu : 0u);
+    }
+    // what K tile t has left, up to `keys` along the summed axis in all
+    __device__ __forceinline__ static int left(int t, int keys) { return KS ? keys - t * KROWS : (keys - t * KROWS) * ES; }
+    // the MFMA operand of step s (0, 1) and 32-row tile i
+    __device__ __forceinline__ u32x4 read(const MPDT_LDS char* stage, int s, int i) const {
+        if constexpr (KS) {
+            // (16 rows on, the swizzle repeats; 32 columns are four chunks on, which
+            // the swizzle may turn over: bits 1 to 3 of the chunk)
+            const uint32_t o = (read0 ^ (uint32_t)((i & 3) * 64)) + s * 16 * 512;
+            const u32x2 x = lds_read_tr16(stage, o), y = lds_read_tr16(stage, o + 4 * 512);
+            return u32x4{x[0], x[1], y[0], y[1]};
+        } else {
+            return lds_load16(stage, (read0 ^ (uint32_t)(s * 32)) + i * 32 * 64);
+        }
+    }
+};
+
+// The tile's product by four waves, one to a SIMD: 64 * TM x 256 of D, 32 * TM x 128 a
+// wave (TM 4, 2 or 1: 256, 128 or 64 rows), accumulated in registers for the whole of k.
+// A stage holds 64 bytes of k of both operands; NS stages are loaded ahead.  For K tile t:
+//   phase X: MFMAs of its first step, among them the reads of the second step's operands
+//            and the direct loads of B of tile t - 1 + NS;
+//   wait for tile t + 1's loads and this wave's reads, barrier;
+//   phase Y: MFMAs of the second step, among them the reads of tile t + 1's first step and
+//            the direct loads of A of tile t + NS (into the stage of tile t).
+// Tiles past the last load nothing (an empty buffer range), so that the count of loads in
+// flight is the same everywhere.
+template <GroupedType T, int MODE, int TM, class Acc>
+__device__ __forceinline__ void tile_product(const GroupedArgs& g, const Tile& t, MPDT_LDS char* lds, int wave, int lane,
+                                             Acc (&acc)[TM][4]) {
+    using F = Fmt<KindOf<T>::kind>;
+    constexpr int ES = F::ES;
+    using OpA = Operand<MODE == GROUPED_TN, TM, ES>;
+    using OpB = Operand<MODE != GROUPED_NT, 4, ES>;
+    constexpr int STAGE = OpA::BYTES + OpB::BYTES;
+    constexpr int NS = TM == 4 ? 4 : TM == 2 ? 5 : 6;
+    constexpr int LOADS = OpA::PIECES + OpB::PIECES;
+    constexpr int NM = TM * 4, GROUPS = TM + 3;     // MFMAs of a step; operand reads: A0 and B0, B1, B2, B3, A1 ..
+    const int keys = t.k1 - t.k0;
+    const int nt = (keys + OpA::KROWS - 1) / OpA::KROWS;
+    const int wm = wave >> 1, wn = wave & 1;
+    OpA A;
+    OpB B;
+    A.init(g.A, g.lda_b, t.m0, t.m_end, t.k0, wave, lane, wm);
+    B.init(MODE == GROUPED_TN ? g.B : g.B + t.group * g.group_b, g.ldb_b, t.n0, g.N, t.k0, wave, lane, wn);
+
+    u32x4 fa[2][TM], fb[2][4];
+    auto read_group = [&](int s, int r, const MPDT_LDS char* stage) {
+        if (r == 0) fa[s][0] = A.read(stage, s, 0);
+        if (r <= 3) fb[s][r] = B.read(stage + OpA::BYTES, s, r);
+        else fa[s][r - 3] = A.read(stage, s, r - 3);
+    };
+    // (the operands change places: a lane then holds four neighbouring columns of a row)
+    auto mma = [&](int s, int i) { acc[i / 4][i % 4] = F::mma(fb[s][i % 4], fa[s][i / 4], acc[i / 4][i % 4]); };
+
+    i32x4 rb{};     // B's buffer of the tile whose loads are due next
+    int left_b = 0;
+#pragma unroll
+    for (int p = 0; p < NS; ++p) {
+        const i32x4 ra = A.rsrc(p, p < nt);
+        rb = B.rsrc(p, p < nt);
+        left_b = OpB::left(p, keys);
+        static_for<0, OpA::PIECES>([&](auto U) { A.load(decltype(U)::value, ra, lds + p * STAGE, wave, OpA::left(p, keys)); });
+        if (p < NS - 1)
+            static_for<0, 4>([&](auto U) { B.load(decltype(U)::value, rb, lds + p * STAGE + OpA::BYTES, wave, left_b); });
+    }
+    wait_vmem<(NS - 2) * LOADS + OpA::PIECES>();
+    wg_barrier();
+#pragma unroll
+    for (int r = 0; r < GROUPS; ++r) read_group(0, r, lds);
+    int cur = 0;
+    for (int k = 0; k < nt - 1; ++k) {
+        const int next = cur + 1 == NS ? 0 : cur + 1, prev = cur == 0 ? NS - 1 : cur - 1;
+        MPDT_LDS char* const sc = lds + cur * STAGE;
+        MPDT_LDS char* const sn = lds + next * STAGE;
+        MPDT_LDS char* const sp = lds + prev * STAGE + OpA::BYTES;
+        i32x4 ra, rb2;
+        int left_a, left_b2;
+        static_for<0, NM>([&](auto I) {
+            constexpr int i = decltype(I)::value;
+            mma(0, i);
+            if constexpr (i < GROUPS) read_group(1, i, sc);
+            if constexpr (i == NM / 2) {
+                ra = A.rsrc(k + NS, k + NS < nt);
+                left_a = OpA::left(k + NS, keys);
+            }
+            if constexpr (i == NM / 2 + 1) {
+                rb2 = B.rsrc(k + NS, k + NS < nt);
+                left_b2 = OpB::left(k + NS, keys);
+            }
+            // B's four loads on the last slots, every second one where there are 16
+            constexpr int STEP = TM == 4 ? 2 : 1, FIRST = NM - 1 - 3 * STEP;
+            if constexpr (i >= FIRST && (i - FIRST) % STEP == 0) B.load((i - FIRST) / STEP, rb, sp, wave, left_b);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        wait_vmem<(NS - 2) * LOADS>();
+        wait_lds();
+        wg_barrier();
+        static_for<0, NM>([&](auto I) {
+            constexpr int i = decltype(I)::value;
+            mma(1, i);
+            if constexpr (i % 4 == 0) A.load(i / 4, ra, sc, wave, left_a);
+            // the reads in between: slots 1, 3, 5 .. of 16; every other free one of fewer
+            if constexpr (TM == 4) {
+                if constexpr (i % 2 == 1 && i / 2 < GROUPS) read_group(0, i / 2, sn);
+            } else if constexpr (TM == 2) {
+                if constexpr (i % 4 != 0 && i - 1 - i / 4 < GROUPS) read_group(0, i - 1 - i / 4, sn);
+            } else {
+                read_group(0, i, sn);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        rb = rb2;
+        left_b = left_b2;
+        cur = next;
+    }
+    MPDT_LDS char* const sc = lds + cur * STAGE;
+    static_for<0, NM>([&](auto I) {
+        constexpr int i = decltype(I)::value;
+        mma(0, i);
+        if constexpr (i < GROUPS) read_group(1, i, sc);
+        __builtin_amdgcn_sched_barrier(0);
+    });
+    wait_lds();
+#pragma unroll
+    for (int i = 0; i < NM; ++i) mma(1, i);
+    // (the empty loads write zeros: they land before LDS is used again)
+    wait_vmem<0>();
+}
+
+// D from the accumulators, through LDS so that it leaves in 16-byte pieces of rows: a wave
+// has 32 KiB of its own for 32 * TM rows of 128 columns (FP32: half as many at a time).
+// Lane element r of a 32 x 32 block: row lane % 32, column 8 (r / 4) + 4 (lane / 32) + r % 4.
+template <GroupedType T, int MODE, int TM, class Out, class Acc>
+__device__ __forceinline__ void tile_store(const GroupedArgs& g, const Tile& t, MPDT_LDS char* lds, int wave, int lane,
+                                           const Acc (&acc)[TM][4]) {
+    constexpr int ES = (int)sizeof(Out), ROW = 128 * ES, CHUNKS = ROW / 16, PER = 16 / ES;
+    constexpr int STEP = ES == 2 ? TM : TM < 2 ? TM : 2;   // 32-row blocks at a time
+    const int wm = wave >> 1, wn = wave & 1, lrow = lane & 31, lhalf = lane >> 5;
+    MPDT_LDS char* const own = lds + wave * 32768;
+    const int row0 = t.m0 + wm * 32 * TM, col0 = t.n0 + wn * 128;
+    Out* const D = reinterpret_cast<Out*>(g.D) + (MODE == GROUPED_TN ? t.group * g.group_d : 0);
+    const bool wide = (uintptr_t)D % 16 == 0 && g.ldd % PER == 0;
+    wg_barrier();       // every wave is done with the stages
+#pragma unroll
+    for (int i0 = 0; i0 < TM; i0 += STEP) {
+#pragma unroll
+        for (int i = i0; i < i0 + STEP; ++i) {
+            float xs = 0;
+            if constexpr (T == GroupedType::I8) {
+                const int row = row0 + i * 32 + lrow;
+                xs = row < t.m_end ? g.x_scale[row] : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int col = j * 32 + 8 * q + 4 * lhalf;
+                    float v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if constexpr (T == GroupedType::I8) {
+                            const int c = min(col0 + col + e, g.N - 1);
+                            v[e] = mul_rn(mul_rn((float)acc[i][j][4 * q + e], xs), g.w_scale[t.group * g.ld_ws + c]);
+                            if (g.bias) v[e] = add_rn(v[e], g.bias[t.group * g.ld_bias + c]);
+                        } else {
+                            v[e] = acc[i][j][4 * q + e];
+                        }
+                    }
+                    // chunk c of row r lies at c ^ r: rows beside each other in other banks
+                    const uint32_t r = (i - i0) * 32 + lrow, c = (uint32_t)(col * ES) / 16;
+                    MPDT_LDS char* const p = own + r * ROW + ((c ^ (r % CHUNKS)) << 4);
+                    if constexpr (ES == 4) {
+                        *(MPDT_LDS f32x4*)p = f32x4{v[0], v[1], v[2], v[3]};
+                    } else {
+                        uint32_t h[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) h[e] = T == GroupedType::F16 ? f32_to_f16_bits(v[e]) : f32_to_bf16_bits(v[e]);
+                        *(MPDT_LDS u32x2*)(p + 8 * lhalf) = u32x2{h[0] | h[1] << 16, h[2] | h[3] << 16};
+                    }
+                }
+        }
+        wait_lds();     // (a wave reads only what it wrote)
+        asm volatile("" ::: "memory");
+#pragma unroll 4
+        for (int q = 0; q < STEP * 32 * CHUNKS / 64; ++q) {
+            const int n = q * 64 + lane, r = n / CHUNKS, c = n % CHUNKS;
+            const u32x4 v = lds_load16(own, r * ROW + ((c ^ (r % CHUNKS)) << 4));
+            const int row = row0 + i0 * 32 + r, col = col0 + c * PER;
+            if (row >= t.m_end || col >= g.N) continue;
+            Out* const to = D + (int64_t)row * g.ldd + col;
+            if (wide && col + PER <= g.N) {
+                *reinterpret_cast<u32x4*>(to) = v;
+            } else {
+#pragma unroll
+                for (int e = 0; e < PER; ++e) {
+                    const uint32_t w = v[e * ES / 4];
+                    if (col + e < g.N) {
+                        if constexpr (ES == 4) to[e] = __uint_as_float(w);
+                        else to[e] = (uint16_t)(w >> (16 * (e & 1)));
+                    }
+                }
+            }
+        }
+        wait_lds();
+        asm volatile("" ::: "memory");
+    }
+}
+
+template <GroupedType T, int MODE, int TM>
+__device__ __forceinline__ void tile_run(const GroupedArgs& g, const Tile& t, MPDT_LDS char* lds, int wave, int lane) {
+    typename Fmt<KindOf<T>::kind>::Acc acc[TM][4];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+    if (t.k1 > t.k0) tile_product<T, MODE, TM>(g, t, lds, wave, lane, acc);
+    if constexpr (T == GroupedType::I8) {
+        tile_store<T, MODE, TM, uint16_t>(g, t, lds, wave, lane, acc);
+    } else {
+        if (g.out16) tile_store<T, MODE, TM, uint16_t>(g, t, lds, wave, lane, acc);
+        else tile_store<T, MODE, TM, float>(g, t, lds, wave, lane, acc);
+    }
+}
+
+// 256 x 256 tiles of problems whose rows are whole 16-byte pieces (of any alignment).
+template <GroupedType T, int MODE>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void grouped_tile_kernel(GroupedArgs g) {
+    __shared__ __attribute__((aligned(1024))) char lds[131072];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Tile t = tile_at<MODE>(g, lane);
+    if (t.group < 0) return;    // (the whole workgroup)
+    if constexpr (MODE == GROUPED_TN) {
+        tile_run<T, MODE, 4>(g, t, lds_cast(lds), wave, lane);
+    } else {
+        // the last rows of a group may fill a half or a quarter of a tile
+        const int rows = t.m_end - t.m0;
+        if (rows > 128) tile_run<T, MODE, 4>(g, t, lds_cast(lds), wave, lane);
+        else if (rows > 64) tile_run<T, MODE, 2>(g, t, lds_cast(lds), wave, lane);
+        else tile_run<T, MODE, 1>(g, t, lds_cast(lds), wave, lane);
+    }
+}
+
 // The most row tiles of BM rows that the groups can have.
 int64_t most_row_tiles(const GroupedArgs& a, int64_t bm) {
     return a.rows / bm + (a.rows < a.groups ? a.rows : a.groups);
@@ -266,12 +646,29 @@ hipError_t launch_any(const GroupedArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// Whether the direct loads can take a problem: operands' rows end on a 16-byte piece, and
+// a tile's offsets fit in 32 bits.
+template <GroupedType T, int MODE>
+bool whole_pieces(const GroupedArgs& a) {
+    constexpr int ES = T == GroupedType::I8 ? 1 : 2;
+    const int64_t row_a = (int64_t)(MODE == GROUPED_TN ? a.M : a.K) * ES;
+    const int64_t row_b = (int64_t)(MODE == GROUPED_NT ? a.K : a.N) * ES;
+    return row_a % 16 == 0 && row_b % 16 == 0 && a.lda_b < (1 << 23) && a.ldb_b < (1 << 23);
+}
+
+template <GroupedType T, int MODE>
+hipError_t launch_mode(const GroupedArgs& a, hipStream_t stream) {
+    if (!whole_pieces<T, MODE>(a)) return launch_any<T, MODE>(a, stream);
+    grouped_tile_kernel<T, MODE><<<dim3((unsigned)grouped_tiles(MODE, a, 256, 256)), dim3(256), 0, stream>>>(a);
+    return hipGetLastError();
+}
+
 template <GroupedType T>
 hipError_t launch_type(int mode, const GroupedArgs& a, hipStream_t stream) {
-    if constexpr (T == GroupedType::I8) return launch_any<T, GROUPED_NT>(a, stream);
+    if constexpr (T == GroupedType::I8) return launch_mode<T, GROUPED_NT>(a, stream);
     else
-        return mode == GROUPED_NN ? launch_any<T, GROUPED_NN>(a, stream)
-               : mode == GROUPED_NT ? launch_any<T, GROUPED_NT>(a, stream) : launch_any<T, GROUPED_TN>(a, stream);
+        return mode == GROUPED_NN ? launch_mode<T, GROUPED_NN>(a, stream)
+               : mode == GROUPED_NT ? launch_mode<T, GROUPED_NT>(a, stream) : launch_mode<T, GROUPED_TN>(a, stream);
 }
 
 }  // namespace
