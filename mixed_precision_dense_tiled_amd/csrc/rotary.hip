@@ -9,6 +9,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "kv_places.hpp"
 #include "layers.hpp"
@@ -46,53 +48,192 @@ __device__ __forceinline__ uint8_t to_e4m3(float x) {
     return (uint8_t)(__builtin_amdgcn_cvt_pk_fp8_f32(x, 0.0f, 0, false) & 0xff);
 }
 
-constexpr int ROPE_TOKENS = 8;
-
-template <bool TO8>
-__global__ __launch_bounds__(256) void append_rope_kernel(RopeArgs r) {
-    const AppendArgs& a = r.ap;
-    __shared__ int64_t dst[ROPE_TOKENS];
-    __shared__ int pos[ROPE_TOKENS], in[ROPE_TOKENS];
-    __shared__ float2 turn[ROPE_TOKENS][64];
-    const int t0 = blockIdx.x * ROPE_TOKENS;
+// What a workgroup's tokens need: where they belong, and their angles.
+template <int N>
+struct Tokens {
+    int64_t dst[N];
+    int pos[N], in[N];
+    float2 turn[N][64];
+};
+// (a workgroup of 256 threads)
+template <int N>
+__device__ __forceinline__ void find_tokens(const RopeArgs& r, int t0, Tokens<N>& to) {
     if (threadIdx.x < 64) {
         const int lane = threadIdx.x;
-        const Place p = place_of<ROPE_TOKENS>(a.kv, a.sv, t0, lane);
-        if (lane < ROPE_TOKENS) {
-            dst[lane] = p.off;
-            pos[lane] = p.pos;
-            in[lane] = p.in;
+        const Place p = place_of<N>(r.ap.kv, r.ap.sv, t0, lane);
+        if (lane < N) {
+            to.dst[lane] = p.off;
+            to.pos[lane] = p.pos;
+            to.in[lane] = p.in;
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < ROPE_TOKENS * r.pairs; i += 256) {
-        const int k = i / r.pairs, j = i - k * r.pairs;
-        if (in[k]) turn[k][j] = cos_sin(pos[k], r.inv_freq[j]);
-    }
+    // a quarter (half, ..) of the threads to a token
+    constexpr int PER = 256 / N;
+    const int k = threadIdx.x / PER;
+    if (to.in[k])
+        for (int j = threadIdx.x % PER; j < r.pairs; j += PER) to.turn[k][j] = cos_sin(to.pos[k], r.inv_freq[j]);
     __syncthreads();
+}
+
+// 8 elements to E4M3: x / scale as the division gives it, from the scale's reciprocal: the
+// product's error comes back through one fused step, after which the quotient is rounded
+// correctly (Markstein's theorem) wherever nothing leaves the range of FP32.  What is past
+// the range of E4M3 keeps the product, and scales far from 1 take the division itself.
+__device__ __forceinline__ u32x2 to_e4m3_8(const float (&x)[8], float scale) {
+    float q[8];
+    if (scale >= 0x1p-60f && scale <= 0x1p60f) {
+        const float r = 1.0f / scale;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float p = x[i] * r;
+            q[i] = fabsf(p) <= 1000.0f ? fmaf(fmaf(-p, scale, x[i]), r, p) : p;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = x[i] / scale;
+    }
+    u32x2 w;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        int c = __builtin_amdgcn_cvt_pk_fp8_f32(cut448(q[4 * j]), cut448(q[4 * j + 1]), 0, false);
+        w[j] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(cut448(q[4 * j + 2]), cut448(q[4 * j + 3]), c, true);
+    }
+    return w;
+}
+
+// Rows in pieces of 16 bytes: a thread takes two pieces of a head that turn together (or
+// that lie beside each other, where nothing turns), four such at a time.  The first
+// four are under way before the workgroup looks its tokens up.  Wants pairs that fill
+// pieces, or neighbouring pairs, which always do.
+template <bool BF16, bool TO8, bool NEAR, int N>
+__global__ __launch_bounds__(256) void append_rope_kernel(RopeArgs r) {
+    const AppendArgs& a = r.ap;
+    __shared__ Tokens<N> tok;
+    const int t0 = blockIdx.x * N;
+    const int per = a.kv.dim / 16, j = threadIdx.x % per, first = threadIdx.x / per, step = 256 / per;
+    const int heads = r.heads + 2 * a.kv.kv_heads, rows = first < step ? N * heads : 0;
+    const int turned = NEAR ? per : r.pairs / 8;        // of q's and K's items
+    constexpr int U = 4;
+    u32x4 x[U][2];
+    // row i: token i / heads; first q's heads, then K's, then V's
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = min(i0 + u * step, N * heads - 1);
+            const int k = N == 1 ? 0 : i / heads, hh = i - k * heads;
+            const int64_t t = min(t0 + k, a.sv.tokens - 1);     // (a row that is there)
+            const int hk = hh - r.heads, hv = hk - a.kv.kv_heads;
+            const char* p = hk < 0 ? r.q + t * r.q_tok_b + hh * r.q_head_b
+                            : hv < 0 ? a.k_new + t * a.k_tok_b + hk * a.k_head_b
+                                     : a.v_new + t * a.v_tok_b + hv * a.v_head_b;
+            const bool apart = !NEAR && hv < 0 && j < turned;
+            const int c0 = apart ? j : 2 * j, c1 = apart ? j + turned : 2 * j + 1;
+            x[u][0] = *reinterpret_cast<const u32x4*>(p + 16 * c0);
+            x[u][1] = *reinterpret_cast<const u32x4*>(p + 16 * c1);
+        }
+    };
+    if (rows) load(first);
+    find_tokens<N>(r, t0, tok);
+    for (int i0 = first; i0 < rows; i0 += U * step) {
+        if (i0 != first) load(i0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * step;
+            if (i >= rows) break;
+            const int k = N == 1 ? 0 : i / heads, hh = i - k * heads;
+            const int hk = hh - r.heads, hv = hk - a.kv.kv_heads;
+            const int64_t dst = tok.dst[k];
+            if (hk < 0 ? !tok.in[k] : dst < 0) continue;
+            const bool apart = !NEAR && hv < 0 && j < turned;
+            const int c0 = apart ? j : 2 * j, c1 = apart ? j + turned : 2 * j + 1;
+            const bool turns = NEAR ? hv < 0 && 8 * j < r.pairs : apart;
+            const bool to8 = TO8 && hk >= 0;
+            float y[2][8];
+            if (turns || to8) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) y[e >> 3][e & 7] = widen((uint16_t)(x[u][e >> 3][(e & 7) >> 1] >> (16 * (e & 1))), BF16);
+            }
+            if (turns) {
+                const float2* cs = tok.turn[k] + 8 * j;
+                if constexpr (NEAR) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (8 * j + e < r.pairs) {
+                            const float2 t = cs[e];
+                            const float p = y[e >> 2][2 * (e & 3)], q = y[e >> 2][2 * (e & 3) + 1];
+                            y[e >> 2][2 * (e & 3)] = p * t.x - q * t.y;
+                            y[e >> 2][2 * (e & 3) + 1] = q * t.x + p * t.y;
+                        }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float2 t = cs[e];
+                        const float p = y[0][e], q = y[1][e];
+                        y[0][e] = p * t.x - q * t.y;
+                        y[1][e] = q * t.x + p * t.y;
+                    }
+                }
+                if (!to8) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int w = 0; w < 4; ++w)
+                            x[u][c][w] = narrow(y[c][2 * w], BF16) | (uint32_t)narrow(y[c][2 * w + 1], BF16) << 16;
+                }
+            }
+            if (hk < 0) {
+                char* to = r.q_out + (int64_t)(t0 + k) * r.qo_tok_b + hh * r.qo_head_b;
+                *reinterpret_cast<u32x4*>(to + 16 * c0) = x[u][0];
+                *reinterpret_cast<u32x4*>(to + 16 * c1) = x[u][1];
+                continue;
+            }
+            const int h = hv < 0 ? hk : hv;
+            char* to = (hv < 0 ? a.kv.k : a.kv.v) + dst + h * a.kv.head_b;
+            if constexpr (TO8) {
+                const float scale = (hv < 0 ? a.kv.k_scale : a.kv.v_scale)[h];
+                *reinterpret_cast<u32x2*>(to + 8 * c0) = to_e4m3_8(y[0], scale);
+                *reinterpret_cast<u32x2*>(to + 8 * c1) = to_e4m3_8(y[1], scale);
+            } else {
+                *reinterpret_cast<u32x4*>(to + 16 * c0) = x[u][0];
+                *reinterpret_cast<u32x4*>(to + 16 * c1) = x[u][1];
+            }
+        }
+    }
+}
+
+// Pairs that fill no pieces: one pair, or one element that does not turn, at a time.
+constexpr int ROPE_TOKENS = 8;
+
+template <bool TO8>
+__global__ __launch_bounds__(256) void append_rope_any_kernel(RopeArgs r) {
+    const AppendArgs& a = r.ap;
+    __shared__ Tokens<ROPE_TOKENS> tok;
+    const int t0 = blockIdx.x * ROPE_TOKENS;
+    find_tokens<ROPE_TOKENS>(r, t0, tok);
     const bool bf16 = a.type == DT_BF16;
     const int dim = a.kv.dim, heads = r.heads + 2 * a.kv.kv_heads;
     // one pair (or one element that is not rotated, or of V) at a time
     const int items = ROPE_TOKENS * heads * dim;
     for (int i = threadIdx.x; i < items; i += 256) {
         const int k = i / (heads * dim), rest = i - k * heads * dim, hh = rest / dim, d = rest - hh * dim;
-        if (!in[k]) continue;
+        if (!tok.in[k]) continue;
         const bool is_q = hh < r.heads, is_v = hh >= r.heads + a.kv.kv_heads;
         const int h = is_q ? hh : is_v ? hh - r.heads - a.kv.kv_heads : hh - r.heads;
-        if (!is_q && dst[k] < 0) continue;
+        if (!is_q && tok.dst[k] < 0) continue;
         const int64_t t = t0 + k;
         const char* src = is_q ? r.q + t * r.q_tok_b + h * r.q_head_b
                           : is_v ? a.v_new + t * a.v_tok_b + h * a.v_head_b : a.k_new + t * a.k_tok_b + h * a.k_head_b;
         char* to = is_q ? r.q_out + t * r.qo_tok_b + h * r.qo_head_b
-                        : (is_v ? a.kv.v : a.kv.k) + dst[k] + h * a.kv.head_b;
+                        : (is_v ? a.kv.v : a.kv.k) + tok.dst[k] + h * a.kv.head_b;
         const uint16_t* x = reinterpret_cast<const uint16_t*>(src);
         const bool turned = !is_v && d < 2 * r.pairs;
         // the second of a pair is done with the first
-        if (turned && (r.interleaved ? d & 1 : d >= r.pairs)) continue;
-        const int d2 = r.interleaved ? d + 1 : d + r.pairs;
+        if (turned && (d >= r.pairs)) continue;
+        const int d2 = d + r.pairs;
         float y = widen(x[d], bf16), y2 = 0;
         if (turned) {
-            const float2 cs = turn[k][r.interleaved ? d >> 1 : d];
+            const float2 cs = tok.turn[k][d];
             const float p = y, q = widen(x[d2], bf16);
             y = p * cs.x - q * cs.y;
             y2 = q * cs.x + p * cs.y;
@@ -111,9 +252,39 @@ __global__ __launch_bounds__(256) void append_rope_kernel(RopeArgs r) {
 }  // namespace
 
 hipError_t launch_paged_append_rope(const RopeArgs& r, hipStream_t stream) {
-    const dim3 grid((unsigned)((r.ap.sv.tokens + ROPE_TOKENS - 1) / ROPE_TOKENS));
-    if (r.ap.kv.type == DT_E4M3) append_rope_kernel<true><<<grid, dim3(256), 0, stream>>>(r);
-    else append_rope_kernel<false><<<grid, dim3(256), 0, stream>>>(r);
+    const AppendArgs& a = r.ap;
+    const bool to8 = a.kv.type == DT_E4M3, bf16 = a.type == DT_BF16;
+    if (!r.interleaved && r.pairs % 8) {
+        const dim3 grid((unsigned)((a.sv.tokens + ROPE_TOKENS - 1) / ROPE_TOKENS));
+        if (to8) append_rope_any_kernel<true><<<grid, dim3(256), 0, stream>>>(r);
+        else append_rope_any_kernel<false><<<grid, dim3(256), 0, stream>>>(r);
+        return hipGetLastError();
+    }
+    // Tokens of a workgroup: enough rows for three rounds of its threads, and one where the
+    // tokens are too few for two workgroups to a CU
+    const int step = 256 / (a.kv.dim / 16), heads = r.heads + 2 * a.kv.kv_heads;
+    int n = 1;
+    while (n < 8 && n * heads < 3 * step && a.sv.tokens / (2 * n) >= 512) n *= 2;
+    const auto go = [&](auto BF16, auto TO8, auto NEAR, auto N) {
+        constexpr int tokens = decltype(N)::value;
+        append_rope_kernel<decltype(BF16)::value, decltype(TO8)::value, decltype(NEAR)::value, tokens>
+            <<<dim3((unsigned)((a.sv.tokens + tokens - 1) / tokens)), dim3(256), 0, stream>>>(r);
+    };
+    const auto yes = std::true_type{};
+    const auto no = std::false_type{};
+    const auto with_n = [&](auto BF16, auto TO8, auto NEAR) {
+        using std::integral_constant;
+        if (n == 1) go(BF16, TO8, NEAR, integral_constant<int, 1>{});
+        else if (n == 2) go(BF16, TO8, NEAR, integral_constant<int, 2>{});
+        else if (n == 4) go(BF16, TO8, NEAR, integral_constant<int, 4>{});
+        else go(BF16, TO8, NEAR, integral_constant<int, 8>{});
+    };
+    const auto with_near = [&](auto BF16, auto TO8) {
+        if (r.interleaved) with_n(BF16, TO8, yes);
+        else with_n(BF16, TO8, no);
+    };
+    if (bf16) to8 ? with_near(yes, yes) : with_near(yes, no);
+    else to8 ? with_near(no, yes) : with_near(no, no);
     return hipGetLastError();
 }
 
