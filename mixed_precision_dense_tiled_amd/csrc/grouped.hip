@@ -8,6 +8,7 @@
 // group of its tile by itself, from a prefix sum over the groups' row tiles; the grid
 // is the most tiles that the rows could need.
 #include <hip/hip_runtime.h>
+#include <limits.h>
 #include <stdint.h>
 
 #include "gemm_common.hpp"
@@ -18,22 +19,24 @@ namespace {
 
 // ---- groups -----------------------------------------------------------------------
 
-// Inclusive sums and running maxima over a wave's lanes.
-__device__ __forceinline__ int lanes_sum(int v, int lane) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(v, d);
-        if (lane >= d) v += o;
-    }
+// Inclusive sums and running maxima over a wave's lanes: within rows of 16 lanes by
+// shifts, then the last lane of a row to the row after it, and of two to the other two.
+// (Lanes that a step does not reach take `none`, which changes nothing.)
+template <class F>
+__device__ __forceinline__ int lanes_scan(int v, int none, F f) {
+    v = f(v, __builtin_amdgcn_update_dpp(none, v, 0x111 /* row_shr:1 */, 0xf, 0xf, false));
+    v = f(v, __builtin_amdgcn_update_dpp(none, v, 0x112, 0xf, 0xf, false));
+    v = f(v, __builtin_amdgcn_update_dpp(none, v, 0x114, 0xf, 0xf, false));
+    v = f(v, __builtin_amdgcn_update_dpp(none, v, 0x118, 0xf, 0xf, false));
+    v = f(v, __builtin_amdgcn_update_dpp(none, v, 0x142 /* row_bcast:15 */, 0xa, 0xf, false));
+    v = f(v, __builtin_amdgcn_update_dpp(none, v, 0x143 /* row_bcast:31 */, 0xc, 0xf, false));
     return v;
 }
-__device__ __forceinline__ int lanes_max(int v, int lane) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(v, d);
-        if (lane >= d) v = max(v, o);
-    }
-    return v;
+__device__ __forceinline__ int lanes_sum(int v) {
+    return lanes_scan(v, 0, [](int a, int b) { return a + b; });
+}
+__device__ __forceinline__ int lanes_max(int v) {
+    return lanes_scan(v, INT_MIN, [](int a, int b) { return max(a, b); });
 }
 
 // Rows [lo, hi) of group e where every offset counts as the largest up to it, cut to
@@ -44,7 +47,7 @@ struct Rows {
 __device__ __forceinline__ Rows rows_of(const GroupedArgs& g, int e, int lane) {
     int lo = 0;
     for (int i = lane; i <= e; i += 64) lo = max(lo, g.offsets[i]);
-    lo = __builtin_amdgcn_readlane(lanes_max(lo, lane), 63);
+    lo = __builtin_amdgcn_readlane(lanes_max(lo), 63);
     lo = min(lo, g.rows);
     return {lo, min(max(lo, g.offsets[e + 1]), g.rows)};
 }
@@ -62,14 +65,14 @@ __device__ __forceinline__ RowTile row_tile(const GroupedArgs& g, int t, int lan
         const int e = e0 + lane;
         int end = e < g.groups ? g.offsets[e + 1] : 0;
         // (a group begins where the one before it ends: one running maximum gives both)
-        end = max(max(most, g.offsets[e0]), lanes_max(end, lane));
+        end = max(max(most, g.offsets[e0]), lanes_max(end));
         int lo = __shfl_up(end, 1);
         if (lane == 0) lo = max(most, g.offsets[e0]);
         most = __builtin_amdgcn_readlane(end, 63);
         lo = min(max(lo, 0), g.rows);
         end = min(max(end, lo), g.rows);
         const int tiles = (end - lo + BM - 1) / BM;
-        const int upto = base + lanes_sum(tiles, lane);
+        const int upto = base + lanes_sum(tiles);
         const uint64_t here = __ballot(t < upto);
         if (here) {
             const int l = __ffsll((unsigned long long)here) - 1;
@@ -80,24 +83,6 @@ __device__ __forceinline__ RowTile row_tile(const GroupedArgs& g, int t, int lan
         base = __builtin_amdgcn_readlane(upto, 63);
     }
     return {-1, 0, 0, 0, 0};
-}
-
-// All groups' row tiles.
-template <int BM>
-__device__ __forceinline__ int all_row_tiles(const GroupedArgs& g, int lane) {
-    int most = 0, sum = 0;
-    for (int e0 = 0; e0 < g.groups; e0 += 64) {
-        const int e = e0 + lane;
-        int end = e < g.groups ? g.offsets[e + 1] : 0;
-        end = max(max(most, g.offsets[e0]), lanes_max(end, lane));
-        int lo = __shfl_up(end, 1);
-        if (lane == 0) lo = max(most, g.offsets[e0]);
-        most = __builtin_amdgcn_readlane(end, 63);
-        lo = min(max(lo, 0), g.rows);
-        end = min(max(end, lo), g.rows);
-        sum += __builtin_amdgcn_readlane(lanes_sum((end - lo + BM - 1) / BM, lane), 63);
-    }
-    return sum;
 }
 
 // ---- any problem --------------------------------------------------------------------
@@ -270,83 +255,191 @@ __global__ __launch_bounds__(256) void grouped_any_kernel(GroupedArgs g) {
 
 // ---- large problems -------------------------------------------------------------------
 
-// A tile of the kernel below.
+constexpr int CUS = 256;
+constexpr int BN = 256;     // columns of a tile
+
+// A workgroup's piece of D.
 struct Tile {
     int group;          // -1: none
     int m0, m_end;      // rows of D (TN: of D[group])
     int n0;
     int k0, k1;         // along the summed axis
+    int tm;             // 64 * tm rows
 };
 
-// Workgroup b's tile.  Workgroups go to the eight XCDs in turn; the first 8 * (tiles / 8)
-// are renumbered so that an XCD has neighbouring tiles, which share rows of A and columns
-// of B in its L2: up to GROUP_M row tiles of a group beside each other, then the next
-// column tile.
-template <int MODE>
+// Lane's group, as its tiles are counted: of 256 rows as far as they go, and for the rows
+// that are left a whole, a half or a quarter of one.
+struct Counts {
+    int lo, end;        // rows of the group
+    int whole;          // row tiles of 256 (129 to 255 left over count as one)
+    int rest;           // 2: a half tile is left over; 1: a quarter; 0: nothing
+};
+// The group of this lane among the 64 from e0 on; `most` is the largest offset before
+// them, and after the call the largest up to their end.
+__device__ __forceinline__ Counts lane_group(const GroupedArgs& g, int e0, int lane, int& most) {
+    const int e = e0 + lane;
+    int end = e < g.groups ? g.offsets[e + 1] : 0;
+    const int begin = max(most, g.offsets[e0]);
+    end = max(begin, lanes_max(end));
+    const int before = __builtin_amdgcn_update_dpp(begin, end, 0x138 /* wave_shr:1 */, 0xf, 0xf, false);
+    most = __builtin_amdgcn_readlane(end, 63);
+    const int lo = min(max(before, 0), g.rows);
+    end = min(max(end, lo), g.rows);
+    const int rows = end - lo, over = rows & 255;
+    return {lo, end, (rows >> 8) + (over > 128), over > 128 || over == 0 ? 0 : over > 64 ? 2 : 1};
+}
+
+// The share of XCD x in n things: [n x / 8, n (x + 1) / 8).
+__device__ __forceinline__ int share(int n, int x) { return (int)((int64_t)n * x / NUM_XCD); }
+
+// Workgroup b's piece.  Workgroups go to the eight XCDs in turn and start in their order.
+//   NN, NT  An XCD takes a run of neighbouring tiles, which share rows of A and columns of
+//           B in its L2.  Where they make few rounds of one to a CU, it is a run of tiles
+//           of each size, the largest first, and whole tiles past the last round are split
+//           in halves or quarters where all CUs together then end sooner (12288 rows over
+//           32 groups of 2048 x 1408: 282 whole tiles, of which 26 would be a round of
+//           their own; 119 us in the groups' order, 100 in this one).  Over many rounds
+//           parts of tiles stay beside their neighbours, whose columns of B they share
+//           (16384 rows over 8 groups of 4096 x 14336: 1787 us with them last, 1747).
+//   TN      The matrices' tiles one group after the other: their work goes by their
+//           groups' rows, so every XCD has its part of every group (a run of groups to an
+//           XCD left one working for 179 us and another for 103).
+template <int MODE, int BM>
 __device__ __forceinline__ Tile tile_at(const GroupedArgs& g, int lane) {
-    constexpr int BM = 256, BN = 256;
     const int tiles_n = (g.N + BN - 1) / BN;
-    Tile t{-1, 0, 0, 0, 0, 0};
-    int total;
-    if constexpr (MODE == GROUPED_TN) total = (g.M + BM - 1) / BM * tiles_n * g.groups;
-    else total = all_row_tiles<BM>(g, lane) * tiles_n;
-    int b = blockIdx.x;
-    if (b >= total) return t;
-    const int per = total / NUM_XCD;
-    if (b < per * NUM_XCD) b = b % NUM_XCD * per + b / NUM_XCD;
-    int tiles_m, local;
+    Tile t{-1, 0, 0, 0, 0, g.K, BM / 64};
     if constexpr (MODE == GROUPED_TN) {
-        tiles_m = (g.M + BM - 1) / BM;
-        t.group = b / (tiles_m * tiles_n);
-        local = b - t.group * tiles_m * tiles_n;
+        const int tiles_m = (g.M + BM - 1) / BM, n = blockIdx.x;
+        t.group = n / (tiles_m * tiles_n);
+        const int in = n - t.group * (tiles_m * tiles_n);
+        t.m0 = in % tiles_m * BM;
+        t.m_end = g.M;
+        t.n0 = in / tiles_m * BN;
         const Rows r = rows_of(g, t.group, lane);
         t.k0 = r.lo;
         t.k1 = r.hi;
-    } else {
-        const RowTile r = row_tile<BM>(g, b / tiles_n, lane);
-        t.group = r.group;
-        tiles_m = r.tiles;
-        local = r.tile * tiles_n + b % tiles_n;
-        t.m0 = r.lo;
-        t.m_end = r.hi;
-        t.k1 = g.K;
+        return t;
     }
-    const int strip = local / (GROUP_M * tiles_n), first = strip * GROUP_M;
-    const int high = min(tiles_m - first, GROUP_M), in = local - strip * GROUP_M * tiles_n;
-    t.m0 += (first + in % high) * BM;
-    t.n0 = in / high * BN;
-    if constexpr (MODE == GROUPED_TN) t.m_end = g.M;
-    // (out of vector divisions: back to scalar registers)
-    t.group = __builtin_amdgcn_readfirstlane(t.group);
-    t.m0 = __builtin_amdgcn_readfirstlane(t.m0);
-    t.m_end = __builtin_amdgcn_readfirstlane(t.m_end);
-    t.n0 = __builtin_amdgcn_readfirstlane(t.n0);
-    t.k0 = __builtin_amdgcn_readfirstlane(t.k0);
-    t.k1 = __builtin_amdgcn_readfirstlane(t.k1);
+    Counts first{};
+    int most = 0, after_first = 0, whole = 0, half = 0, quarter = 0;
+    for (int e0 = 0; e0 < g.groups; e0 += 64) {
+        const Counts c = lane_group(g, e0, lane, most);
+        if (e0 == 0) {
+            first = c;
+            after_first = most;
+        }
+        whole += __builtin_amdgcn_readlane(lanes_sum(c.whole), 63);
+        half += __popcll(__ballot(c.rest == 2));
+        quarter += __popcll(__ballot(c.rest == 1));
+    }
+    whole *= tiles_n;
+    half *= tiles_n;
+    quarter *= tiles_n;
+    // many rounds: a run of all tiles to an XCD, parts of tiles in their place
+    const bool many = whole >= 4 * CUS;
+    const int x = blockIdx.x % NUM_XCD;
+    int n = blockIdx.x / NUM_XCD, part = 0, split = 1, rest = 0;    // rest: 2 the half tiles, 1 the quarters, 0 whole ones
+    if (many) {
+        const int all = whole + half + quarter;
+        n += share(all, x);
+        if (n >= share(all, x + 1)) return t;
+    } else {
+        const int full = whole / CUS * CUS, left = whole - full;
+        split = left * 4 + half + quarter <= CUS ? 4 : left * 2 + half + quarter <= CUS ? 2 : 1;
+        const int a = full / NUM_XCD, b = share(left * split, x + 1) - share(left * split, x);
+        const int c = share(half, x + 1) - share(half, x);
+        if (n < a) {
+            n += x * a;
+        } else if ((n -= a) < b) {
+            n += share(left * split, x);
+            part = n % split;
+            n = full + n / split;
+            t.tm = 4 / split;
+        } else if ((n -= b) < c) {
+            n += share(half, x);
+            rest = t.tm = 2;
+        } else {
+            n += share(quarter, x) - c;
+            rest = t.tm = 1;
+            if (n >= share(quarter, x + 1)) return t;
+        }
+    }
+    // its group
+    int row_tile = n / tiles_n, base = 0;
+    most = after_first;
+    for (int e0 = 0; e0 < g.groups; e0 += 64) {
+        const Counts q = e0 == 0 ? first : lane_group(g, e0, lane, most);
+        const int count = many ? q.whole + (q.rest > 0) : rest == 0 ? q.whole : q.rest == rest;
+        const int upto = base + lanes_sum(count);
+        const uint64_t here = __ballot(row_tile < upto);
+        if (here) {
+            const int l = __ffsll((unsigned long long)here) - 1, of = __builtin_amdgcn_readlane(count, l);
+            const int wholes = __builtin_amdgcn_readlane(q.whole, l);
+            row_tile -= __builtin_amdgcn_readlane(upto, l) - of;
+            t.group = e0 + l;
+            t.m_end = __builtin_amdgcn_readlane(q.end, l);
+            t.m0 = __builtin_amdgcn_readlane(q.lo, l);
+            if (rest) {
+                t.m0 += wholes * 256;
+                t.n0 = n % tiles_n * BN;
+            } else {
+                // up to GROUP_M row tiles beside each other, then the next column tile
+                const int local = row_tile * tiles_n + n % tiles_n, s = local / (GROUP_M * tiles_n);
+                const int high = min(of - s * GROUP_M, GROUP_M), in = local - s * GROUP_M * tiles_n;
+                const int m = s * GROUP_M + in % high;
+                if (m == wholes) t.tm = __builtin_amdgcn_readlane(q.rest, l);
+                t.m0 += m * 256 + part * 64 * t.tm;
+                t.n0 = in / high * BN;
+                if (t.m0 >= t.m_end) t.group = -1;      // (a part of a tile that is not full)
+            }
+            return t;
+        }
+        base = __builtin_amdgcn_readlane(upto, 63);
+    }
     return t;
+}
+// The most workgroups that this takes: row tiles of the groups, the parts past the last
+// round, and what the XCDs' shares round up.
+int64_t tile_workgroups(const GroupedArgs& a) {
+    const int64_t tn = (a.N + BN - 1) / BN;
+    return tn * (a.rows / 256 + (a.rows < a.groups ? a.rows : a.groups)) + CUS + 4 * NUM_XCD;
+}
+
+// (out of vector divisions: back to scalar registers)
+__device__ __forceinline__ Tile scalar(const Tile& t) {
+    return {__builtin_amdgcn_readfirstlane(t.group), __builtin_amdgcn_readfirstlane(t.m0),
+            __builtin_amdgcn_readfirstlane(t.m_end), __builtin_amdgcn_readfirstlane(t.n0),
+            __builtin_amdgcn_readfirstlane(t.k0), __builtin_amdgcn_readfirstlane(t.k1),
+            __builtin_amdgcn_readfirstlane(t.tm)};
 }
 
 constexpr uint32_t NOWHERE = 0x80000000u;   // a lane offset past every buffer range: the load gives zeros
 
-// One operand of a tile: 64 * TT rows (KC), or columns of KS rows, by 64 bytes of the
-// summed axis to a stage.  Direct loads move 1 KiB an instruction: 16 rows of 64 bytes
-// (KC), or 2 rows of 512 (KS, always 256 columns).  The swizzle is on the global side:
+// One operand of a tile: 64 * TT rows (KC), or columns of KS rows (TT 4 or 2), by 64 bytes
+// of the summed axis to a stage.  Direct loads move 1 KiB an instruction: 16 rows of 64
+// bytes (KC), or 2 rows of 512 (KS; 4 of 256 with TT 2).  The swizzle is on the global side:
 // the lane that fills a chunk of LDS reads the chunk that belongs there.
 template <bool KS, int TT, int ES>
 struct Operand {
-    static constexpr int PIECES = KS ? 4 : TT;      // a wave's
+    static constexpr int PIECES = TT;       // a wave's
     static constexpr int BYTES = PIECES * 4096;
-    static constexpr int ROW = KS ? 512 : 64;
+    static constexpr int ROW = KS ? 128 * TT : 64, LANES = ROW / 16;    // bytes of a row, lanes that load it
+    static_assert(!KS || (ES == 2 && TT >= 2), "16-bit rows of at least 128 columns across the summed axis");
     static constexpr int KROWS = 64 / ES;
     uint32_t voff[PIECES];  // from the K tile's first byte; NOWHERE for rows or columns past the end
     int idx[PIECES];        // KC: the chunk's byte along the summed axis; KS: its row
     uint64_t base;          // of K tile 0
     int64_t step;           // bytes to the next K tile
+    int64_t back_b;         // bytes by which the last K tile begins earlier
+    int have;               // what all K tiles hold along the summed axis, in the units of idx
     uint32_t read0;         // LDS offset of this lane's operand of step 0, 32-row tile 0
 
-    // rows (columns) [r0, end) of the operand at p, summed from k0 on
-    __device__ __forceinline__ void init(const char* p, int64_t ld, int r0, int end, int k0, int wave, int lane,
-                                         int w_half) {
+    // rows (columns) [r0, end) of the operand at p, summed over `keys` from k0 on, the last
+    // tile `back` elements earlier
+    __device__ __forceinline__ void init(const char* p, int64_t ld, int r0, int end, int k0, int keys, int back,
+                                         int wave, int lane, int w_half) {
+        back_b = back * (KS ? ld : ES);
+        have = (keys + back) * (KS ? 1 : ES);
         if constexpr (KS) {
             base = (uint64_t)(uintptr_t)p + (uint64_t)((int64_t)k0 * ld + (int64_t)r0 * ES);
             step = (int64_t)KROWS * ld;
@@ -357,8 +450,8 @@ struct Operand {
 #pragma unroll
         for (int u = 0; u < PIECES; ++u) {
             if constexpr (KS) {
-                const int row = (wave * PIECES + u) * 2 + (lane >> 5);
-                const uint32_t c = (uint32_t)(lane & 31) ^ swz_b<2>(row);
+                const int row = (wave * PIECES + u) * (64 / LANES) + lane / LANES;
+                const uint32_t c = (uint32_t)(lane % LANES) ^ swz_b<2>(row);
                 idx[u] = row;
                 voff[u] = r0 + (int)c * 8 < end ? (uint32_t)row * (uint32_t)ld + c * 16u : NOWHERE;
             } else {
@@ -372,7 +465,7 @@ struct Operand {
         const int first = w_half * 32 * TT;     // this wave's first row (column)
         if constexpr (KS) {
             const uint32_t col = first + 16 * (grp & 1), k = 8 * (grp >> 1) + (gp >> 2);
-            read0 = k * 512 + ((((col >> 3) + ((gp & 3) >> 1)) ^ swz_b<2>(k)) << 4) + 8 * (gp & 1);
+            read0 = k * ROW + ((((col >> 3) + ((gp & 3) >> 1)) ^ swz_b<2>(k)) << 4) + 8 * (gp & 1);
         } else {
             const uint32_t r = first + lrow;
             read0 = r * 64 + ((lhalf ^ swz_a<4>(r)) << 4);
@@ -383,18 +476,21 @@ struct Operand {
         const uint32_t v = idx[u] < left ? voff[u] : NOWHERE;
         lds_dma16<0, true>(rsrc, stage + (wave * PIECES + u) * 1024, v, 0u);
     }
-    __device__ __forceinline__ i32x4 rsrc(int t, bool live) const {
-        return rsrc_words(base + (uint64_t)((int64_t)t * step), live ? 0x7fffffffu : 0u);
+    // K tile t of nt, at `at`: its buffer (empty past the last), and the next one's place
+    __device__ __forceinline__ i32x4 rsrc(uint64_t& at, int t, int nt) const {
+        const i32x4 r = rsrc_words(t == nt - 1 ? at - (uint64_t)back_b : at, t < nt ? 0x7fffffffu : 0u);
+        at += (uint64_t)step;
+        return r;
     }
-    // what K tile t has left, up to `keys` along the summed axis in all
-    __device__ __forceinline__ static int left(int t, int keys) { return KS ? keys - t * KROWS : (keys - t * KROWS) * ES; }
+    // what it holds along the summed axis (and more)
+    __device__ __forceinline__ int left(int t) const { return have - t * (KS ? KROWS : 64); }
     // the MFMA operand of step s (0, 1) and 32-row tile i
     __device__ __forceinline__ u32x4 read(const MPDT_LDS char* stage, int s, int i) const {
         if constexpr (KS) {
-            // (16 rows on, the swizzle repeats; 32 columns are four chunks on, which
-            // the swizzle may turn over: bits 1 to 3 of the chunk)
-            const uint32_t o = (read0 ^ (uint32_t)((i & 3) * 64)) + s * 16 * 512;
-            const u32x2 x = lds_read_tr16(stage, o), y = lds_read_tr16(stage, o + 4 * 512);
+            // (4 rows on, the swizzle repeats; 32 columns on are bits 2 and 3 of the
+            // chunk, which the swizzle may have turned over)
+            const uint32_t o = (read0 ^ (uint32_t)(i * 64)) + s * 16 * ROW;
+            const u32x2 x = lds_read_tr16(stage, o), y = lds_read_tr16(stage, o + 4 * ROW);
             return u32x4{x[0], x[1], y[0], y[1]};
         } else {
             return lds_load16(stage, (read0 ^ (uint32_t)(s * 32)) + i * 32 * 64);
@@ -402,133 +498,180 @@ struct Operand {
     }
 };
 
-// The tile's product by four waves, one to a SIMD: 64 * TM x 256 of D, 32 * TM x 128 a
-// wave (TM 4, 2 or 1: 256, 128 or 64 rows), accumulated in registers for the whole of k.
-// A stage holds 64 bytes of k of both operands; NS stages are loaded ahead.  For K tile t:
+// A tile's product by four waves, one to a SIMD: 64 * TM x 256 of D, 32 * TM x 128 a wave
+// (TM 4, 2 or 1), accumulated in registers for the whole of k.  A stage holds 64 bytes of k
+// of both operands; NS stages are loaded ahead.  For K tile t:
 //   phase X: MFMAs of its first step, among them the reads of the second step's operands
 //            and the direct loads of B of tile t - 1 + NS;
 //   wait for tile t + 1's loads and this wave's reads, barrier;
 //   phase Y: MFMAs of the second step, among them the reads of tile t + 1's first step and
 //            the direct loads of A of tile t + NS (into the stage of tile t).
 // Tiles past the last load nothing (an empty buffer range), so that the count of loads in
-// flight is the same everywhere.
-template <GroupedType T, int MODE, int TM, class Acc>
-__device__ __forceinline__ void tile_product(const GroupedArgs& g, const Tile& t, MPDT_LDS char* lds, int wave, int lane,
-                                             Acc (&acc)[TM][4]) {
+// flight is the same everywhere.  Where rows along k end inside a 16-byte piece, the last
+// tile is the 64 bytes that end with them: what it repeats of the tile before is cleared
+// in both operands.
+template <GroupedType T, int MODE, int TM, int LDS>
+struct Product {
     using F = Fmt<KindOf<T>::kind>;
-    constexpr int ES = F::ES;
+    using Acc = typename F::Acc;
+    static constexpr int ES = F::ES;
     using OpA = Operand<MODE == GROUPED_TN, TM, ES>;
     using OpB = Operand<MODE != GROUPED_NT, 4, ES>;
-    constexpr int STAGE = OpA::BYTES + OpB::BYTES;
-    constexpr int NS = TM == 4 ? 4 : TM == 2 ? 5 : 6;
-    constexpr int LOADS = OpA::PIECES + OpB::PIECES;
-    constexpr int NM = TM * 4, GROUPS = TM + 3;     // MFMAs of a step; operand reads: A0 and B0, B1, B2, B3, A1 ..
-    const int keys = t.k1 - t.k0;
-    const int nt = (keys + OpA::KROWS - 1) / OpA::KROWS;
-    const int wm = wave >> 1, wn = wave & 1;
+    static constexpr int STAGE = OpA::BYTES + OpB::BYTES;
+    static constexpr int NS = LDS / STAGE < 6 ? LDS / STAGE : 6;
+    static constexpr int LOADS = OpA::PIECES + OpB::PIECES;
+    static constexpr int NM = TM * 4, GROUPS = TM + 3;  // MFMAs of a step; operand reads: A0 and B0, B1, B2, B3, A1 ..
     OpA A;
     OpB B;
-    A.init(g.A, g.lda_b, t.m0, t.m_end, t.k0, wave, lane, wm);
-    B.init(MODE == GROUPED_TN ? g.B : g.B + t.group * g.group_b, g.ldb_b, t.n0, g.N, t.k0, wave, lane, wn);
+    int keys, nt, back;
 
-    u32x4 fa[2][TM], fb[2][4];
-    auto read_group = [&](int s, int r, const MPDT_LDS char* stage) {
-        if (r == 0) fa[s][0] = A.read(stage, s, 0);
-        if (r <= 3) fb[s][r] = B.read(stage + OpA::BYTES, s, r);
-        else fa[s][r - 3] = A.read(stage, s, r - 3);
-    };
-    // (the operands change places: a lane then holds four neighbouring columns of a row)
-    auto mma = [&](int s, int i) { acc[i / 4][i % 4] = F::mma(fb[s][i % 4], fa[s][i / 4], acc[i / 4][i % 4]); };
-
-    i32x4 rb{};     // B's buffer of the tile whose loads are due next
-    int left_b = 0;
-#pragma unroll
-    for (int p = 0; p < NS; ++p) {
-        const i32x4 ra = A.rsrc(p, p < nt);
-        rb = B.rsrc(p, p < nt);
-        left_b = OpB::left(p, keys);
-        static_for<0, OpA::PIECES>([&](auto U) { A.load(decltype(U)::value, ra, lds + p * STAGE, wave, OpA::left(p, keys)); });
-        if (p < NS - 1)
-            static_for<0, 4>([&](auto U) { B.load(decltype(U)::value, rb, lds + p * STAGE + OpA::BYTES, wave, left_b); });
+    __device__ __forceinline__ void init(const GroupedArgs& g, const Tile& t, int wave, int lane) {
+        keys = t.k1 - t.k0;
+        nt = (keys + OpA::KROWS - 1) / OpA::KROWS;
+        back = MODE != GROUPED_TN && keys * ES % 16 ? nt * OpA::KROWS - keys : 0;
+        A.init(g.A, g.lda_b, t.m0, t.m_end, t.k0, keys, back, wave, lane, wave >> 1);
+        B.init(MODE == GROUPED_TN ? g.B : g.B + t.group * g.group_b, g.ldb_b, t.n0, g.N, t.k0, keys, back, wave, lane,
+               wave & 1);
     }
-    wait_vmem<(NS - 2) * LOADS + OpA::PIECES>();
-    wg_barrier();
+
+    // The product into acc; LDS is free when every wave has returned.
+    __device__ __forceinline__ void run(MPDT_LDS char* lds, int wave, int lane, Acc (&acc)[TM][4]) const {
+        uint64_t at_a = A.base, at_b = B.base;
+        i32x4 rb{};     // B's buffer of the tile whose loads are due next
+        int left_b = 0;
 #pragma unroll
-    for (int r = 0; r < GROUPS; ++r) read_group(0, r, lds);
-    int cur = 0;
-    for (int k = 0; k < nt - 1; ++k) {
-        const int next = cur + 1 == NS ? 0 : cur + 1, prev = cur == 0 ? NS - 1 : cur - 1;
+        for (int p = 0; p < NS; ++p) {
+            const i32x4 ra = A.rsrc(at_a, p, nt);
+            const int left_a = A.left(p);
+            rb = B.rsrc(at_b, p, nt);
+            left_b = B.left(p);
+            static_for<0, OpA::PIECES>([&](auto U) { A.load(decltype(U)::value, ra, lds + p * STAGE, wave, left_a); });
+            if (p < NS - 1)
+                static_for<0, 4>([&](auto U) { B.load(decltype(U)::value, rb, lds + p * STAGE + OpA::BYTES, wave, left_b); });
+        }
+        u32x4 fa[2][TM], fb[2][4];
+        auto read_group = [&](int s, int r, const MPDT_LDS char* stage) {
+            if (r == 0) fa[s][0] = A.read(stage, s, 0);
+            if (r <= 3) fb[s][r] = B.read(stage + OpA::BYTES, s, r);
+            else fa[s][r - 3] = A.read(stage, s, r - 3);
+        };
+        // (the operands change places: a lane then holds four neighbouring columns of a row)
+        auto mma = [&](int s, int i) { acc[i / 4][i % 4] = F::mma(fb[s][i % 4], fa[s][i / 4], acc[i / 4][i % 4]); };
+
+        wait_vmem<(NS - 2) * LOADS + OpA::PIECES>();
+        wg_barrier();
+#pragma unroll
+        for (int r = 0; r < GROUPS; ++r) read_group(0, r, lds);
+        int cur = 0;
+        for (int k = 0; k < nt - 1; ++k) {
+            const int next = cur + 1 == NS ? 0 : cur + 1, prev = cur == 0 ? NS - 1 : cur - 1;
+            MPDT_LDS char* const sc = lds + cur * STAGE;
+            MPDT_LDS char* const sn = lds + next * STAGE;
+            MPDT_LDS char* const sp = lds + prev * STAGE + OpA::BYTES;
+            i32x4 ra, rb2;
+            int left_a, left_b2;
+            static_for<0, NM>([&](auto I) {
+                constexpr int i = decltype(I)::value;
+                mma(0, i);
+                if constexpr (i < GROUPS) read_group(1, i, sc);
+                if constexpr (i == NM / 2) {
+                    ra = A.rsrc(at_a, k + NS, nt);
+                    left_a = A.left(k + NS);
+                }
+                if constexpr (i == NM / 2 + 1) {
+                    rb2 = B.rsrc(at_b, k + NS, nt);
+                    left_b2 = B.left(k + NS);
+                }
+                // B's four loads on the last slots, every second one where there are 16
+                constexpr int STEP = TM == 4 ? 2 : 1, FIRST = NM - 1 - 3 * STEP;
+                if constexpr (i >= FIRST && (i - FIRST) % STEP == 0) B.load((i - FIRST) / STEP, rb, sp, wave, left_b);
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            wait_vmem<(NS - 2) * LOADS>();
+            wait_lds();
+            wg_barrier();
+            static_for<0, NM>([&](auto I) {
+                constexpr int i = decltype(I)::value;
+                mma(1, i);
+                if constexpr (i % 4 == 0) A.load(i / 4, ra, sc, wave, left_a);
+                // the reads in between: slots 1, 3, 5 .. of 16; every other free one of fewer
+                if constexpr (TM == 4) {
+                    if constexpr (i % 2 == 1 && i / 2 < GROUPS) read_group(0, i / 2, sn);
+                } else if constexpr (TM == 2) {
+                    if constexpr (i % 4 != 0 && i - 1 - i / 4 < GROUPS) read_group(0, i - 1 - i / 4, sn);
+                } else {
+                    read_group(0, i, sn);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            rb = rb2;
+            left_b = left_b2;
+            cur = next;
+        }
         MPDT_LDS char* const sc = lds + cur * STAGE;
-        MPDT_LDS char* const sn = lds + next * STAGE;
-        MPDT_LDS char* const sp = lds + prev * STAGE + OpA::BYTES;
-        i32x4 ra, rb2;
-        int left_a, left_b2;
+        auto clear = [&](int s) {
+            const int n = min(max(back * ES - s * 32 - (lane >> 5) * 16, 0), 16);
+#pragma unroll
+            for (int i = 0; i < TM; ++i) fa[s][i] = mask_head(fa[s][i], n);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) fb[s][i] = mask_head(fb[s][i], n);
+        };
+        if (back) clear(0);
         static_for<0, NM>([&](auto I) {
             constexpr int i = decltype(I)::value;
             mma(0, i);
             if constexpr (i < GROUPS) read_group(1, i, sc);
-            if constexpr (i == NM / 2) {
-                ra = A.rsrc(k + NS, k + NS < nt);
-                left_a = OpA::left(k + NS, keys);
-            }
-            if constexpr (i == NM / 2 + 1) {
-                rb2 = B.rsrc(k + NS, k + NS < nt);
-                left_b2 = OpB::left(k + NS, keys);
-            }
-            // B's four loads on the last slots, every second one where there are 16
-            constexpr int STEP = TM == 4 ? 2 : 1, FIRST = NM - 1 - 3 * STEP;
-            if constexpr (i >= FIRST && (i - FIRST) % STEP == 0) B.load((i - FIRST) / STEP, rb, sp, wave, left_b);
             __builtin_amdgcn_sched_barrier(0);
         });
-        wait_vmem<(NS - 2) * LOADS>();
         wait_lds();
-        wg_barrier();
-        static_for<0, NM>([&](auto I) {
-            constexpr int i = decltype(I)::value;
-            mma(1, i);
-            if constexpr (i % 4 == 0) A.load(i / 4, ra, sc, wave, left_a);
-            // the reads in between: slots 1, 3, 5 .. of 16; every other free one of fewer
-            if constexpr (TM == 4) {
-                if constexpr (i % 2 == 1 && i / 2 < GROUPS) read_group(0, i / 2, sn);
-            } else if constexpr (TM == 2) {
-                if constexpr (i % 4 != 0 && i - 1 - i / 4 < GROUPS) read_group(0, i - 1 - i / 4, sn);
-            } else {
-                read_group(0, i, sn);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        });
-        rb = rb2;
-        left_b = left_b2;
-        cur = next;
-    }
-    MPDT_LDS char* const sc = lds + cur * STAGE;
-    static_for<0, NM>([&](auto I) {
-        constexpr int i = decltype(I)::value;
-        mma(0, i);
-        if constexpr (i < GROUPS) read_group(1, i, sc);
-        __builtin_amdgcn_sched_barrier(0);
-    });
-    wait_lds();
+        if (back) clear(1);
 #pragma unroll
-    for (int i = 0; i < NM; ++i) mma(1, i);
-    // (the empty loads write zeros: they land before LDS is used again)
-    wait_vmem<0>();
+        for (int i = 0; i < NM; ++i) mma(1, i);
+        // (the empty loads write zeros: they land before LDS is used again)
+        wait_vmem<0>();
+    }
+};
+
+// Four neighbouring values of a vector of n, from c on; 0 past its end.
+__device__ __forceinline__ f32x4 four_of(const float* p, int c, int n) {
+    typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+    if (c + 4 <= n) {
+        const f32x4_any v = *reinterpret_cast<const f32x4_any*>(p + c);
+        return f32x4{v[0], v[1], v[2], v[3]};
+    }
+    f32x4 v{0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+        if (c + e < n) v[e] = p[c + e];
+    return v;
 }
 
 // D from the accumulators, through LDS so that it leaves in 16-byte pieces of rows: a wave
-// has 32 KiB of its own for 32 * TM rows of 128 columns (FP32: half as many at a time).
-// Lane element r of a 32 x 32 block: row lane % 32, column 8 (r / 4) + 4 (lane / 32) + r % 4.
-template <GroupedType T, int MODE, int TM, class Out, class Acc>
-__device__ __forceinline__ void tile_store(const GroupedArgs& g, const Tile& t, MPDT_LDS char* lds, int wave, int lane,
-                                           const Acc (&acc)[TM][4]) {
+// has a quarter of LDS for as many of its blocks of 32 rows by 128 columns as fit.  Lane
+// element r of a 32 x 32 block: row lane % 32, column 8 (r / 4) + 4 (lane / 32) + r % 4.
+// (m_own, n_own: a tile that was moved back to end with the operand stores from there on)
+template <GroupedType T, int MODE, int TM, int LDS, class Out, class Acc>
+__device__ __forceinline__ void tile_store(const GroupedArgs& g, const Tile& t, int m_own, int n_own, MPDT_LDS char* lds,
+                                           int wave, int lane, const Acc (&acc)[TM][4]) {
     constexpr int ES = (int)sizeof(Out), ROW = 128 * ES, CHUNKS = ROW / 16, PER = 16 / ES;
-    constexpr int STEP = ES == 2 ? TM : TM < 2 ? TM : 2;   // 32-row blocks at a time
+    constexpr int FIT = LDS / 4 / (32 * ROW), STEP = FIT >= TM ? TM : FIT >= 2 ? 2 : 1;
+    static_assert(FIT >= 1, "a block of a wave's rows fits its quarter of LDS");
+    typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
     const int wm = wave >> 1, wn = wave & 1, lrow = lane & 31, lhalf = lane >> 5;
-    MPDT_LDS char* const own = lds + wave * 32768;
     const int row0 = t.m0 + wm * 32 * TM, col0 = t.n0 + wn * 128;
-    Out* const D = reinterpret_cast<Out*>(g.D) + (MODE == GROUPED_TN ? t.group * g.group_d : 0);
-    const bool wide = (uintptr_t)D % 16 == 0 && g.ldd % PER == 0;
     wg_barrier();       // every wave is done with the stages
+    if (row0 >= t.m_end || col0 >= g.N) return;     // (the whole wave)
+    MPDT_LDS char* const own = lds + wave * (LDS / 4);
+    Out* const D = reinterpret_cast<Out*>(g.D) + (MODE == GROUPED_TN ? t.group * g.group_d : 0);
+    f32x4 ws[T == GroupedType::I8 ? 16 : 1], bias[T == GroupedType::I8 ? 16 : 1];
+    if constexpr (T == GroupedType::I8) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int col = col0 + (i >> 2) * 32 + 8 * (i & 3) + 4 * lhalf;
+            ws[i] = four_of(g.w_scale + t.group * g.ld_ws, col, g.N);
+            bias[i] = g.bias ? four_of(g.bias + t.group * g.ld_bias, col, g.N) : f32x4{-0.0f, -0.0f, -0.0f, -0.0f};
+        }
+    }
 #pragma unroll
     for (int i0 = 0; i0 < TM; i0 += STEP) {
 #pragma unroll
@@ -542,20 +685,15 @@ __device__ __forceinline__ void tile_store(const GroupedArgs& g, const Tile& t, 
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int col = j * 32 + 8 * q + 4 * lhalf;
                     float v[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        if constexpr (T == GroupedType::I8) {
-                            const int c = min(col0 + col + e, g.N - 1);
-                            v[e] = mul_rn(mul_rn((float)acc[i][j][4 * q + e], xs), g.w_scale[t.group * g.ld_ws + c]);
-                            if (g.bias) v[e] = add_rn(v[e], g.bias[t.group * g.ld_bias + c]);
-                        } else {
-                            v[e] = acc[i][j][4 * q + e];
-                        }
+                        if constexpr (T == GroupedType::I8)     // (x + -0 is x)
+                            v[e] = add_rn(mul_rn(mul_rn((float)acc[i][j][4 * q + e], xs), ws[4 * j + q][e]), bias[4 * j + q][e]);
+                        else v[e] = acc[i][j][4 * q + e];
                     }
                     // chunk c of row r lies at c ^ r: rows beside each other in other banks
-                    const uint32_t r = (i - i0) * 32 + lrow, c = (uint32_t)(col * ES) / 16;
+                    const uint32_t r = (i - i0) * 32 + lrow, c = (uint32_t)((j * 32 + 8 * q + 4 * lhalf) * ES) / 16;
                     MPDT_LDS char* const p = own + r * ROW + ((c ^ (r % CHUNKS)) << 4);
                     if constexpr (ES == 4) {
                         *(MPDT_LDS f32x4*)p = f32x4{v[0], v[1], v[2], v[3]};
@@ -574,15 +712,15 @@ __device__ __forceinline__ void tile_store(const GroupedArgs& g, const Tile& t, 
             const int n = q * 64 + lane, r = n / CHUNKS, c = n % CHUNKS;
             const u32x4 v = lds_load16(own, r * ROW + ((c ^ (r % CHUNKS)) << 4));
             const int row = row0 + i0 * 32 + r, col = col0 + c * PER;
-            if (row >= t.m_end || col >= g.N) continue;
+            if (row >= t.m_end || row < m_own) continue;
             Out* const to = D + (int64_t)row * g.ldd + col;
-            if (wide && col + PER <= g.N) {
-                *reinterpret_cast<u32x4*>(to) = v;
+            if (col >= n_own && col + PER <= g.N) {
+                *reinterpret_cast<u32x4_any*>(to) = v;
             } else {
 #pragma unroll
                 for (int e = 0; e < PER; ++e) {
                     const uint32_t w = v[e * ES / 4];
-                    if (col + e < g.N) {
+                    if (col + e >= n_own && col + e < g.N) {
                         if constexpr (ES == 4) to[e] = __uint_as_float(w);
                         else to[e] = (uint16_t)(w >> (16 * (e & 1)));
                     }
@@ -594,8 +732,8 @@ __device__ __forceinline__ void tile_store(const GroupedArgs& g, const Tile& t, 
     }
 }
 
-template <GroupedType T, int MODE, int TM>
-__device__ __forceinline__ void tile_run(const GroupedArgs& g, const Tile& t, MPDT_LDS char* lds, int wave, int lane) {
+template <GroupedType T, int MODE, int TM, int LDS>
+__device__ __forceinline__ void tile_run(const GroupedArgs& g, Tile t, MPDT_LDS char* lds, int wave, int lane) {
     typename Fmt<KindOf<T>::kind>::Acc acc[TM][4];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
@@ -603,31 +741,47 @@ __device__ __forceinline__ void tile_run(const GroupedArgs& g, const Tile& t, MP
         for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
-    if (t.k1 > t.k0) tile_product<T, MODE, TM>(g, t, lds, wave, lane, acc);
+    // rows across k that end inside a 16-byte piece: the last tile ends with them
+    const int m_own = t.m0, n_own = t.n0;
+    if (MODE == GROUPED_TN && g.M % 8) t.m0 = min(t.m0, g.M - 64 * TM);
+    if (MODE != GROUPED_NT && g.N % 8) t.n0 = min(t.n0, g.N - BN);
+    if (t.k1 > t.k0) {
+        Product<T, MODE, TM, LDS> p;
+        p.init(g, t, wave, lane);
+        p.run(lds, wave, lane, acc);
+    }
     if constexpr (T == GroupedType::I8) {
-        tile_store<T, MODE, TM, uint16_t>(g, t, lds, wave, lane, acc);
+        tile_store<T, MODE, TM, LDS, uint16_t>(g, t, m_own, n_own, lds, wave, lane, acc);
     } else {
-        if (g.out16) tile_store<T, MODE, TM, uint16_t>(g, t, lds, wave, lane, acc);
-        else tile_store<T, MODE, TM, float>(g, t, lds, wave, lane, acc);
+        if (g.out16) tile_store<T, MODE, TM, LDS, uint16_t>(g, t, m_own, n_own, lds, wave, lane, acc);
+        else tile_store<T, MODE, TM, LDS, float>(g, t, m_own, n_own, lds, wave, lane, acc);
     }
 }
 
-// 256 x 256 tiles of problems whose rows are whole 16-byte pieces (of any alignment).
+// 256 x 256 tiles, one workgroup to a CU.
 template <GroupedType T, int MODE>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void grouped_tile_kernel(GroupedArgs g) {
-    __shared__ __attribute__((aligned(1024))) char lds[131072];
+    constexpr int LDS = 131072;
+    __shared__ __attribute__((aligned(1024))) char lds_[LDS];
+    MPDT_LDS char* const lds = lds_cast(lds_);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const Tile t = tile_at<MODE>(g, lane);
+    const Tile t = scalar(tile_at<MODE, 256>(g, lane));
     if (t.group < 0) return;    // (the whole workgroup)
-    if constexpr (MODE == GROUPED_TN) {
-        tile_run<T, MODE, 4>(g, t, lds_cast(lds), wave, lane);
-    } else {
-        // the last rows of a group may fill a half or a quarter of a tile
-        const int rows = t.m_end - t.m0;
-        if (rows > 128) tile_run<T, MODE, 4>(g, t, lds_cast(lds), wave, lane);
-        else if (rows > 64) tile_run<T, MODE, 2>(g, t, lds_cast(lds), wave, lane);
-        else tile_run<T, MODE, 1>(g, t, lds_cast(lds), wave, lane);
-    }
+    if (t.tm == 4) tile_run<T, MODE, 4, LDS>(g, t, lds, wave, lane);
+    else if (t.tm == 2) tile_run<T, MODE, 2, LDS>(g, t, lds, wave, lane);
+    else tile_run<T, MODE, 1, LDS>(g, t, lds, wave, lane);
+}
+
+// The weights' gradient: 128 x 256 tiles, two workgroups to a CU.  A group's rows make a
+// short sum, so that a tile's beginning and its store take as long as its product (384
+// rows: 2 + 3 us and 10); another workgroup's product goes on meanwhile.
+template <GroupedType T>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void grouped_grad_kernel(GroupedArgs g) {
+    constexpr int LDS = 73728;
+    __shared__ __attribute__((aligned(1024))) char lds_[LDS];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Tile t = scalar(tile_at<GROUPED_TN, 128>(g, lane));
+    tile_run<T, GROUPED_TN, 2, LDS>(g, t, lds_cast(lds_), wave, lane);
 }
 
 // The most row tiles of BM rows that the groups can have.
@@ -646,20 +800,23 @@ hipError_t launch_any(const GroupedArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Whether the direct loads can take a problem: operands' rows end on a 16-byte piece, and
-// a tile's offsets fit in 32 bits.
+// Whether the direct loads can take a problem: a tile's offsets fit in 32 bits, and where
+// rows end inside a 16-byte piece there is a whole tile to end with them.
 template <GroupedType T, int MODE>
-bool whole_pieces(const GroupedArgs& a) {
+bool by_tiles(const GroupedArgs& a) {
     constexpr int ES = T == GroupedType::I8 ? 1 : 2;
-    const int64_t row_a = (int64_t)(MODE == GROUPED_TN ? a.M : a.K) * ES;
-    const int64_t row_b = (int64_t)(MODE == GROUPED_NT ? a.K : a.N) * ES;
-    return row_a % 16 == 0 && row_b % 16 == 0 && a.lda_b < (1 << 23) && a.ldb_b < (1 << 23);
+    if (a.lda_b >= (1 << 23) || a.ldb_b >= (1 << 23)) return false;
+    if (MODE != GROUPED_TN && a.K * (int64_t)ES % 16 && a.K < 64 / ES) return false;
+    if (MODE != GROUPED_NT && a.N % 8 && a.N < BN) return false;
+    return MODE != GROUPED_TN || a.M % 8 == 0 || a.M >= 128;
 }
 
 template <GroupedType T, int MODE>
 hipError_t launch_mode(const GroupedArgs& a, hipStream_t stream) {
-    if (!whole_pieces<T, MODE>(a)) return launch_any<T, MODE>(a, stream);
-    grouped_tile_kernel<T, MODE><<<dim3((unsigned)grouped_tiles(MODE, a, 256, 256)), dim3(256), 0, stream>>>(a);
+    if (!by_tiles<T, MODE>(a)) return launch_any<T, MODE>(a, stream);
+    if constexpr (MODE == GROUPED_TN)
+        grouped_grad_kernel<T><<<dim3((unsigned)grouped_tiles(MODE, a, 128, BN)), dim3(256), 0, stream>>>(a);
+    else grouped_tile_kernel<T, MODE><<<dim3((unsigned)tile_workgroups(a)), dim3(256), 0, stream>>>(a);
     return hipGetLastError();
 }
 

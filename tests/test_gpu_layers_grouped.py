@@ -58,6 +58,13 @@ SIZES = [
     ([513, 511], 520, 257),
     ([40, 260], 1000, 1000),
     ([700], 2056, 300),
+    ([300, 0, 200], 1003, 611),         # rows that end inside a vector, along and across the sum
+    ([130, 70], 77, 301),
+    ([260, 1], 33, 259),
+    ([129, 255, 64], 47, 1025),
+    ([70000], 16, 264),                 # more whole tiles than two rounds of the card
+    ([300, 20000, 90, 40000, 5, 70, 8000], 24, 300),
+    ([257, 0, 100] * 40, 8, 16),        # whole and part tiles past the 64th group
 ]
 
 
