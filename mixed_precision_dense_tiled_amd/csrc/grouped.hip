@@ -265,6 +265,7 @@ struct Tile {
     int n0;
     int k0, k1;         // along the summed axis
     int tm;             // 64 * tm rows
+    int turn;           // NT: column tile n begins with K tile n * turn
 };
 
 // Lane's group, as its tiles are counted: of 256 rows as far as they go, and for the rows
@@ -289,6 +290,14 @@ __device__ __forceinline__ Counts lane_group(const GroupedArgs& g, int e0, int l
     return {lo, end, (rows >> 8) + (over > 128), over > 128 || over == 0 ? 0 : over > 64 ? 2 : 1};
 }
 
+// B^T's rows lie K apart: workgroups that walk along k in step read from the same few
+// memory channels wherever K is a multiple of their round.  Column tile n therefore begins
+// n times this many bytes further on, an odd number of 128-byte lines, and goes round
+// (16 matrices of 4096 x 4096 BF16 over 128 rows: 128 us in step, 98 so; INT8 over 1536
+// rows 77 and 62).  Where many tiles share rows of A, they walk in step, for their L2's sake
+// (8192 rows, 4096 x 14336: 904 us, 938 with turns).
+constexpr int TURN_BYTES = 1920, TURN = TURN_BYTES / 64;
+
 // The share of XCD x in n things: [n x / 8, n (x + 1) / 8).
 __device__ __forceinline__ int share(int n, int x) { return (int)((int64_t)n * x / NUM_XCD); }
 
@@ -307,7 +316,7 @@ __device__ __forceinline__ int share(int n, int x) { return (int)((int64_t)n * x
 template <int MODE, int BM>
 __device__ __forceinline__ Tile tile_at(const GroupedArgs& g, int lane) {
     const int tiles_n = (g.N + BN - 1) / BN;
-    Tile t{-1, 0, 0, 0, 0, g.K, BM / 64};
+    Tile t{-1, 0, 0, 0, 0, g.K, BM / 64, 0};
     if constexpr (MODE == GROUPED_TN) {
         const int tiles_m = (g.M + BM - 1) / BM, n = blockIdx.x;
         t.group = n / (tiles_m * tiles_n);
@@ -337,6 +346,7 @@ __device__ __forceinline__ Tile tile_at(const GroupedArgs& g, int lane) {
     quarter *= tiles_n;
     // many rounds: a run of all tiles to an XCD, parts of tiles in their place
     const bool many = whole >= 4 * CUS;
+    t.turn = many ? 0 : TURN;
     const int x = blockIdx.x % NUM_XCD;
     int n = blockIdx.x / NUM_XCD, part = 0, split = 1, rest = 0;    // rest: 2 the half tiles, 1 the quarters, 0 whole ones
     if (many) {
@@ -410,7 +420,7 @@ __device__ __forceinline__ Tile scalar(const Tile& t) {
     return {__builtin_amdgcn_readfirstlane(t.group), __builtin_amdgcn_readfirstlane(t.m0),
             __builtin_amdgcn_readfirstlane(t.m_end), __builtin_amdgcn_readfirstlane(t.n0),
             __builtin_amdgcn_readfirstlane(t.k0), __builtin_amdgcn_readfirstlane(t.k1),
-            __builtin_amdgcn_readfirstlane(t.tm)};
+            __builtin_amdgcn_readfirstlane(t.tm), __builtin_amdgcn_readfirstlane(t.turn)};
 }
 
 constexpr uint32_t NOWHERE = 0x80000000u;   // a lane offset past every buffer range: the load gives zeros
@@ -476,11 +486,9 @@ struct Operand {
         const uint32_t v = idx[u] < left ? voff[u] : NOWHERE;
         lds_dma16<0, true>(rsrc, stage + (wave * PIECES + u) * 1024, v, 0u);
     }
-    // K tile t of nt, at `at`: its buffer (empty past the last), and the next one's place
-    __device__ __forceinline__ i32x4 rsrc(uint64_t& at, int t, int nt) const {
-        const i32x4 r = rsrc_words(t == nt - 1 ? at - (uint64_t)back_b : at, t < nt ? 0x7fffffffu : 0u);
-        at += (uint64_t)step;
-        return r;
+    // the buffer of K tile t, which begins at `at` (one that is not there is empty)
+    __device__ __forceinline__ i32x4 rsrc(uint64_t at, bool last, bool there) const {
+        return rsrc_words(last ? at - (uint64_t)back_b : at, there ? 0x7fffffffu : 0u);
     }
     // what it holds along the summed axis (and more)
     __device__ __forceinline__ int left(int t) const { return have - t * (KS ? KROWS : 64); }
@@ -523,12 +531,13 @@ struct Product {
     static constexpr int NM = TM * 4, GROUPS = TM + 3;  // MFMAs of a step; operand reads: A0 and B0, B1, B2, B3, A1 ..
     OpA A;
     OpB B;
-    int keys, nt, back;
+    int keys, nt, back, from;
 
     __device__ __forceinline__ void init(const GroupedArgs& g, const Tile& t, int wave, int lane) {
         keys = t.k1 - t.k0;
         nt = (keys + OpA::KROWS - 1) / OpA::KROWS;
         back = MODE != GROUPED_TN && keys * ES % 16 ? nt * OpA::KROWS - keys : 0;
+        from = MODE == GROUPED_NT && !back ? t.n0 / BN * t.turn % nt : 0;
         A.init(g.A, g.lda_b, t.m0, t.m_end, t.k0, keys, back, wave, lane, wave >> 1);
         B.init(MODE == GROUPED_TN ? g.B : g.B + t.group * g.group_b, g.ldb_b, t.n0, g.N, t.k0, keys, back, wave, lane,
                wave & 1);
@@ -536,15 +545,27 @@ struct Product {
 
     // The product into acc; LDS is free when every wave has returned.
     __device__ __forceinline__ void run(MPDT_LDS char* lds, int wave, int lane, Acc (&acc)[TM][4]) const {
-        uint64_t at_a = A.base, at_b = B.base;
+        // the tile that is loaded next, from `from` on and round
+        int pos = from;
+        uint64_t at_a = A.base + (uint64_t)(from * A.step), at_b = B.base + (uint64_t)(from * B.step);
+        auto step = [&] {
+            at_a += (uint64_t)A.step;
+            at_b += (uint64_t)B.step;
+            if (++pos == nt && MODE == GROUPED_NT) {
+                pos = 0;
+                at_a = A.base;
+                at_b = B.base;
+            }
+        };
         i32x4 rb{};     // B's buffer of the tile whose loads are due next
         int left_b = 0;
 #pragma unroll
         for (int p = 0; p < NS; ++p) {
-            const i32x4 ra = A.rsrc(at_a, p, nt);
-            const int left_a = A.left(p);
-            rb = B.rsrc(at_b, p, nt);
-            left_b = B.left(p);
+            const i32x4 ra = A.rsrc(at_a, pos == nt - 1, p < nt);
+            const int left_a = A.left(pos);
+            rb = B.rsrc(at_b, pos == nt - 1, p < nt);
+            left_b = B.left(pos);
+            step();
             static_for<0, OpA::PIECES>([&](auto U) { A.load(decltype(U)::value, ra, lds + p * STAGE, wave, left_a); });
             if (p < NS - 1)
                 static_for<0, 4>([&](auto U) { B.load(decltype(U)::value, rb, lds + p * STAGE + OpA::BYTES, wave, left_b); });
@@ -575,12 +596,13 @@ struct Product {
                 mma(0, i);
                 if constexpr (i < GROUPS) read_group(1, i, sc);
                 if constexpr (i == NM / 2) {
-                    ra = A.rsrc(at_a, k + NS, nt);
-                    left_a = A.left(k + NS);
+                    ra = A.rsrc(at_a, pos == nt - 1, k + NS < nt);
+                    left_a = A.left(pos);
                 }
                 if constexpr (i == NM / 2 + 1) {
-                    rb2 = B.rsrc(at_b, k + NS, nt);
-                    left_b2 = B.left(k + NS);
+                    rb2 = B.rsrc(at_b, pos == nt - 1, k + NS < nt);
+                    left_b2 = B.left(pos);
+                    step();
                 }
                 // B's four loads on the last slots, every second one where there are 16
                 constexpr int STEP = TM == 4 ? 2 : 1, FIRST = NM - 1 - 3 * STEP;
@@ -772,6 +794,23 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     else tile_run<T, MODE, 1, LDS>(g, t, lds, wave, lane);
 }
 
+// 64 x 256 tiles of A . B, two workgroups to a CU: groups of few rows, whose matrices have
+// to be read.  Neighbouring tiles go to different XCDs, so that the card reads whole rows of
+// a matrix at a time (8 groups of 4096 x 14336 over 128 rows: 163 us, 5.8 TB/s; 198 with a
+// run of tiles to an XCD).
+template <GroupedType T>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void grouped_low_kernel(GroupedArgs g) {
+    constexpr int LDS = 81920;
+    __shared__ __attribute__((aligned(1024))) char lds_[LDS];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tiles_n = (g.N + BN - 1) / BN;
+    const RowTile r = row_tile<64>(g, blockIdx.x / tiles_n, lane);
+    if (r.group < 0) return;    // (the whole workgroup)
+    const int local = r.tile * tiles_n + blockIdx.x % tiles_n;
+    const Tile t{r.group, r.lo + local % r.tiles * 64, r.hi, local / r.tiles * BN, 0, g.K, 1, 0};
+    tile_run<T, GROUPED_NN, 1, LDS>(g, scalar(t), lds_cast(lds_), wave, lane);
+}
+
 // The weights' gradient: 128 x 256 tiles, two workgroups to a CU.  A group's rows make a
 // short sum, so that a tile's beginning and its store take as long as its product (384
 // rows: 2 + 3 us and 10); another workgroup's product goes on meanwhile.
@@ -782,6 +821,234 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Tile t = scalar(tile_at<GROUPED_TN, 128>(g, lane));
     tile_run<T, GROUPED_TN, 2, LDS>(g, t, lds_cast(lds_), wave, lane);
+}
+
+// ---- few rows --------------------------------------------------------------------------
+
+// One operand of a strip: R rows (KC) of KT bytes along the summed axis, or R columns of
+// KROWS rows (KS), all loaded by one wave, 1 KiB an instruction.  The swizzles as above;
+// KS rows of 64 columns have 8 pieces, which take turns by pairs over four rows.
+template <bool KS, int R, int KT, int ES>
+struct Strip {
+    static constexpr int KROWS = KT / ES;
+    static constexpr int ROW = KS ? R * ES : KT, LANES = ROW / 16;
+    static constexpr int BYTES = R * KT, PIECES = BYTES / 1024;
+    static_assert(!KS || ES == 2, "16-bit rows across the summed axis");
+    uint32_t voff[PIECES];
+    int idx[PIECES];
+    uint64_t base;
+    int64_t step, back_b;
+    int have;
+    uint32_t read0;
+
+    __device__ __forceinline__ static uint32_t swizzle(uint32_t row) {
+        if constexpr (!KS) return swz_a<LANES>(row);
+        else if constexpr (LANES == 16) return swz_b<2>(row);
+        else return (row & 3u) << 1;
+    }
+    __device__ __forceinline__ void init(const char* p, int64_t ld, int r0, int end, int keys, int back, int lane) {
+        base = (uint64_t)(uintptr_t)p + (uint64_t)(KS ? (int64_t)r0 * ES : (int64_t)r0 * ld);
+        step = KS ? (int64_t)KROWS * ld : KT;
+        back_b = back * (KS ? ld : ES);
+        have = (keys + back) * (KS ? 1 : ES);
+#pragma unroll
+        for (int u = 0; u < PIECES; ++u) {
+            const int row = u * (64 / LANES) + lane / LANES;
+            const uint32_t c = (uint32_t)(lane % LANES) ^ swizzle(row);
+            idx[u] = KS ? row : (int)c * 16;
+            voff[u] = r0 + (KS ? (int)c * 8 : row) < end ? (uint32_t)row * (uint32_t)ld + c * 16u : NOWHERE;
+        }
+        const uint32_t lrow = lane & 31, lhalf = lane >> 5, grp = lane >> 4, gp = lane & 15;
+        if constexpr (KS) {
+            const uint32_t k = 8 * (grp >> 1) + (gp >> 2), c = 2 * (grp & 1) + ((gp & 3) >> 1);
+            read0 = k * ROW + ((c ^ swizzle(k)) << 4) + 8 * (gp & 1);
+        } else {
+            read0 = lrow * ROW + ((lhalf ^ swizzle(lrow)) << 4);
+        }
+    }
+    // all of K tile t of nt
+    __device__ __forceinline__ void load(int t, int nt, MPDT_LDS char* to) const {
+        const uint64_t at = base + (uint64_t)((int64_t)t * step - (t == nt - 1 ? back_b : 0));
+        const i32x4 r = rsrc_words(at, t < nt ? 0x7fffffffu : 0u);
+        const int left = have - t * (KS ? KROWS : KT);
+#pragma unroll
+        for (int u = 0; u < PIECES; ++u) lds_dma16<0, true>(r, to + u * 1024, idx[u] < left ? voff[u] : NOWHERE, 0u);
+    }
+    // the MFMA operand of step s and 32-row (column) tile i
+    __device__ __forceinline__ u32x4 read(const MPDT_LDS char* from, int s, int i) const {
+        if constexpr (KS) {
+            const uint32_t o = (read0 ^ (uint32_t)(i * 64)) + s * 16 * ROW;
+            const u32x2 x = lds_read_tr16(from, o), y = lds_read_tr16(from, o + 4 * ROW);
+            return u32x4{x[0], x[1], y[0], y[1]};
+        } else {
+            return lds_load16(from, (read0 ^ (uint32_t)(s * 32)) + i * 32 * ROW);
+        }
+    }
+};
+
+// Few tiles: bound by the reading of the matrices and by how long a workgroup takes for
+// its own.  A workgroup takes 32 * MT rows and a strip of 64 columns; its four waves take
+// every fourth K tile each, through rings of direct loads of their own that no barrier
+// holds up, and their sums are joined in LDS at the end.  8 rows of 8 groups of 2048 x 1408:
+// 10.4 us, 24.7 by the tiles above (strips of 128 columns 12.9, rings of twice the depth in
+// one workgroup to a CU 12.0).
+template <GroupedType T, int MODE, int MT>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) void grouped_few_kernel(GroupedArgs g) {
+    constexpr int SN = 64;
+    using F = Fmt<KindOf<T>::kind>;
+    using Acc = typename F::Acc;
+    using Sum = typename std::conditional<T == GroupedType::I8, i32x4, f32x4>::type;
+    constexpr int ES = F::ES, KT = MODE == GROUPED_NT ? 128 : 64, NJ = SN / 32;
+    using OpA = Strip<false, 32 * MT, KT, ES>;
+    using OpB = Strip<MODE == GROUPED_NN, SN, KT, ES>;
+    constexpr int STAGE = OpA::BYTES + OpB::BYTES, LOADS = OpA::PIECES + OpB::PIECES;
+    constexpr int PART = 32 * MT * SN * 4;      // a wave's sums
+    // (two workgroups to a CU, where rings of two stages and the sums fit its half)
+    constexpr int HALF = 163840 / 2 / 4, MOST = 2 * STAGE <= HALF && PART <= HALF ? HALF : 2 * HALF;
+    constexpr int NS = MOST / STAGE < 6 ? MOST / STAGE : 6;
+    static_assert(NS >= 2 && PART <= NS * STAGE && (NS - 1) * LOADS < 64, "rings and sums fit");
+    __shared__ __attribute__((aligned(1024))) char lds_[4 * NS * STAGE];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int strips = (g.N + SN - 1) / SN;
+    const RowTile rt = row_tile<32 * MT>(g, blockIdx.x / strips, lane);
+    if (rt.group < 0) return;   // (the whole workgroup)
+    // a group's row tiles of one strip beside each other: they read the same columns
+    const int local = rt.tile * strips + blockIdx.x % strips;
+    const int group = __builtin_amdgcn_readfirstlane(rt.group);
+    const int m0 = __builtin_amdgcn_readfirstlane(rt.lo + local % rt.tiles * (32 * MT));
+    const int m_end = __builtin_amdgcn_readfirstlane(rt.hi);
+    const int n_own = __builtin_amdgcn_readfirstlane(local / rt.tiles * SN);
+    const int n0 = MODE == GROUPED_NN && g.N % 8 ? min(n_own, g.N - SN) : n_own;
+
+    const int nt = (g.K + OpA::KROWS - 1) / OpA::KROWS;
+    const int back = (int64_t)g.K * ES % 16 ? nt * OpA::KROWS - g.K : 0;
+    OpA A;
+    OpB B;
+    A.init(g.A, g.lda_b, m0, m_end, g.K, back, lane);
+    B.init(g.B + group * g.group_b, g.ldb_b, n0, g.N, g.K, back, lane);
+    Acc acc[MT][NJ];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+    MPDT_LDS char* const ring = lds_cast(lds_) + wave * NS * STAGE;
+    // (in turns along k, as above)
+    const int from = MODE == GROUPED_NT && !back ? n0 / SN * (TURN_BYTES / KT) % nt : 0;
+    auto load = [&](int t, int slot) {
+        const int at = t >= nt ? t : t + from >= nt ? t + from - nt : t + from;
+        A.load(at, nt, ring + slot * STAGE);
+        B.load(at, nt, ring + slot * STAGE + OpA::BYTES);
+    };
+#pragma unroll
+    for (int p = 0; p < NS - 1; ++p) load(wave + 4 * p, p);
+    int slot = 0;
+    for (int t = wave; t < nt; t += 4) {
+        // (the slot that is filled now was read in the last round)
+        load(t + 4 * (NS - 1), slot == 0 ? NS - 1 : slot - 1);
+        wait_vmem<(NS - 1) * LOADS>();
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("" ::: "memory");
+        const MPDT_LDS char* const at = ring + slot * STAGE;
+        u32x4 a[KT / 32][MT], b[KT / 32][NJ];
+#pragma unroll
+        for (int s = 0; s < KT / 32; ++s) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i) a[s][i] = A.read(at, s, i);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) b[s][j] = B.read(at + OpA::BYTES, s, j);
+        }
+        if (back && t == nt - 1) {
+            // what the last tile repeats
+#pragma unroll
+            for (int s = 0; s < KT / 32; ++s) {
+                const int n = min(max(back * ES - s * 32 - (lane >> 5) * 16, 0), 16);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) a[s][i] = mask_head(a[s][i], n);
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) b[s][j] = mask_head(b[s][j], n);
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < KT / 32; ++s)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) acc[i][j] = F::mma(b[s][j], a[s][i], acc[i][j]);
+        wait_lds();
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("" ::: "memory");
+        slot = slot + 1 == NS ? 0 : slot + 1;
+    }
+    // join the waves' sums: value (row, column) of wave w at w * PART + (row * SN + column)
+    // * 4, pieces of a row turned by the row
+    wait_vmem<0>();
+    wg_barrier();
+    const int lrow = lane & 31, lhalf = lane >> 5;
+    constexpr int CHUNKS = SN / 4;
+    MPDT_LDS char* const sums = lds_cast(lds_);
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int row = i * 32 + lrow, c = j * 8 + 2 * q + lhalf;
+                *(MPDT_LDS Sum*)(sums + wave * PART + row * SN * 4 + ((c ^ (row & 15)) << 4)) =
+                    Sum{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+            }
+    wait_lds();
+    wg_barrier();
+    typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+    typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+    for (int n = threadIdx.x; n < 32 * MT * CHUNKS; n += 256) {
+        const int r = n / CHUNKS, c = n % CHUNKS, row = m0 + r, col = n0 + 4 * c;
+        if (row >= m_end || col >= g.N || col + 4 <= n_own) continue;
+        Sum v = *(MPDT_LDS Sum*)(sums + r * SN * 4 + ((c ^ (r & 15)) << 4));
+#pragma unroll
+        for (int w = 1; w < 4; ++w) v += *(MPDT_LDS Sum*)(sums + w * PART + r * SN * 4 + ((c ^ (r & 15)) << 4));
+        float f[4];
+        if constexpr (T == GroupedType::I8) {
+            const float xs = g.x_scale[row];
+            const f32x4 ws = four_of(g.w_scale + group * g.ld_ws, col, g.N);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = mul_rn(mul_rn((float)v[e], xs), ws[e]);
+            if (g.bias) {
+                const f32x4 bias = four_of(g.bias + group * g.ld_bias, col, g.N);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[e] = add_rn(f[e], bias[e]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = v[e];
+        }
+        const int64_t at = (int64_t)row * g.ldd + col;
+        const bool all = col >= n_own && col + 4 <= g.N;
+        if (T == GroupedType::I8 || g.out16) {
+            uint16_t* const to = reinterpret_cast<uint16_t*>(g.D) + at;
+            uint32_t h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = T == GroupedType::F16 ? f32_to_f16_bits(f[e]) : f32_to_bf16_bits(f[e]);
+            if (all) {
+                *reinterpret_cast<u32x2_any*>(to) = u32x2_any{h[0] | h[1] << 16, h[2] | h[3] << 16};
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (col + e >= n_own && col + e < g.N) to[e] = (uint16_t)h[e];
+            }
+        } else {
+            float* const to = reinterpret_cast<float*>(g.D) + at;
+            if (all) {
+                *reinterpret_cast<u32x4_any*>(to) =
+                    u32x4_any{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (col + e >= n_own && col + e < g.N) to[e] = f[e];
+            }
+        }
+    }
 }
 
 // The most row tiles of BM rows that the groups can have.
@@ -811,12 +1078,45 @@ bool by_tiles(const GroupedArgs& a) {
     return MODE != GROUPED_TN || a.M % 8 == 0 || a.M >= 128;
 }
 
+// Whether the strips can: as above, with their own widths.
+template <GroupedType T, int MODE>
+bool by_strips(const GroupedArgs& a) {
+    constexpr int ES = T == GroupedType::I8 ? 1 : 2, KT = MODE == GROUPED_NT ? 128 : 64;
+    if (a.lda_b >= (1 << 23) || a.ldb_b >= (1 << 23) || a.K == 0) return false;
+    if (a.K * (int64_t)ES % 16 && a.K < KT / ES) return false;
+    return MODE != GROUPED_NN || a.N % 8 == 0 || a.N >= 64;
+}
+
+template <GroupedType T, int MODE, int MT>
+hipError_t launch_few(const GroupedArgs& a, hipStream_t stream) {
+    const int64_t groups = (a.N + 63) / 64 * most_row_tiles(a, 32 * MT);
+    grouped_few_kernel<T, MODE, MT><<<dim3((unsigned)groups), dim3(256), 0, stream>>>(a);
+    return hipGetLastError();
+}
+
 template <GroupedType T, int MODE>
 hipError_t launch_mode(const GroupedArgs& a, hipStream_t stream) {
-    if (!by_tiles<T, MODE>(a)) return launch_any<T, MODE>(a, stream);
-    if constexpr (MODE == GROUPED_TN)
+    if constexpr (MODE == GROUPED_TN) {
+        if (!by_tiles<T, MODE>(a)) return launch_any<T, MODE>(a, stream);
         grouped_grad_kernel<T><<<dim3((unsigned)grouped_tiles(MODE, a, 128, BN)), dim3(256), 0, stream>>>(a);
-    else grouped_tile_kernel<T, MODE><<<dim3((unsigned)tile_workgroups(a)), dim3(256), 0, stream>>>(a);
+    } else {
+        // Too few tiles of 64 rows for half of the CUs: strips (512 rows of 4 groups of 2048 x
+        // 2048, 96 tiles: 16 us, 31 by tiles; 1024 rows, 160 tiles: 26 either way), two blocks
+        // of 32 rows where one would often not do.
+        const int64_t low = most_row_tiles(a, 64) * ((a.N + BN - 1) / BN);
+        if (low <= CUS / 2 && by_strips<T, MODE>(a))
+            return a.rows > 20 * (int64_t)a.groups ? launch_few<T, MODE, 2>(a, stream) : launch_few<T, MODE, 1>(a, stream);
+        if (!by_tiles<T, MODE>(a)) return launch_any<T, MODE>(a, stream);
+        if constexpr (MODE == GROUPED_NN) {
+            // Few rows to a group (128 rows of 16 groups of 4096 x 4096: 86 us, 91 by the larger
+            // tiles; 1536 rows: 161 and 101)
+            if (a.rows <= 48 * (int64_t)a.groups) {
+                grouped_low_kernel<T><<<dim3((unsigned)low), dim3(256), 0, stream>>>(a);
+                return hipGetLastError();
+            }
+        }
+        grouped_tile_kernel<T, MODE><<<dim3((unsigned)tile_workgroups(a)), dim3(256), 0, stream>>>(a);
+    }
     return hipGetLastError();
 }
 

@@ -62,6 +62,11 @@ SIZES = [
     ([130, 70], 77, 301),
     ([260, 1], 33, 259),
     ([129, 255, 64], 47, 1025),
+    ([700, 0, 900, 513, 129, 65, 1, 800], 200, 1032),
+    ([700, 0, 900, 513, 129, 65, 1, 800], 1003, 1501),
+    ([2000, 2200], 33, 1025),
+    ([1500, 1600, 90, 64], 72, 1288),
+    ([4000, 17, 250], 520, 2056),
     ([70000], 16, 264),                 # more whole tiles than two rounds of the card
     ([300, 20000, 90, 40000, 5, 70, 8000], 24, 300),
     ([257, 0, 100] * 40, 8, 16),        # whole and part tiles past the 64th group
