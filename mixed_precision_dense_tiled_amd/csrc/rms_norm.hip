@@ -15,6 +15,7 @@
 
 #include "device_common.hpp"
 #include "layers.hpp"
+#include "quotient.hpp"
 
 namespace mpdt {
 namespace {
@@ -206,12 +207,14 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(NormArgs 
 #pragma unroll
             for (int e = 1; e < 8; ++e) amax[u] = larger(amax[u], fabsf(y[u][e]));
         }
+        float inverse = 1.0f;
         if constexpr (QUANT != NORM_E4M3_BLOCKS) {
             float m = amax[0];
 #pragma unroll
             for (int u = 1; u < PIECES; ++u) m = larger(m, amax[u]);
             scale = scale_of(over_row<NT>(m, red_f, [](float p, float q) { return larger(p, q); }), QMAX);
             if (tid == 0) a.scales[row * a.ld_scales] = scale;
+            inverse = 1.0f / scale;
         }
 #pragma unroll
         for (int u = 0; u < PIECES; ++u) {
@@ -221,13 +224,23 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(NormArgs 
                 // 16 lanes hold a block of 128
                 scale = scale_of(over_lanes(amax[u], 8, [](float p, float q) { return larger(p, q); }), QMAX);
                 if ((tid & 15) == 0 && n > 0) a.scales[row * a.ld_scales + e0 / 128] = scale;
+                inverse = 1.0f / scale;
+            }
+            // (|y| is at most qmax scales where the scale is a usual one)
+            float ys[8];
+            if (divides(scale)) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ys[e] = quotient(y[u][e], scale, inverse);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ys[e] = y[u][e] / scale;
             }
             uint32_t code[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 float q[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) q[j] = cut(y[u][4 * i + j] / scale, QMAX);
+                for (int j = 0; j < 4; ++j) q[j] = cut(ys[4 * i + j], QMAX);
                 if constexpr (QUANT == NORM_I8_ROWS) {
                     code[i] = 0;
 #pragma unroll
@@ -299,9 +312,9 @@ __global__ __launch_bounds__(NT) void rms_norm_grad_kernel(NormGradArgs a) {
     for (int u = 0; u < PIECES; ++u)
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[u][e] = 0;
-    int turn = 0;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
-        Piece<T> g[PIECES], h[PIECES], r[PIECES];
+    // (the next row's loads are under way while this one is reduced)
+    Piece<T> g[PIECES], h[PIECES], r[PIECES];
+    auto load = [&](int64_t row) {
 #pragma unroll
         for (int u = 0; u < PIECES; ++u) {
             const int e0 = 8 * (tid + NT * u);
@@ -309,8 +322,12 @@ __global__ __launch_bounds__(NT) void rms_norm_grad_kernel(NormGradArgs a) {
             h[u].load(a.h + row * a.h_b + (int64_t)e0 * ES, a.dim - e0);
             if (a.grad_res) r[u].load(a.grad_res + row * a.gres_b + (int64_t)e0 * ES, a.dim - e0);
         }
+    };
+    int turn = 0;
+    load(blockIdx.x);
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
         const float rstd = a.rstd[row];
-        float c = 0;
+        float c = 0, d[PIECES][8], x[PIECES][8];
 #pragma unroll
         for (int u = 0; u < PIECES; ++u) {
             const int e0 = 8 * (tid + NT * u);
@@ -318,25 +335,29 @@ __global__ __launch_bounds__(NT) void rms_norm_grad_kernel(NormGradArgs a) {
             load_weight<T>(a.weight, a.w_f32, e0, a.dim - e0, w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float v = g[u].get(e), x = h[u].get(e);
-                c += v * w[e] * x;
-                dw[u][e] += v * (x * rstd);
+                const float v = g[u].get(e);
+                x[u][e] = h[u].get(e);
+                d[u][e] = v * w[e];
+                c += d[u][e] * x[u][e];
+                dw[u][e] += v * (x[u][e] * rstd);
             }
         }
+        Piece<T> res[PIECES];
+#pragma unroll
+        for (int u = 0; u < PIECES; ++u) res[u] = r[u];
+        if (row + gridDim.x < a.rows) load(row + gridDim.x);
         // (two sets of partial sums in turn: one barrier a row)
         c = over_row<NT>(c, red[turn], [](float p, float q) { return p + q; });
         c = rstd * rstd * (c / a.dim);
 #pragma unroll
         for (int u = 0; u < PIECES; ++u) {
             const int e0 = 8 * (tid + NT * u);
-            float w[8];
-            load_weight<T>(a.weight, a.w_f32, e0, a.dim - e0, w);
             Piece<T> o;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                float d = rstd * (g[u].get(e) * w[e] - h[u].get(e) * c);
-                if (a.grad_res) d += r[u].get(e);
-                o.put(e, d);
+                float y = rstd * (d[u][e] - x[u][e] * c);
+                if (a.grad_res) y += res[u].get(e);
+                o.put(e, y);
             }
             o.store(a.grad_h + row * a.gh_b + (int64_t)e0 * ES, a.dim - e0);
         }
@@ -351,17 +372,31 @@ __global__ __launch_bounds__(NT) void rms_norm_grad_kernel(NormGradArgs a) {
     }
 }
 
-// Columns' sums of the workgroups: 64 columns to a workgroup, its four waves a
-// quarter of the rows each, joined in order.
+// Columns' sums of the workgroups: 64 columns to a workgroup, 16 threads of four columns
+// beside each other and a sixteenth of the rows to each such line, joined in order.
 __global__ __launch_bounds__(256) void rms_norm_grad_sum_kernel(const float* ws, int groups, int dim, float* out) {
-    __shared__ float part[4][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = blockIdx.x * 64 + lane;
-    float s = 0;
-    if (col < dim)
-        for (int i = groups * wave / 4; i < groups * (wave + 1) / 4; ++i) s += ws[(int64_t)i * dim + col];
-    part[wave][lane] = s;
+    __shared__ f32x4 part[16][16];
+    const int x = threadIdx.x & 15, y = threadIdx.x >> 4, col = blockIdx.x * 64 + 4 * x;
+    const int lo = groups * y / 16, hi = groups * (y + 1) / 16;
+    f32x4 s{0, 0, 0, 0};
+    if (col + 4 <= dim) {
+        typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+#pragma unroll 8
+        for (int i = lo; i < hi; ++i) s += *reinterpret_cast<const f32x4_any*>(ws + (int64_t)i * dim + col);
+    } else {
+        for (int i = lo; i < hi; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (col + e < dim) s[e] += ws[(int64_t)i * dim + col + e];
+    }
+    part[y][x] = s;
     __syncthreads();
-    if (wave == 0 && col < dim) out[col] = ((part[0][lane] + part[1][lane]) + part[2][lane]) + part[3][lane];
+    if (threadIdx.x < 64 && blockIdx.x * 64 + threadIdx.x < (unsigned)dim) {
+        float v = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v += part[i][threadIdx.x >> 2][threadIdx.x & 3];
+        out[blockIdx.x * 64 + threadIdx.x] = v;
+    }
 }
 
 template <int T>

@@ -14,6 +14,7 @@
 #include "device_common.hpp"
 #include "kv_places.hpp"
 #include "layers.hpp"
+#include "quotient.hpp"
 
 namespace mpdt {
 namespace {
@@ -76,18 +77,16 @@ __device__ __forceinline__ void find_tokens(const RopeArgs& r, int t0, Tokens<N>
     __syncthreads();
 }
 
-// 8 elements to E4M3: x / scale as the division gives it, from the scale's reciprocal: the
-// product's error comes back through one fused step, after which the quotient is rounded
-// correctly (Markstein's theorem) wherever nothing leaves the range of FP32.  What is past
-// the range of E4M3 keeps the product, and scales far from 1 take the division itself.
+// 8 elements to E4M3, as the division by the scale gives them.  (What is past the range of
+// E4M3 keeps the product with the reciprocal, which is past it too.)
 __device__ __forceinline__ u32x2 to_e4m3_8(const float (&x)[8], float scale) {
     float q[8];
-    if (scale >= 0x1p-60f && scale <= 0x1p60f) {
+    if (divides(scale)) {
         const float r = 1.0f / scale;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float p = x[i] * r;
-            q[i] = fabsf(p) <= 1000.0f ? fmaf(fmaf(-p, scale, x[i]), r, p) : p;
+            q[i] = fabsf(p) <= 1000.0f ? quotient(x[i], scale, r) : p;
         }
     } else {
 #pragma unroll
