@@ -32,7 +32,7 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
     if (threadIdx.x < 64) {
         const int lane = threadIdx.x;
         const Place p = place_of<APPEND_TOKENS>(a.kv, a.sv, t0, lane);
-        if (lane < APPEND_TOKENS) dst[lane] = p.off;
+        if (lane < APPEND_TOKENS) dst[lane] = slot_of(a.kv, a.sv, p);
     }
     __syncthreads();
     const int per_row = a.kv.dim / 8, per_tok = a.kv.kv_heads * per_row;

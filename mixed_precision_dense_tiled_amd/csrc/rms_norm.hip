@@ -30,11 +30,16 @@ template <int T> struct Piece {
     static constexpr int W = 2 * ES;
     uint32_t w[W];
 
-    __device__ __forceinline__ void load(const char* p, int n) {   // n elements of 8, the rest 0
+    // n elements of 8, the rest 0; PAST the caches, where nobody reads them again
+    template <bool PAST = false>
+    __device__ __forceinline__ void load(const char* p, int n) {
         if (n >= 8) {
 #pragma unroll
             for (int i = 0; i < W / 4; ++i) {
-                const u32x4_any v = *reinterpret_cast<const u32x4_any*>(p + 16 * i);
+                const u32x4_any* const from = reinterpret_cast<const u32x4_any*>(p + 16 * i);
+                u32x4_any v;
+                if constexpr (PAST) v = __builtin_nontemporal_load(from);
+                else v = *from;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) w[4 * i + j] = v[j];
             }
@@ -81,22 +86,6 @@ template <int T> struct Piece {
     }
 };
 
-// 8 weights as FP32.
-template <int T>
-__device__ __forceinline__ void load_weight(const char* p, int w_f32, int e0, int n, float (&w)[8]) {
-    if (T == DT_F32 || w_f32) {
-        Piece<DT_F32> v;
-        v.load(p + 4 * (int64_t)e0, n);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = v.get(e);
-    } else {
-        Piece<T> v;
-        v.load(p + 2 * (int64_t)e0, n);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = v.get(e);
-    }
-}
-
 // The larger of two magnitudes; NaN where either is.
 __device__ __forceinline__ float larger(float a, float b) { return a >= b ? a : (b == b ? (a == a ? b : a) : b); }
 
@@ -129,21 +118,55 @@ __device__ __forceinline__ float scale_of(float amax, float qmax) {
 }
 __device__ __forceinline__ float cut(float x, float most) { return x > most ? most : x < -most ? -most : x; }
 
-// NT threads to a row (64: four rows to a workgroup of 256).
-template <int T, int QUANT, int NT, int PIECES>
+// 8 values of y at a scale, as codes.
+template <int QUANT>
+__device__ __forceinline__ u32x2 codes_of(const float (&y)[8], float scale, float inverse) {
+    constexpr float QMAX = QUANT == NORM_I8_ROWS ? 127.0f : 448.0f;
+    float q[8];
+    // (|y| is at most qmax scales where the scale is a usual one)
+    if (divides(scale)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[e] = quotient(y[e], scale, inverse);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[e] = y[e] / scale;
+    }
+    u32x2 code;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if constexpr (QUANT == NORM_I8_ROWS) {
+            code[i] = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float x = cut(q[4 * i + j], QMAX);
+                const int c = x == x ? (int)__builtin_rintf(x) : 0;
+                code[i] |= (uint32_t)(c & 0xff) << (8 * j);
+            }
+        } else {
+            const float* const x = q + 4 * i;
+            const int p = __builtin_amdgcn_cvt_pk_fp8_f32(cut(x[0], QMAX), cut(x[1], QMAX), 0, false);
+            code[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(cut(x[2], QMAX), cut(x[3], QMAX), p, true);
+        }
+    }
+    return code;
+}
+
+// NT threads to a row (64: four rows to a workgroup of 256).  WT: the weight's type.
+template <int T, int WT, int QUANT, int NT, int PIECES>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(NormArgs a) {
     __shared__ double red_d[NT / 64];
     __shared__ float red_f[NT / 64];
-    constexpr int ROWS = NT < 256 ? 256 / NT : 1;
+    constexpr int ROWS = NT < 256 ? 256 / NT : 1, ES = Piece<T>::ES;
     const int tid = threadIdx.x % NT;
     const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / NT;
     if (row >= a.rows) return;   // (whole waves; rows that share a workgroup share no barrier)
     const char* x = a.x + row * a.x_b;
     Piece<T> h[PIECES];
+    Piece<WT> w[PIECES];
 #pragma unroll
     for (int u = 0; u < PIECES; ++u) {
         const int e0 = 8 * (tid + NT * u);
-        h[u].load(x + (int64_t)e0 * Piece<T>::ES, a.dim - e0);
+        h[u].template load<true>(x + (int64_t)e0 * ES, a.dim - e0);
     }
     if (a.residual) {
         const char* r = a.residual + row * a.res_b;
@@ -151,18 +174,25 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(NormArgs 
 #pragma unroll
         for (int u = 0; u < PIECES; ++u) {
             const int e0 = 8 * (tid + NT * u);
-            p[u].load(r + (int64_t)e0 * Piece<T>::ES, a.dim - e0);
+            p[u].template load<true>(r + (int64_t)e0 * ES, a.dim - e0);
         }
 #pragma unroll
-        for (int u = 0; u < PIECES; ++u)
+        for (int u = 0; u < PIECES; ++u) {
+            const int e0 = 8 * (tid + NT * u);
+            w[u].load(a.weight + (int64_t)e0 * Piece<WT>::ES, a.dim - e0);
+        }
+#pragma unroll
+        for (int u = 0; u < PIECES; ++u) {
+            const int e0 = 8 * (tid + NT * u);
 #pragma unroll
             for (int e = 0; e < 8; ++e) h[u].put(e, h[u].get(e) + p[u].get(e));
-        if (a.h) {
+            if (a.h) h[u].store(a.h + row * a.h_b + (int64_t)e0 * ES, a.dim - e0);
+        }
+    } else {
 #pragma unroll
-            for (int u = 0; u < PIECES; ++u) {
-                const int e0 = 8 * (tid + NT * u);
-                h[u].store(a.h + row * a.h_b + (int64_t)e0 * Piece<T>::ES, a.dim - e0);
-            }
+        for (int u = 0; u < PIECES; ++u) {
+            const int e0 = 8 * (tid + NT * u);
+            w[u].load(a.weight + (int64_t)e0 * Piece<WT>::ES, a.dim - e0);
         }
     }
     double sum = 0;
@@ -177,82 +207,51 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(NormArgs 
     const float rstd = (float)(1.0 / sqrt(sum / a.dim + a.eps));
     if (a.rstd && tid == 0) a.rstd[row] = rstd;
 
-    float y[PIECES][8];
+    // (y is worked out where it is used: kept, it would cost a third of the waves)
+    auto y_of = [&](int u, float (&y)[8]) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = mul_rn(mul_rn(h[u].get(e), rstd), w[u].get(e));
+    };
+    // (past the row's end a piece holds 0 * rstd: an amax of 0, or NaN where rstd is, as
+    // it is in the whole row then)
+    auto amax_of = [](const float (&y)[8]) {
+        float m = fabsf(y[0]);
+#pragma unroll
+        for (int e = 1; e < 8; ++e) m = larger(m, fabsf(y[e]));
+        return m;
+    };
+    char* out = a.out + row * a.out_b;
+    float scale = 1.0f, inverse = 1.0f, y[8];
+    constexpr float QMAX = QUANT == NORM_I8_ROWS ? 127.0f : 448.0f;
+    if constexpr (QUANT == NORM_I8_ROWS || QUANT == NORM_E4M3_ROWS) {
+        y_of(0, y);
+        float m = amax_of(y);
+#pragma unroll
+        for (int u = 1; u < PIECES; ++u) {
+            y_of(u, y);
+            m = larger(m, amax_of(y));
+        }
+        scale = scale_of(over_row<NT>(m, red_f, [](float p, float q) { return larger(p, q); }), QMAX);
+        inverse = 1.0f / scale;
+        if (tid == 0) a.scales[row * a.ld_scales] = scale;
+    }
 #pragma unroll
     for (int u = 0; u < PIECES; ++u) {
-        const int e0 = 8 * (tid + NT * u);
-        float w[8];
-        load_weight<T>(a.weight, a.w_f32, e0, a.dim - e0, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[u][e] = mul_rn(mul_rn(h[u].get(e), rstd), w[e]);
-    }
-    char* out = a.out + row * a.out_b;
-    if constexpr (QUANT == NORM_PLAIN) {
-#pragma unroll
-        for (int u = 0; u < PIECES; ++u) {
-            const int e0 = 8 * (tid + NT * u);
+        const int e0 = 8 * (tid + NT * u), n = a.dim - e0;
+        y_of(u, y);
+        if constexpr (QUANT == NORM_PLAIN) {
             Piece<T> o;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o.put(e, y[u][e]);
-            o.store(out + (int64_t)e0 * Piece<T>::ES, a.dim - e0);
-        }
-    } else {
-        constexpr float QMAX = QUANT == NORM_I8_ROWS ? 127.0f : 448.0f;
-        float amax[PIECES], scale = 1.0f;
-        // (past the row's end a piece holds 0 * rstd: an amax of 0, or NaN where rstd
-        // is, as it is in the whole row then)
-#pragma unroll
-        for (int u = 0; u < PIECES; ++u) {
-            amax[u] = fabsf(y[u][0]);
-#pragma unroll
-            for (int e = 1; e < 8; ++e) amax[u] = larger(amax[u], fabsf(y[u][e]));
-        }
-        float inverse = 1.0f;
-        if constexpr (QUANT != NORM_E4M3_BLOCKS) {
-            float m = amax[0];
-#pragma unroll
-            for (int u = 1; u < PIECES; ++u) m = larger(m, amax[u]);
-            scale = scale_of(over_row<NT>(m, red_f, [](float p, float q) { return larger(p, q); }), QMAX);
-            if (tid == 0) a.scales[row * a.ld_scales] = scale;
-            inverse = 1.0f / scale;
-        }
-#pragma unroll
-        for (int u = 0; u < PIECES; ++u) {
-            const int e0 = 8 * (tid + NT * u);
-            const int n = a.dim - e0;
+            for (int e = 0; e < 8; ++e) o.put(e, y[e]);
+            o.store(out + (int64_t)e0 * ES, n);
+        } else {
             if constexpr (QUANT == NORM_E4M3_BLOCKS) {
                 // 16 lanes hold a block of 128
-                scale = scale_of(over_lanes(amax[u], 8, [](float p, float q) { return larger(p, q); }), QMAX);
-                if ((tid & 15) == 0 && n > 0) a.scales[row * a.ld_scales + e0 / 128] = scale;
+                scale = scale_of(over_lanes(amax_of(y), 8, [](float p, float q) { return larger(p, q); }), QMAX);
                 inverse = 1.0f / scale;
+                if ((tid & 15) == 0 && n > 0) a.scales[row * a.ld_scales + e0 / 128] = scale;
             }
-            // (|y| is at most qmax scales where the scale is a usual one)
-            float ys[8];
-            if (divides(scale)) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) ys[e] = quotient(y[u][e], scale, inverse);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) ys[e] = y[u][e] / scale;
-            }
-            uint32_t code[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float q[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) q[j] = cut(ys[4 * i + j], QMAX);
-                if constexpr (QUANT == NORM_I8_ROWS) {
-                    code[i] = 0;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int c = q[j] == q[j] ? (int)__builtin_rintf(q[j]) : 0;
-                        code[i] |= (uint32_t)(c & 0xff) << (8 * j);
-                    }
-                } else {
-                    int p = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
-                    code[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], p, true);
-                }
-            }
+            const u32x2 code = codes_of<QUANT>(y, scale, inverse);
             if (n >= 8) {
                 *reinterpret_cast<u32x2_any*>(out + e0) = u32x2_any{code[0], code[1]};
             } else {
@@ -279,17 +278,17 @@ hipError_t by_width(int dim, F f) {
 #undef MPDT_W
 }
 
-template <int T>
+template <int T, int WT>
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
     return by_width(a.dim, [&](auto NT, auto P) {
         constexpr int nt = decltype(NT)::value, p = decltype(P)::value;
         constexpr int rows = nt < 256 ? 256 / nt : 1;
         const dim3 grid((unsigned)((a.rows + rows - 1) / rows)), block(nt < 256 ? 256 : nt);
         switch (a.quant) {
-            case NORM_PLAIN: rms_norm_kernel<T, NORM_PLAIN, nt, p><<<grid, block, 0, stream>>>(a); break;
-            case NORM_I8_ROWS: rms_norm_kernel<T, NORM_I8_ROWS, nt, p><<<grid, block, 0, stream>>>(a); break;
-            case NORM_E4M3_ROWS: rms_norm_kernel<T, NORM_E4M3_ROWS, nt, p><<<grid, block, 0, stream>>>(a); break;
-            default: rms_norm_kernel<T, NORM_E4M3_BLOCKS, nt, p><<<grid, block, 0, stream>>>(a); break;
+            case NORM_PLAIN: rms_norm_kernel<T, WT, NORM_PLAIN, nt, p><<<grid, block, 0, stream>>>(a); break;
+            case NORM_I8_ROWS: rms_norm_kernel<T, WT, NORM_I8_ROWS, nt, p><<<grid, block, 0, stream>>>(a); break;
+            case NORM_E4M3_ROWS: rms_norm_kernel<T, WT, NORM_E4M3_ROWS, nt, p><<<grid, block, 0, stream>>>(a); break;
+            default: rms_norm_kernel<T, WT, NORM_E4M3_BLOCKS, nt, p><<<grid, block, 0, stream>>>(a); break;
         }
         return hipGetLastError();
     });
@@ -302,7 +301,7 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
 constexpr int GRAD_GROUPS = 512;
 int grad_groups(int64_t rows) { return (int)(rows < GRAD_GROUPS ? rows : GRAD_GROUPS); }
 
-template <int T, int NT, int PIECES>
+template <int T, int WT, int NT, int PIECES>
 __global__ __launch_bounds__(NT) void rms_norm_grad_kernel(NormGradArgs a) {
     __shared__ float red[2][NT / 64];
     const int tid = threadIdx.x;
@@ -331,13 +330,13 @@ __global__ __launch_bounds__(NT) void rms_norm_grad_kernel(NormGradArgs a) {
 #pragma unroll
         for (int u = 0; u < PIECES; ++u) {
             const int e0 = 8 * (tid + NT * u);
-            float w[8];
-            load_weight<T>(a.weight, a.w_f32, e0, a.dim - e0, w);
+            Piece<WT> w;
+            w.load(a.weight + (int64_t)e0 * Piece<WT>::ES, a.dim - e0);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float v = g[u].get(e);
                 x[u][e] = h[u].get(e);
-                d[u][e] = v * w[e];
+                d[u][e] = v * w.get(e);
                 c += d[u][e] * x[u][e];
                 dw[u][e] += v * (x[u][e] * rstd);
             }
@@ -399,11 +398,11 @@ __global__ __launch_bounds__(256) void rms_norm_grad_sum_kernel(const float* ws,
     }
 }
 
-template <int T>
+template <int T, int WT>
 hipError_t launch_grad(const NormGradArgs& a, int groups, hipStream_t stream) {
     const auto go = [&](auto NT, auto P) {
         constexpr int nt = decltype(NT)::value, p = decltype(P)::value;
-        rms_norm_grad_kernel<T, nt, p><<<dim3(groups), dim3(nt), 0, stream>>>(a);
+        rms_norm_grad_kernel<T, WT, nt, p><<<dim3(groups), dim3(nt), 0, stream>>>(a);
         return hipGetLastError();
     };
     using std::integral_constant;
@@ -418,8 +417,10 @@ hipError_t launch_grad(const NormGradArgs& a, int groups, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t stream) {
-    return a.type == DT_F32 ? launch_norm<DT_F32>(a, stream)
-           : a.type == DT_BF16 ? launch_norm<DT_BF16>(a, stream) : launch_norm<DT_F16>(a, stream);
+    if (a.type == DT_F32) return launch_norm<DT_F32, DT_F32>(a, stream);
+    if (a.type == DT_BF16)
+        return a.w_f32 ? launch_norm<DT_BF16, DT_F32>(a, stream) : launch_norm<DT_BF16, DT_BF16>(a, stream);
+    return a.w_f32 ? launch_norm<DT_F16, DT_F32>(a, stream) : launch_norm<DT_F16, DT_F16>(a, stream);
 }
 
 int64_t rms_norm_backward_ws(int64_t rows, int64_t dim) {
@@ -430,9 +431,11 @@ int64_t rms_norm_backward_ws(int64_t rows, int64_t dim) {
 hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t stream) {
     const int groups = grad_groups(a.rows);
     if (groups > 0) {
-        const hipError_t e = a.type == DT_F32 ? launch_grad<DT_F32>(a, groups, stream)
-                             : a.type == DT_BF16 ? launch_grad<DT_BF16>(a, groups, stream)
-                                                 : launch_grad<DT_F16>(a, groups, stream);
+        const hipError_t e = a.type == DT_F32 ? launch_grad<DT_F32, DT_F32>(a, groups, stream)
+                             : a.type == DT_BF16 ? (a.w_f32 ? launch_grad<DT_BF16, DT_F32>(a, groups, stream)
+                                                            : launch_grad<DT_BF16, DT_BF16>(a, groups, stream))
+                                                 : (a.w_f32 ? launch_grad<DT_F16, DT_F32>(a, groups, stream)
+                                                            : launch_grad<DT_F16, DT_F16>(a, groups, stream));
         if (e != hipSuccess || groups == 1) return e;
     }
     // (no rows: sums of nothing)

@@ -59,21 +59,29 @@ struct Tokens {
 // (a workgroup of 256 threads)
 template <int N>
 __device__ __forceinline__ void find_tokens(const RopeArgs& r, int t0, Tokens<N>& to) {
+    Place p{};
     if (threadIdx.x < 64) {
         const int lane = threadIdx.x;
-        const Place p = place_of<N>(r.ap.kv, r.ap.sv, t0, lane);
+        p = place_of<N>(r.ap.kv, r.ap.sv, t0, lane);
         if (lane < N) {
-            to.dst[lane] = p.off;
             to.pos[lane] = p.pos;
             to.in[lane] = p.in;
         }
     }
-    __syncthreads();
-    // a quarter (half, ..) of the threads to a token
+    // half (a quarter, ..) of the threads to a token
     constexpr int PER = 256 / N;
-    const int k = threadIdx.x / PER;
-    if (to.in[k])
-        for (int j = threadIdx.x % PER; j < r.pairs; j += PER) to.turn[k][j] = cos_sin(to.pos[k], r.inv_freq[j]);
+    const int k = threadIdx.x / PER, j = threadIdx.x % PER;
+    const float f = j < r.pairs ? r.inv_freq[j] : 0.0f;
+    __syncthreads();
+    // (the page's number is on its way while the angles are worked out)
+    int64_t dst = -1;
+    if (threadIdx.x < N) dst = slot_of(r.ap.kv, r.ap.sv, p);
+    if (to.in[k]) {
+        if (j < r.pairs) to.turn[k][j] = cos_sin(to.pos[k], f);
+        if constexpr (PER < 64)
+            for (int i = j + PER; i < r.pairs; i += PER) to.turn[k][i] = cos_sin(to.pos[k], r.inv_freq[i]);
+    }
+    if (threadIdx.x < N) to.dst[threadIdx.x] = dst;
     __syncthreads();
 }
 
@@ -115,21 +123,36 @@ __global__ __launch_bounds__(256) void append_rope_kernel(RopeArgs r) {
     const int turned = NEAR ? per : r.pairs / 8;        // of q's and K's items
     constexpr int U = 4;
     u32x4 x[U][2];
-    // row i: token i / heads; first q's heads, then K's, then V's
+    // row i: all of q's, then K's, then V's (a wave then has rows of one kind); of each kind
+    // one token's heads after the other's
+    struct Row {
+        int kind, k, h;     // 0 q, 1 K, 2 V
+    };
+    auto row_at = [&](int i) {
+        Row w{0, 0, i};
+        int n = r.heads;
+        if (i >= N * r.heads) {
+            n = a.kv.kv_heads;
+            w.h -= N * r.heads;
+            w.kind = w.h >= N * n ? 2 : 1;
+            w.h -= (w.kind - 1) * N * n;
+        }
+        w.k = N == 1 ? 0 : w.h / n;
+        w.h -= w.k * n;
+        return w;
+    };
     auto load = [&](int i0) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int i = min(i0 + u * step, N * heads - 1);
-            const int k = N == 1 ? 0 : i / heads, hh = i - k * heads;
-            const int64_t t = min(t0 + k, a.sv.tokens - 1);     // (a row that is there)
-            const int hk = hh - r.heads, hv = hk - a.kv.kv_heads;
-            const char* p = hk < 0 ? r.q + t * r.q_tok_b + hh * r.q_head_b
-                            : hv < 0 ? a.k_new + t * a.k_tok_b + hk * a.k_head_b
-                                     : a.v_new + t * a.v_tok_b + hv * a.v_head_b;
-            const bool apart = !NEAR && hv < 0 && j < turned;
+            const Row w = row_at(min(i0 + u * step, N * heads - 1));
+            const int64_t t = min(t0 + w.k, a.sv.tokens - 1);   // (a row that is there)
+            const char* p = w.kind == 0 ? r.q + t * r.q_tok_b + w.h * r.q_head_b
+                            : w.kind == 1 ? a.k_new + t * a.k_tok_b + w.h * a.k_head_b
+                                          : a.v_new + t * a.v_tok_b + w.h * a.v_head_b;
+            const bool apart = !NEAR && w.kind < 2 && j < turned;
             const int c0 = apart ? j : 2 * j, c1 = apart ? j + turned : 2 * j + 1;
-            x[u][0] = *reinterpret_cast<const u32x4*>(p + 16 * c0);
-            x[u][1] = *reinterpret_cast<const u32x4*>(p + 16 * c1);
+            x[u][0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p + 16 * c0));
+            x[u][1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p + 16 * c1));
         }
     };
     if (rows) load(first);
@@ -140,14 +163,13 @@ __global__ __launch_bounds__(256) void append_rope_kernel(RopeArgs r) {
         for (int u = 0; u < U; ++u) {
             const int i = i0 + u * step;
             if (i >= rows) break;
-            const int k = N == 1 ? 0 : i / heads, hh = i - k * heads;
-            const int hk = hh - r.heads, hv = hk - a.kv.kv_heads;
+            const auto [kind, k, h] = row_at(i);
             const int64_t dst = tok.dst[k];
-            if (hk < 0 ? !tok.in[k] : dst < 0) continue;
-            const bool apart = !NEAR && hv < 0 && j < turned;
+            if (kind == 0 ? !tok.in[k] : dst < 0) continue;
+            const bool apart = !NEAR && kind < 2 && j < turned;
             const int c0 = apart ? j : 2 * j, c1 = apart ? j + turned : 2 * j + 1;
-            const bool turns = NEAR ? hv < 0 && 8 * j < r.pairs : apart;
-            const bool to8 = TO8 && hk >= 0;
+            const bool turns = NEAR ? kind < 2 && 8 * j < r.pairs : apart;
+            const bool to8 = TO8 && kind > 0;
             float y[2][8];
             if (turns || to8) {
 #pragma unroll
@@ -181,16 +203,15 @@ __global__ __launch_bounds__(256) void append_rope_kernel(RopeArgs r) {
                             x[u][c][w] = narrow(y[c][2 * w], BF16) | (uint32_t)narrow(y[c][2 * w + 1], BF16) << 16;
                 }
             }
-            if (hk < 0) {
-                char* to = r.q_out + (int64_t)(t0 + k) * r.qo_tok_b + hh * r.qo_head_b;
+            if (kind == 0) {
+                char* to = r.q_out + (int64_t)(t0 + k) * r.qo_tok_b + h * r.qo_head_b;
                 *reinterpret_cast<u32x4*>(to + 16 * c0) = x[u][0];
                 *reinterpret_cast<u32x4*>(to + 16 * c1) = x[u][1];
                 continue;
             }
-            const int h = hv < 0 ? hk : hv;
-            char* to = (hv < 0 ? a.kv.k : a.kv.v) + dst + h * a.kv.head_b;
+            char* to = (kind == 1 ? a.kv.k : a.kv.v) + dst + h * a.kv.head_b;
             if constexpr (TO8) {
-                const float scale = (hv < 0 ? a.kv.k_scale : a.kv.v_scale)[h];
+                const float scale = (kind == 1 ? a.kv.k_scale : a.kv.v_scale)[h];
                 *reinterpret_cast<u32x2*>(to + 8 * c0) = to_e4m3_8(y[0], scale);
                 *reinterpret_cast<u32x2*>(to + 8 * c1) = to_e4m3_8(y[1], scale);
             } else {

@@ -13,7 +13,6 @@ inputs that require a gradient, and gradients are calls of their own.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from collections import namedtuple
 
@@ -89,12 +88,22 @@ def _stack(t, dtype, name):
 
 
 def _on(ref, name, *ts):
-    """All on ref's GPU, which is the current device within this context."""
+    """All on ref's GPU."""
     _same_device(ref, *ts)
     if not ref.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    return contextlib.nullcontext() if ref.get_device() == torch.cuda.current_device() else \
-        torch.cuda.device(ref.device)
+
+
+def _call(ref, fn, *args):
+    """The native call on ref's device and torch's current stream there."""
+    native = getattr(_native or _lib(), fn)
+    if ref.get_device() == torch.cuda.current_device():
+        status = native(*args, _stream(ref))
+    else:
+        with torch.cuda.device(ref.device):
+            status = native(*args, _stream(ref))
+    if status:
+        _check(fn, status)
 
 
 def _norm_operands(x, weight, name):
@@ -134,41 +143,50 @@ def rms_norm(x, weight, eps=1e-6, residual=None, quant=None, return_rstd=False, 
         raise ValueError(f"quant must be one of None, 'int8', 'fp8_rows', 'fp8_blocks', got {quant!r}")
     if residual is None and residual_out is not None:
         raise ValueError("residual_out needs a residual")
-    out_type = x.dtype if quant is None else torch.int8 if quant == "int8" else torch.uint8
-    grid = (rows, -(-dim // 128)) if quant == "fp8_blocks" else (rows,)
-    if quant is None and scales_out is not None:
-        raise ValueError("scales_out belongs to an output of 8 bits")
-    for t, shape, name in ((residual, (rows, dim), "residual"), (out, (rows, dim), "out"),
-                           (residual_out, (rows, dim), "residual_out"), (scales_out, grid, "scales_out")):
-        _shape(t, shape, name)
-    where = _on(x, "x", ("weight", weight), ("residual", residual), ("out", out), ("scales_out", scales_out),
-                ("residual_out", residual_out))
     if dim == 0:
         raise ValueError("x must have at least one column")
-    px, ldx = _mat(x, x.dtype, "x")
+    dtype, device = x.dtype, x.device
+    out_type = dtype if quant is None else torch.int8 if quant == "int8" else torch.uint8
+    if quant is None and scales_out is not None:
+        raise ValueError("scales_out belongs to an output of 8 bits")
+    _shape(residual, (rows, dim), "residual")
+    _shape(out, (rows, dim), "out")
+    _shape(residual_out, (rows, dim), "residual_out")
+    blocks = quant == "fp8_blocks"
+    grid = (rows, -(-dim // 128)) if blocks else (rows,)
+    _shape(scales_out, grid, "scales_out")
+    _on(x, "x", ("weight", weight), ("residual", residual), ("out", out), ("scales_out", scales_out),
+        ("residual_out", residual_out))
+    px, ldx = _mat(x, dtype, "x")
     pr = ph = ps = pd = None
-    ldr = ldh = lds = dim
+    ldr = ldh = ldo = lds = dim
+    # (what is made here is as the call wants it)
     if residual is not None:
-        pr, ldr = _mat(residual, x.dtype, "residual")
+        pr, ldr = _mat(residual, dtype, "residual")
         if residual_out is None:
-            residual_out = torch.empty((rows, dim), dtype=x.dtype, device=x.device)
-        ph, ldh = _mat(residual_out, x.dtype, "residual_out")
+            residual_out = torch.empty((rows, dim), dtype=dtype, device=device)
+            ph = residual_out.data_ptr()
+        else:
+            ph, ldh = _mat(residual_out, dtype, "residual_out")
     if out is None:
-        out = torch.empty((rows, dim), dtype=out_type, device=x.device)
-    po, ldo = _mat(out, out_type, "out")
+        out = torch.empty((rows, dim), dtype=out_type, device=device)
+        po = out.data_ptr()
+    else:
+        po, ldo = _mat(out, out_type, "out")
     if quant is not None:
+        lds = grid[-1] if blocks else 1
         if scales_out is None:
-            scales_out = torch.empty(grid, dtype=torch.float32, device=x.device)
-        if quant == "fp8_blocks":
+            scales_out = torch.empty(grid, dtype=torch.float32, device=device)
+            ps = scales_out.data_ptr()
+        elif blocks:
             ps, lds = _mat(scales_out, torch.float32, "scales_out")
         else:
-            ps, lds = _floats(scales_out, rows, "scales_out"), 1
-    rstd = torch.empty(rows, dtype=torch.float32, device=x.device) if return_rstd else None
+            ps = _floats(scales_out, rows, "scales_out")
+    rstd = torch.empty(rows, dtype=torch.float32, device=device) if return_rstd else None
     if rstd is not None:
         pd = rstd.data_ptr()
-    with where:
-        _check("rms_norm", _lib().rms_norm(code, rows, dim, px, ldx, pr, ldr, w_code, weight.data_ptr(), eps,
-                                           _NORM_OUT[quant], po, ldo, ps, lds, ph, ldh, pd, _stream(x)))
+    _call(x, "rms_norm", code, rows, dim, px, ldx, pr, ldr, w_code, weight.data_ptr(), eps, _NORM_OUT[quant], po,
+          ldo, ps, lds, ph, ldh, pd)
     return RmsNorm(out, scales_out, residual_out, rstd)
 
 
@@ -183,7 +201,7 @@ def rms_norm_backward(grad, h, weight, rstd, grad_residual=None, out=None):
     rows, dim, code, w_code = _norm_operands(h, weight, "h")
     for t, name in ((grad, "grad"), (grad_residual, "grad_residual"), (out, "out")):
         _shape(t, (rows, dim), name)
-    where = _on(h, "h", ("grad", grad), ("weight", weight), ("rstd", rstd), ("grad_residual", grad_residual),
+    _on(h, "h", ("grad", grad), ("weight", weight), ("rstd", rstd), ("grad_residual", grad_residual),
                 ("out", out))
     if dim == 0:
         raise ValueError("h must have at least one column")
@@ -200,10 +218,8 @@ def rms_norm_backward(grad, h, weight, rstd, grad_residual=None, out=None):
     if size < 0:
         raise MpdtError("rms_norm_backward", 1, L.mpdt_last_error().decode())
     ws = torch.empty(size, dtype=torch.uint8, device=h.device) if size else None
-    with where:
-        _check("rms_norm_backward",
-               L.rms_norm_backward(code, rows, dim, pg, ldg, ph, ldh, w_code, weight.data_ptr(), pd, pr, ldr, po, ldo,
-                                   grad_weight.data_ptr(), None if ws is None else ws.data_ptr(), size, _stream(h)))
+    _call(h, "rms_norm_backward", code, rows, dim, pg, ldg, ph, ldh, w_code, weight.data_ptr(), pd, pr, ldr, po, ldo,
+          grad_weight.data_ptr(), None if ws is None else ws.data_ptr(), size)
     return out, grad_weight
 
 
@@ -242,19 +258,19 @@ def paged_kv_append_rope(q, k, v, k_cache, v_cache, table, cu_q, lens, inv_freq,
             raise ValueError("q must be [tokens, heads, dim] with at least one head")
         heads = q.shape[1]
         pq, qt, qh = _rows3(q, (tokens, heads, kv.dim), dtype, "q")
-    where = _on(k, "k", ("q", q), ("v", v), ("k_cache", k_cache), ("v_cache", v_cache), ("table", table),
+    _on(k, "k", ("q", q), ("v", v), ("k_cache", k_cache), ("v_cache", v_cache), ("table", table),
                 ("cu_q", cu_q), ("lens", lens), ("inv_freq", inv_freq), ("k_scale", k_scale), ("v_scale", v_scale),
                 ("out", out))
     if q is not None:
         if out is None:
             out = torch.empty((tokens, heads, kv.dim), dtype=dtype, device=q.device)
-        po, ot, oh = _rows3(out, (tokens, heads, kv.dim), dtype, "out")
+            po, ot, oh = out.data_ptr(), heads * kv.dim, kv.dim
+        else:
+            po, ot, oh = _rows3(out, (tokens, heads, kv.dim), dtype, "out")
     if tokens == 0:
         return out      # (an empty tensor has no address)
-    with where:
-        _check("paged_kv_append_rope",
-               _lib().paged_kv_append_rope(kv, sq, _DTYPE[dtype], pk, kt, kh, pv, vt, vh, pf, inv_freq.shape[0],
-                                           int(bool(interleaved)), heads, pq, qt, qh, po, ot, oh, _stream(k)))
+    _call(k, "paged_kv_append_rope", kv, sq, _DTYPE[dtype], pk, kt, kh, pv, vt, vh, pf, inv_freq.shape[0],
+          int(bool(interleaved)), heads, pq, qt, qh, po, ot, oh)
     return out
 
 
@@ -301,14 +317,14 @@ def gemm_grouped(A, B, offsets, trans_b=False, out=None, d16=False):
     _shape(out, (rows, N), "out")
     kind = _out_type(out, A.dtype, d16)
     pa, lda = _mat(A, A.dtype, "A")
-    where = _on(A, "A", ("B", B), ("offsets", offsets), ("out", out))
+    _on(A, "A", ("B", B), ("offsets", offsets), ("out", out))
     if out is None:
         out = torch.empty((rows, N), dtype=kind, device=A.device)
-    pd, ldd = _mat(out, kind, "out")
-    with where:
-        _check("gemm_grouped", _lib().gemm_grouped(code, groups, rows, N, K, pa, lda, pb, ldb, sb,
-                                                   int(bool(trans_b)), poff, pd, ldd, int(kind != torch.float32),
-                                                   _stream(A)))
+        pd, ldd = out.data_ptr(), max(N, 1)
+    else:
+        pd, ldd = _mat(out, kind, "out")
+    _call(A, "gemm_grouped", code, groups, rows, N, K, pa, lda, pb, ldb, sb, int(bool(trans_b)), poff, pd, ldd,
+          int(kind != torch.float32))
     return out
 
 
@@ -330,13 +346,12 @@ def gemm_grouped_wgrad(A, G, offsets, out=None, d16=False):
     kind = _out_type(out, A.dtype, d16)
     pa, lda = _mat(A, A.dtype, "A")
     pg, ldg = _mat(G, A.dtype, "G")
-    where = _on(A, "A", ("G", G), ("offsets", offsets), ("out", out))
+    _on(A, "A", ("G", G), ("offsets", offsets), ("out", out))
     if out is None:
         out = torch.empty((groups, K, N), dtype=kind, device=A.device)
     pd, ldd, sd = _stack(out, kind, "out")
-    with where:
-        _check("gemm_grouped_wgrad", _lib().gemm_grouped_wgrad(code, groups, rows, N, K, pa, lda, pg, ldg, poff, pd,
-                                                               ldd, sd, int(kind != torch.float32), _stream(A)))
+    _call(A, "gemm_grouped_wgrad", code, groups, rows, N, K, pa, lda, pg, ldg, poff, pd, ldd, sd,
+          int(kind != torch.float32))
     return out
 
 
@@ -359,12 +374,12 @@ def gemm_grouped_w8a8(X, x_scale, W, w_scale, offsets, bias=None, out=None):
     psx = _floats(x_scale, rows, "x_scale")
     psw, ldsw = _mat(w_scale, torch.float32, "w_scale")
     pb, ldb = (None, N) if bias is None else _mat(bias, torch.float32, "bias")
-    where = _on(X, "X", ("x_scale", x_scale), ("W", W), ("w_scale", w_scale), ("offsets", offsets), ("bias", bias),
+    _on(X, "X", ("x_scale", x_scale), ("W", W), ("w_scale", w_scale), ("offsets", offsets), ("bias", bias),
                 ("out", out))
     if out is None:
         out = torch.empty((rows, N), dtype=torch.bfloat16, device=X.device)
-    py, ldy = _mat(out, torch.bfloat16, "out")
-    with where:
-        _check("gemm_grouped_w8a8", _lib().gemm_grouped_w8a8(groups, rows, N, K, px, ldx, psx, pw, ldw, sw, psw,
-                                                             ldsw, pb, ldb, poff, py, ldy, _stream(X)))
+        py, ldy = out.data_ptr(), max(N, 1)
+    else:
+        py, ldy = _mat(out, torch.bfloat16, "out")
+    _call(X, "gemm_grouped_w8a8", groups, rows, N, K, px, ldx, psx, pw, ldw, sw, psw, ldsw, pb, ldb, poff, py, ldy)
     return out
