@@ -244,6 +244,29 @@ def test_matrices_past_4_gib():
         close(got[5 * j:5 * j + 5], x @ w, x.abs() @ w.abs(), f32, K)
 
 
+def test_rows_far_apart():
+    """Leading dimensions past what the direct loads' offsets hold."""
+    off = torch.tensor([0, 4, 9], dtype=torch.int32, device="cuda")
+    wide = torch.zeros((9, 1 << 23), dtype=bf16, device="cuda")     # 16 MiB a row
+    a, g = wide[:, 8:80], wide[:, 1 << 20:(1 << 20) + 136]
+    x, y = mats((9, 72), bf16, 1, True)[1], mats((9, 136), bf16, 2, True)[1]
+    a.copy_(x)
+    g.copy_(y)
+    b, bc = mats((2, 72, 136), bf16, 3, True)
+    got, grad = mp.gemm_grouped(a, b, off), mp.gemm_grouped_wgrad(a, g, off)
+    for i, (lo, hi) in enumerate(((0, 4), (4, 9))):
+        assert torch.equal(got[lo:hi].cpu(), x[lo:hi].float() @ bc[i].float())
+        assert torch.equal(grad[i].cpu(), x[lo:hi].float().T @ y[lo:hi].float())
+
+
+def test_one_matrix_for_all_groups():
+    """A stride of 0 between groups."""
+    off = torch.tensor([0, 100, 100, 190], dtype=torch.int32, device="cuda")
+    a, ac = mats((190, 128), f16, 1, True)
+    b, bc = mats((1, 128, 264), f16, 2, True)
+    assert torch.equal(mp.gemm_grouped(a, b.expand(3, -1, -1), off).cpu(), ac.float() @ bc[0].float())
+
+
 def test_gradients_against_differences():
     """Both gradients along a direction, from the forward product (linear in each side,
     so a difference of whole steps is exact but for roundings)."""
