@@ -899,8 +899,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
     using Acc = typename F::Acc;
     using Sum = typename std::conditional<T == GroupedType::I8, i32x4, f32x4>::type;
     constexpr int ES = F::ES, KT = MODE == GROUPED_NT ? 128 : 64, NJ = SN / 32;
-    using OpA = Strip<false, 32 * MT, KT, ES>;
-    using OpB = Strip<MODE == GROUPED_NN, SN, KT, ES>;
+    using OpA = Strip<MODE == GROUPED_TN, 32 * MT, KT, ES>;
+    using OpB = Strip<MODE != GROUPED_NT, SN, KT, ES>;
     constexpr int STAGE = OpA::BYTES + OpB::BYTES, LOADS = OpA::PIECES + OpB::PIECES;
     constexpr int PART = 32 * MT * SN * 4;      // a wave's sums
     // (two workgroups to a CU, where rings of two stages and the sums fit its half)
@@ -910,22 +910,44 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
     __shared__ __attribute__((aligned(1024))) char lds_[4 * NS * STAGE];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int strips = (g.N + SN - 1) / SN;
-    const RowTile rt = row_tile<32 * MT>(g, blockIdx.x / strips, lane);
-    if (rt.group < 0) return;   // (the whole workgroup)
-    // a group's row tiles of one strip beside each other: they read the same columns
-    const int local = rt.tile * strips + blockIdx.x % strips;
-    const int group = __builtin_amdgcn_readfirstlane(rt.group);
-    const int m0 = __builtin_amdgcn_readfirstlane(rt.lo + local % rt.tiles * (32 * MT));
-    const int m_end = __builtin_amdgcn_readfirstlane(rt.hi);
-    const int n_own = __builtin_amdgcn_readfirstlane(local / rt.tiles * SN);
-    const int n0 = MODE == GROUPED_NN && g.N % 8 ? min(n_own, g.N - SN) : n_own;
+    int group, m_own, m_end, n_own, k0, keys;
+    if constexpr (MODE == GROUPED_TN) {
+        const int tiles_m = (g.M + 32 * MT - 1) / (32 * MT), tile = blockIdx.x / strips;
+        group = tile / tiles_m;
+        m_own = (tile - group * tiles_m) * (32 * MT);
+        m_end = g.M;
+        n_own = blockIdx.x % strips * SN;
+        const Rows r = rows_of(g, group, lane);
+        k0 = r.lo;
+        keys = r.hi - r.lo;
+    } else {
+        const RowTile rt = row_tile<32 * MT>(g, blockIdx.x / strips, lane);
+        if (rt.group < 0) return;   // (the whole workgroup)
+        // a group's row tiles of one strip beside each other: they read the same columns
+        const int local = rt.tile * strips + blockIdx.x % strips;
+        group = rt.group;
+        m_own = rt.lo + local % rt.tiles * (32 * MT);
+        m_end = rt.hi;
+        n_own = local / rt.tiles * SN;
+        k0 = 0;
+        keys = g.K;
+    }
+    // (out of vector divisions: back to scalar registers)
+    group = __builtin_amdgcn_readfirstlane(group);
+    m_own = __builtin_amdgcn_readfirstlane(m_own);
+    m_end = __builtin_amdgcn_readfirstlane(m_end);
+    n_own = __builtin_amdgcn_readfirstlane(n_own);
+    k0 = __builtin_amdgcn_readfirstlane(k0);
+    keys = __builtin_amdgcn_readfirstlane(keys);
+    const int m0 = MODE == GROUPED_TN && g.M % 8 ? min(m_own, g.M - 32 * MT) : m_own;
+    const int n0 = MODE != GROUPED_NT && g.N % 8 ? min(n_own, g.N - SN) : n_own;
 
-    const int nt = (g.K + OpA::KROWS - 1) / OpA::KROWS;
-    const int back = (int64_t)g.K * ES % 16 ? nt * OpA::KROWS - g.K : 0;
+    const int nt = (keys + OpA::KROWS - 1) / OpA::KROWS;
+    const int back = MODE != GROUPED_TN && (int64_t)keys * ES % 16 ? nt * OpA::KROWS - keys : 0;
     OpA A;
     OpB B;
-    A.init(g.A, g.lda_b, m0, m_end, g.K, back, lane);
-    B.init(g.B + group * g.group_b, g.ldb_b, n0, g.N, g.K, back, lane);
+    A.init(g.A + (int64_t)k0 * g.lda_b, g.lda_b, m0, m_end, keys, back, lane);
+    B.init(MODE == GROUPED_TN ? g.B + (int64_t)k0 * g.ldb_b : g.B + group * g.group_b, g.ldb_b, n0, g.N, keys, back, lane);
     Acc acc[MT][NJ];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -1004,7 +1026,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
     typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
     for (int n = threadIdx.x; n < 32 * MT * CHUNKS; n += 256) {
         const int r = n / CHUNKS, c = n % CHUNKS, row = m0 + r, col = n0 + 4 * c;
-        if (row >= m_end || col >= g.N || col + 4 <= n_own) continue;
+        if (row >= m_end || row < m_own || col >= g.N || col + 4 <= n_own) continue;
         Sum v = *(MPDT_LDS Sum*)(sums + r * SN * 4 + ((c ^ (r & 15)) << 4));
 #pragma unroll
         for (int w = 1; w < 4; ++w) v += *(MPDT_LDS Sum*)(sums + w * PART + r * SN * 4 + ((c ^ (r & 15)) << 4));
@@ -1023,7 +1045,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
 #pragma unroll
             for (int e = 0; e < 4; ++e) f[e] = v[e];
         }
-        const int64_t at = (int64_t)row * g.ldd + col;
+        const int64_t at = (MODE == GROUPED_TN ? group * g.group_d : 0) + (int64_t)row * g.ldd + col;
         const bool all = col >= n_own && col + 4 <= g.N;
         if (T == GroupedType::I8 || g.out16) {
             uint16_t* const to = reinterpret_cast<uint16_t*>(g.D) + at;
@@ -1082,14 +1104,15 @@ bool by_tiles(const GroupedArgs& a) {
 template <GroupedType T, int MODE>
 bool by_strips(const GroupedArgs& a) {
     constexpr int ES = T == GroupedType::I8 ? 1 : 2, KT = MODE == GROUPED_NT ? 128 : 64;
-    if (a.lda_b >= (1 << 23) || a.ldb_b >= (1 << 23) || a.K == 0) return false;
-    if (a.K * (int64_t)ES % 16 && a.K < KT / ES) return false;
-    return MODE != GROUPED_NN || a.N % 8 == 0 || a.N >= 64;
+    if (a.lda_b >= (1 << 23) || a.ldb_b >= (1 << 23)) return false;
+    if (MODE != GROUPED_TN && (a.K == 0 || (a.K * (int64_t)ES % 16 && a.K < KT / ES))) return false;
+    if (MODE != GROUPED_NT && a.N % 8 && a.N < 64) return false;
+    return MODE != GROUPED_TN || a.M % 8 == 0 || a.M >= 64;
 }
 
 template <GroupedType T, int MODE, int MT>
 hipError_t launch_few(const GroupedArgs& a, hipStream_t stream) {
-    const int64_t groups = (a.N + 63) / 64 * most_row_tiles(a, 32 * MT);
+    const int64_t groups = grouped_tiles(MODE, a, 32 * MT, 64);
     grouped_few_kernel<T, MODE, MT><<<dim3((unsigned)groups), dim3(256), 0, stream>>>(a);
     return hipGetLastError();
 }
@@ -1097,6 +1120,10 @@ hipError_t launch_few(const GroupedArgs& a, hipStream_t stream) {
 template <GroupedType T, int MODE>
 hipError_t launch_mode(const GroupedArgs& a, hipStream_t stream) {
     if constexpr (MODE == GROUPED_TN) {
+        // Tiles for less than half of the CUs: 64 x 64, each summed by four waves (12357 rows
+        // of 2 groups into 768 x 320, 18 tiles: 28 us, 78 by tiles; 16000 rows of 2 into 1001 x
+        // 1001, 64 tiles: 90 and 116; 8192 rows of 4 into 1024 x 1024, 128 tiles: 36 and 34)
+        if (grouped_tiles(MODE, a, 128, BN) < CUS / 2 && by_strips<T, MODE>(a)) return launch_few<T, MODE, 2>(a, stream);
         if (!by_tiles<T, MODE>(a)) return launch_any<T, MODE>(a, stream);
         grouped_grad_kernel<T><<<dim3((unsigned)grouped_tiles(MODE, a, 128, BN)), dim3(256), 0, stream>>>(a);
     } else {

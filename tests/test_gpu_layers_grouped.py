@@ -54,6 +54,8 @@ SIZES = [
     ([257, 255, 0], 136, 264),
     ([300, 30, 3], 192, 520),
     ([1] * 70, 40, 48),                 # more groups than lanes
+    ([700, 0, 1301], 136, 200),         # few tiles of D, long sums
+    ([5, 0, 70] * 24, 131, 263),        # many tiles of D that end inside
     ([0] * 65 + [5] + [0] * 80 + [600], 72, 260),
     ([513, 511], 520, 257),
     ([40, 260], 1000, 1000),
