@@ -296,36 +296,57 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
 
 // ---- gradient ------------------------------------------------------------------
 
-// Each workgroup walks rows of its own and keeps its columns' sums of grad * h * rstd
-// in registers; a second launch adds the workgroups' sums in their order.
-constexpr int GRAD_GROUPS = 512;
-int grad_groups(int64_t rows) { return (int)(rows < GRAD_GROUPS ? rows : GRAD_GROUPS); }
+// Each workgroup (each wave, for rows of up to 1024 elements) walks rows of its own and
+// keeps its columns' sums of grad * h * rstd in registers; a second launch adds the
+// workgroups' sums in their order.  Few workgroups leave loads waiting, many have that
+// many sums to write and read again (us at workgroups: 500 x 5120 FP16 20 at 500, 14.4 at
+// 250, 15.5 at 128; 16000 x 1000 53 at 512, 27 at 1024 of four rows; 2000 x 16384 60 at
+// 512, 46 at 256).
+int grad_groups(int64_t rows, int64_t dim) {
+    const int64_t n = dim <= 1024 ? (rows + 3) / 4 : rows;     // (rows of a workgroup at a time)
+    const int64_t most = dim <= 2048 ? 1024 : dim <= 8192 ? 512 : 256;
+    const int64_t few = n < 128 ? n : n < 384 ? 128 : n / 3;
+    return (int)(few < most ? few : most);
+}
 
 template <int T, int WT, int NT, int PIECES>
-__global__ __launch_bounds__(NT) void rms_norm_grad_kernel(NormGradArgs a) {
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_grad_kernel(NormGradArgs a) {
     __shared__ float red[2][NT / 64];
-    const int tid = threadIdx.x;
-    constexpr int ES = Piece<T>::ES;
+    constexpr int ES = Piece<T>::ES, ROWS = NT < 256 ? 256 / NT : 1;
+    // (the next row's loads are under way while one is reduced, where registers hold both)
+    constexpr bool AHEAD = NT < 1024 || (PIECES == 2 && T != DT_F32);
+    const int tid = threadIdx.x % NT, part = threadIdx.x / NT;
+    const int64_t step = (int64_t)gridDim.x * ROWS;
     float dw[PIECES][8];
 #pragma unroll
     for (int u = 0; u < PIECES; ++u)
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[u][e] = 0;
-    // (the next row's loads are under way while this one is reduced)
     Piece<T> g[PIECES], h[PIECES], r[PIECES];
+    auto load_res = [&](int64_t row) {
+        if (!a.grad_res) return;
+#pragma unroll
+        for (int u = 0; u < PIECES; ++u) {
+            const int e0 = 8 * (tid + NT * u);
+            r[u].load(a.grad_res + row * a.gres_b + (int64_t)e0 * ES, a.dim - e0);
+        }
+    };
     auto load = [&](int64_t row) {
 #pragma unroll
         for (int u = 0; u < PIECES; ++u) {
             const int e0 = 8 * (tid + NT * u);
             g[u].load(a.grad + row * a.grad_b + (int64_t)e0 * ES, a.dim - e0);
             h[u].load(a.h + row * a.h_b + (int64_t)e0 * ES, a.dim - e0);
-            if (a.grad_res) r[u].load(a.grad_res + row * a.gres_b + (int64_t)e0 * ES, a.dim - e0);
         }
+        if constexpr (AHEAD) load_res(row);
     };
     int turn = 0;
-    load(blockIdx.x);
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+    int64_t row = (int64_t)blockIdx.x * ROWS + part;
+    if (AHEAD && row < a.rows) load(row);
+    // (rows that share a workgroup are a wave's each and share no barrier)
+    for (; row < a.rows; row += step, turn ^= 1) {
         const float rstd = a.rstd[row];
+        if constexpr (!AHEAD) load(row);
         float c = 0, d[PIECES][8], x[PIECES][8];
 #pragma unroll
         for (int u = 0; u < PIECES; ++u) {
@@ -342,24 +363,48 @@ __global__ __launch_bounds__(NT) void rms_norm_grad_kernel(NormGradArgs a) {
             }
         }
         Piece<T> res[PIECES];
+        if constexpr (AHEAD) {
 #pragma unroll
-        for (int u = 0; u < PIECES; ++u) res[u] = r[u];
-        if (row + gridDim.x < a.rows) load(row + gridDim.x);
+            for (int u = 0; u < PIECES; ++u) res[u] = r[u];
+            if (row + step < a.rows) load(row + step);
+        }
         // (two sets of partial sums in turn: one barrier a row)
         c = over_row<NT>(c, red[turn], [](float p, float q) { return p + q; });
         c = rstd * rstd * (c / a.dim);
+        if constexpr (!AHEAD) load_res(row);
 #pragma unroll
         for (int u = 0; u < PIECES; ++u) {
             const int e0 = 8 * (tid + NT * u);
             Piece<T> o;
+            Piece<WT> w;
+            if constexpr (!AHEAD) w.load(a.weight + (int64_t)e0 * Piece<WT>::ES, a.dim - e0);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
+                // (not ahead: g and h are still held, and d and x made of them again)
+                if constexpr (!AHEAD) d[u][e] = g[u].get(e) * w.get(e), x[u][e] = h[u].get(e);
                 float y = rstd * (d[u][e] - x[u][e] * c);
-                if (a.grad_res) y += res[u].get(e);
+                if (a.grad_res) y += (AHEAD ? res[u] : r[u]).get(e);
                 o.put(e, y);
             }
             o.store(a.grad_h + row * a.gh_b + (int64_t)e0 * ES, a.dim - e0);
         }
+    }
+    if constexpr (ROWS > 1) {
+        // the waves' sums, in their order
+        __shared__ float sums[ROWS - 1][NT * 8 * PIECES];
+        if (part > 0)
+#pragma unroll
+            for (int u = 0; u < PIECES; ++u)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sums[part - 1][(u * 8 + e) * NT + tid] = dw[u][e];
+        __syncthreads();
+        if (part > 0) return;
+#pragma unroll
+        for (int k = 0; k < ROWS - 1; ++k)
+#pragma unroll
+            for (int u = 0; u < PIECES; ++u)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) dw[u][e] += sums[k][(u * 8 + e) * NT + tid];
     }
     float* to = gridDim.x == 1 ? a.grad_weight : a.ws + (int64_t)blockIdx.x * a.dim;
 #pragma unroll
@@ -372,11 +417,12 @@ __global__ __launch_bounds__(NT) void rms_norm_grad_kernel(NormGradArgs a) {
 }
 
 // Columns' sums of the workgroups: 64 columns to a workgroup, 16 threads of four columns
-// beside each other and a sixteenth of the rows to each such line, joined in order.
-__global__ __launch_bounds__(256) void rms_norm_grad_sum_kernel(const float* ws, int groups, int dim, float* out) {
-    __shared__ f32x4 part[16][16];
+// beside each other and a 64th of the rows to each such line, joined in order.
+__global__ __launch_bounds__(1024) void rms_norm_grad_sum_kernel(const float* ws, int groups, int dim, float* out) {
+    constexpr int LINES = 64;
+    __shared__ f32x4 part[LINES][16];
     const int x = threadIdx.x & 15, y = threadIdx.x >> 4, col = blockIdx.x * 64 + 4 * x;
-    const int lo = groups * y / 16, hi = groups * (y + 1) / 16;
+    const int lo = groups * y / LINES, hi = groups * (y + 1) / LINES;
     f32x4 s{0, 0, 0, 0};
     if (col + 4 <= dim) {
         typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
@@ -390,23 +436,26 @@ __global__ __launch_bounds__(256) void rms_norm_grad_sum_kernel(const float* ws,
     }
     part[y][x] = s;
     __syncthreads();
-    if (threadIdx.x < 64 && blockIdx.x * 64 + threadIdx.x < (unsigned)dim) {
-        float v = 0;
+    // (halves of the lines onto each other)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v += part[i][threadIdx.x >> 2][threadIdx.x & 3];
-        out[blockIdx.x * 64 + threadIdx.x] = v;
+    for (int n = LINES / 2; n >= 1; n /= 2) {
+        if (y < n) part[y][x] += part[y + n][x];
+        __syncthreads();
     }
+    if (threadIdx.x < 64 && blockIdx.x * 64 + threadIdx.x < (unsigned)dim)
+        out[blockIdx.x * 64 + threadIdx.x] = part[0][threadIdx.x >> 2][threadIdx.x & 3];
 }
 
 template <int T, int WT>
 hipError_t launch_grad(const NormGradArgs& a, int groups, hipStream_t stream) {
     const auto go = [&](auto NT, auto P) {
         constexpr int nt = decltype(NT)::value, p = decltype(P)::value;
-        rms_norm_grad_kernel<T, WT, nt, p><<<dim3(groups), dim3(nt), 0, stream>>>(a);
+        rms_norm_grad_kernel<T, WT, nt, p><<<dim3(groups), dim3(nt < 256 ? 256 : nt), 0, stream>>>(a);
         return hipGetLastError();
     };
     using std::integral_constant;
     if (a.dim <= 512) return go(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+    if (a.dim <= 1024) return go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
     if (a.dim <= 2048) return go(integral_constant<int, 256>{}, integral_constant<int, 1>{});
     if (a.dim <= 4096) return go(integral_constant<int, 512>{}, integral_constant<int, 1>{});
     if (a.dim <= 8192) return go(integral_constant<int, 512>{}, integral_constant<int, 2>{});
@@ -424,12 +473,12 @@ hipError_t launch_rms_norm(const NormArgs& a, hipStream_t stream) {
 }
 
 int64_t rms_norm_backward_ws(int64_t rows, int64_t dim) {
-    const int g = grad_groups(rows);
+    const int g = grad_groups(rows, dim);
     return g > 1 ? 4 * g * dim : 0;
 }
 
 hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t stream) {
-    const int groups = grad_groups(a.rows);
+    const int groups = grad_groups(a.rows, a.dim);
     if (groups > 0) {
         const hipError_t e = a.type == DT_F32 ? launch_grad<DT_F32, DT_F32>(a, groups, stream)
                              : a.type == DT_BF16 ? (a.w_f32 ? launch_grad<DT_BF16, DT_F32>(a, groups, stream)
@@ -439,7 +488,7 @@ hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t stream) {
         if (e != hipSuccess || groups == 1) return e;
     }
     // (no rows: sums of nothing)
-    rms_norm_grad_sum_kernel<<<dim3((a.dim + 63) / 64), dim3(256), 0, stream>>>(a.ws, groups, a.dim, a.grad_weight);
+    rms_norm_grad_sum_kernel<<<dim3((a.dim + 63) / 64), dim3(1024), 0, stream>>>(a.ws, groups, a.dim, a.grad_weight);
     return hipGetLastError();
 }
 

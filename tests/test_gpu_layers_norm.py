@@ -153,6 +153,20 @@ def test_backward(dtype, dim):
         assert torch.equal(g, gh)
 
 
+@pytest.mark.parametrize("rows, dim", [(2500, 513), (5000, 1001), (3300, 1500), (1601, 2200), (1600, 5000), (800, 9001),
+                                       (300, 32768)])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_backward_many_rows(dtype, rows, dim):
+    """More rows than are held at a time."""
+    (h, hc), (g, gc), (r, rc) = (rows_like(rows, dim, dtype, dim + i, 0, 0) for i in range(3))
+    w = (1 + 0.3 * torch.randn(dim, generator=torch.Generator().manual_seed(dim))).to(dtype)
+    rstd = norm_rstd(hc, 1e-6)
+    gh, gw = mp.rms_norm_backward(g, h, w.cuda(), rstd.cuda(), grad_residual=r, out=g)
+    dh, off, dw, off_w = norm_backward(gc, hc, w, rstd, rc)
+    near(gh, dh, off, dtype)
+    assert ((gw.cpu().double() - dw).abs() <= off_w + 2.0 ** -149).all()
+
+
 def test_backward_against_differences():
     """The gradient along a direction, from outputs of the forward kernel at both sides."""
     rows, dim, step = 3, 96, 2.0 ** -8
