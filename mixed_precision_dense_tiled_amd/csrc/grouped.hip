@@ -255,7 +255,6 @@ __global__ __launch_bounds__(256) void grouped_any_kernel(GroupedArgs g) {
 
 // ---- large problems -------------------------------------------------------------------
 
-constexpr int CUS = 256;
 constexpr int BN = 256;     // columns of a tile
 
 // A workgroup's piece of D.

@@ -13,6 +13,8 @@ namespace mpdt {
 // What a norm writes (the values of the C ABI's mpdt_norm_out).
 enum : int { NORM_PLAIN = 0, NORM_I8_ROWS = 1, NORM_E4M3_ROWS = 2, NORM_E4M3_BLOCKS = 3 };
 
+constexpr int CUS = 256;   // compute units
+
 constexpr int64_t NORM_MAX_DIM = 32768;
 constexpr int64_t NORM_MAX_ROWS = LAUNCH_THREADS / 1024;   // a workgroup of up to 1024 threads to a row
 

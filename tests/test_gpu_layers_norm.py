@@ -89,6 +89,20 @@ def test_numbers_that_are_none(quant):
     assert got.scales[0].eq(1).all() and got.scales[1].isnan().all()
 
 
+@pytest.mark.parametrize("dim", [2560, 4096, 5120, 6144, 6150, 8192])
+def test_many_rows(dim):
+    """More rows than CUs: as in few."""
+    w = (1 + 0.3 * torch.randn(dim, generator=torch.Generator().manual_seed(6))).cuda()
+    x, r = rows_like(600, dim, torch.bfloat16, 1, 0, 0)[0], rows_like(600, dim, torch.bfloat16, 2, 0, 0)[0]
+    for quant in (None, "int8", "fp8_rows", "fp8_blocks"):
+        many = mp.rms_norm(x, w, residual=r, quant=quant)
+        few = [mp.rms_norm(x[i:i + 200], w, residual=r[i:i + 200], quant=quant) for i in (0, 200, 400)]
+        assert torch.equal(many.out, torch.cat([f.out for f in few]))
+        assert torch.equal(many.residual, torch.cat([f.residual for f in few]))
+        if quant is not None:
+            assert torch.equal(many.scales, torch.cat([f.scales for f in few]))
+
+
 def test_in_place_and_apart():
     """x and residual updated in place; buffers around the rows stay."""
     dim, rows, dtype = 1000, 7, torch.bfloat16
