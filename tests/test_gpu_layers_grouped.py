@@ -229,6 +229,52 @@ def test_numbers_that_are_none_stay_in_their_rows():
     assert again[1][99].isnan().all() and torch.equal(again[1][:99], grad[1][:99])
 
 
+@pytest.mark.parametrize("sizes, K, N", [([300, 513, 7], 264, 520), ([40, 0, 90] * 30, 131, 263),
+                                         ([600, 41, 700], 72, 100)])
+def test_numbers_that_are_none_beside_tiles(sizes, K, N):
+    """A group of nothing but NaN, and NaN behind the last group, next to groups that
+    tiles of every size take."""
+    o = offs(sizes)
+    rows = o[-1] + 100
+    off = torch.tensor(o, dtype=torch.int32, device="cuda")
+    bad = 1 if sizes[1] else 2
+    for dtype in (bf16, f16):
+        a, ac = mats((rows, K), dtype, 1, True)
+        g, gc = mats((rows, N), dtype, 2, True)
+        b, bc = mats((len(sizes), K, N), dtype, 3, True)
+        for t in (a, g):
+            t[o[bad]:o[bad + 1]] = float("nan")
+            t[o[-1]:] = float("nan")
+        b[bad] = float("inf")
+        d, dt = mp.gemm_grouped(a, b, off), mp.gemm_grouped(g, b, off, trans_b=True)
+        dw = mp.gemm_grouped_wgrad(a, g, off)
+        for i, (lo, hi) in enumerate(groups_of(o, rows)):
+            if i == bad:
+                assert d[lo:hi].isnan().all() and dt[lo:hi].isnan().all() and dw[i].isnan().all()
+                continue
+            assert torch.equal(d[lo:hi].cpu(), ac[lo:hi].float() @ bc[i].float())
+            assert torch.equal(dt[lo:hi].cpu(), gc[lo:hi].float() @ bc[i].float().T)
+            assert torch.equal(dw[i].cpu(), ac[lo:hi].float().T @ gc[lo:hi].float())
+
+
+def test_rows_past_4_gib():
+    """Rows of one group more than 2^32 bytes apart."""
+    o = [0, 1, 1400, 1500]
+    off = torch.tensor(o, dtype=torch.int32, device="cuda")
+    wide = torch.zeros((1500, 1 << 21), dtype=bf16, device="cuda")     # 4 MiB a row
+    a, g = wide[:, 8:80], wide[:, 1 << 20:(1 << 20) + 136]
+    x, y = mats((1500, 72), bf16, 1, True)[1], mats((1500, 136), bf16, 2, True)[1]
+    a.copy_(x)
+    g.copy_(y)
+    b, bc = mats((3, 72, 136), bf16, 3, True)
+    got, back = mp.gemm_grouped(a, b, off), mp.gemm_grouped(g, b, off, trans_b=True)
+    grad = mp.gemm_grouped_wgrad(a, g, off)
+    for i, (lo, hi) in enumerate(zip(o, o[1:])):
+        assert torch.equal(got[lo:hi].cpu(), x[lo:hi].float() @ bc[i].float())
+        assert torch.equal(back[lo:hi].cpu(), y[lo:hi].float() @ bc[i].float().T)
+        assert torch.equal(grad[i].cpu(), x[lo:hi].float().T @ y[lo:hi].float())
+
+
 def test_matrices_past_4_gib():
     """Groups whose matrices lie more than 2^32 bytes apart."""
     K, N, e = 1024, 4096, 600
