@@ -145,7 +145,7 @@ def rms_norm(x, weight, eps=1e-6, residual=None, quant=None, return_rstd=False, 
         raise ValueError("residual_out needs a residual")
     if dim == 0:
         raise ValueError("x must have at least one column")
-    dtype, device = x.dtype, x.device
+    dtype = x.dtype
     out_type = dtype if quant is None else torch.int8 if quant == "int8" else torch.uint8
     if quant is None and scales_out is not None:
         raise ValueError("scales_out belongs to an output of 8 bits")
@@ -164,25 +164,25 @@ def rms_norm(x, weight, eps=1e-6, residual=None, quant=None, return_rstd=False, 
     if residual is not None:
         pr, ldr = _mat(residual, dtype, "residual")
         if residual_out is None:
-            residual_out = torch.empty((rows, dim), dtype=dtype, device=device)
+            residual_out = x.new_empty((rows, dim))
             ph = residual_out.data_ptr()
         else:
             ph, ldh = _mat(residual_out, dtype, "residual_out")
     if out is None:
-        out = torch.empty((rows, dim), dtype=out_type, device=device)
+        out = x.new_empty((rows, dim), dtype=out_type)
         po = out.data_ptr()
     else:
         po, ldo = _mat(out, out_type, "out")
     if quant is not None:
         lds = grid[-1] if blocks else 1
         if scales_out is None:
-            scales_out = torch.empty(grid, dtype=torch.float32, device=device)
+            scales_out = x.new_empty(grid, dtype=torch.float32)
             ps = scales_out.data_ptr()
         elif blocks:
             ps, lds = _mat(scales_out, torch.float32, "scales_out")
         else:
             ps = _floats(scales_out, rows, "scales_out")
-    rstd = torch.empty(rows, dtype=torch.float32, device=device) if return_rstd else None
+    rstd = x.new_empty(rows, dtype=torch.float32) if return_rstd else None
     if rstd is not None:
         pd = rstd.data_ptr()
     _call(x, "rms_norm", code, rows, dim, px, ldx, pr, ldr, w_code, weight.data_ptr(), eps, _NORM_OUT[quant], po,
@@ -210,14 +210,14 @@ def rms_norm_backward(grad, h, weight, rstd, grad_residual=None, out=None):
     pr, ldr = (None, dim) if grad_residual is None else _mat(grad_residual, h.dtype, "grad_residual")
     pd = _floats(rstd, rows, "rstd")
     if out is None:
-        out = torch.empty((rows, dim), dtype=h.dtype, device=h.device)
+        out = h.new_empty((rows, dim))
     po, ldo = _mat(out, h.dtype, "out")
-    grad_weight = torch.empty(dim, dtype=torch.float32, device=h.device)
+    grad_weight = h.new_empty(dim, dtype=torch.float32)
     L = _lib()
     size = L.rms_norm_backward_workspace(rows, dim)
     if size < 0:
         raise MpdtError("rms_norm_backward", 1, L.mpdt_last_error().decode())
-    ws = torch.empty(size, dtype=torch.uint8, device=h.device) if size else None
+    ws = h.new_empty(size, dtype=torch.uint8) if size else None
     _call(h, "rms_norm_backward", code, rows, dim, pg, ldg, ph, ldh, w_code, weight.data_ptr(), pd, pr, ldr, po, ldo,
           grad_weight.data_ptr(), None if ws is None else ws.data_ptr(), size)
     return out, grad_weight
@@ -263,7 +263,7 @@ def paged_kv_append_rope(q, k, v, k_cache, v_cache, table, cu_q, lens, inv_freq,
                 ("out", out))
     if q is not None:
         if out is None:
-            out = torch.empty((tokens, heads, kv.dim), dtype=dtype, device=q.device)
+            out = q.new_empty((tokens, heads, kv.dim))
             po, ot, oh = out.data_ptr(), heads * kv.dim, kv.dim
         else:
             po, ot, oh = _rows3(out, (tokens, heads, kv.dim), dtype, "out")
@@ -319,7 +319,7 @@ def gemm_grouped(A, B, offsets, trans_b=False, out=None, d16=False):
     pa, lda = _mat(A, A.dtype, "A")
     _on(A, "A", ("B", B), ("offsets", offsets), ("out", out))
     if out is None:
-        out = torch.empty((rows, N), dtype=kind, device=A.device)
+        out = A.new_empty((rows, N), dtype=kind)
         pd, ldd = out.data_ptr(), max(N, 1)
     else:
         pd, ldd = _mat(out, kind, "out")
@@ -348,7 +348,7 @@ def gemm_grouped_wgrad(A, G, offsets, out=None, d16=False):
     pg, ldg = _mat(G, A.dtype, "G")
     _on(A, "A", ("G", G), ("offsets", offsets), ("out", out))
     if out is None:
-        out = torch.empty((groups, K, N), dtype=kind, device=A.device)
+        out = A.new_empty((groups, K, N), dtype=kind)
     pd, ldd, sd = _stack(out, kind, "out")
     _call(A, "gemm_grouped_wgrad", code, groups, rows, N, K, pa, lda, pg, ldg, poff, pd, ldd, sd,
           int(kind != torch.float32))
@@ -377,7 +377,7 @@ def gemm_grouped_w8a8(X, x_scale, W, w_scale, offsets, bias=None, out=None):
     _on(X, "X", ("x_scale", x_scale), ("W", W), ("w_scale", w_scale), ("offsets", offsets), ("bias", bias),
                 ("out", out))
     if out is None:
-        out = torch.empty((rows, N), dtype=torch.bfloat16, device=X.device)
+        out = X.new_empty((rows, N), dtype=torch.bfloat16)
         py, ldy = out.data_ptr(), max(N, 1)
     else:
         py, ldy = _mat(out, torch.bfloat16, "out")
