@@ -13,7 +13,7 @@
 //
 // 8192 x 7168 BF16 with a residual into E4M3 blocks: 80 us, 5.1 TB/s, what a large copy
 // reaches; without the residual 60 us, bound by the codes' arithmetic (39.5 us without
-// codes; both with rows that the last cache holds).  Gradient of 3001 x 5120 FP16: 30 us
+// codes; both with rows that the last cache holds).  Gradient of 3001 x 5120 FP16: 27 us
 // and 4 for the columns' sums.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -313,7 +313,7 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
 // keeps its columns' sums of grad * h * rstd in registers; a second launch adds the
 // workgroups' sums in their order.  Few workgroups leave loads waiting, many have that
 // many sums to write and read again (us at workgroups: 500 x 5120 FP16 20 at 500, 14.4 at
-// 250, 15.5 at 128; 16000 x 1000 53 at 512, 27 at 1024 of four rows; 2000 x 16384 60 at
+// 250, 15.5 at 128 of 512 threads; 16000 x 1000 53 at 512, 27 at 1024 of four rows; 2000 x 16384 60 at
 // 512, 46 at 256).
 int grad_groups(int64_t rows, int64_t dim) {
     const int64_t n = dim <= 1024 ? (rows + 3) / 4 : rows;     // (rows of a workgroup at a time)
@@ -471,6 +471,9 @@ hipError_t launch_grad(const NormGradArgs& a, int groups, hipStream_t stream) {
     if (a.dim <= 1024) return go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
     if (a.dim <= 2048) return go(integral_constant<int, 256>{}, integral_constant<int, 1>{});
     if (a.dim <= 4096) return go(integral_constant<int, 512>{}, integral_constant<int, 1>{});
+    // (8192 x 6144 FP16 68 us, 72 by 512 threads of two, 65 by 256 of three, which take 16.3 where 500
+    // x 5120 take 13.2 so; 8192 x 7168 80 by 512 of two, 97 by 1024 of one)
+    if (a.dim <= 6144) return go(integral_constant<int, 768>{}, integral_constant<int, 1>{});
     if (a.dim <= 8192) return go(integral_constant<int, 512>{}, integral_constant<int, 2>{});
     if (a.dim <= 16384) return go(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
     return go(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
