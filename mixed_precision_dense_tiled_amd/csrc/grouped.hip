@@ -816,17 +816,37 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     tile_run<T, GROUPED_NN, 1, LDS>(g, scalar(t), lds_cast(lds_), wave, lane);
 }
 
-// The weights' gradient: 128 x 256 tiles, two workgroups to a CU.  A group's rows make a
-// short sum, so that a tile's beginning and its store take as long as its product (384
-// rows: 2 + 3 us and 10); another workgroup's product goes on meanwhile (12288 rows over 29
-// groups of 2048 x 1408 FP16: 116 to 125 us, 565 TFLOP/s, 185 MB of D written).
-template <GroupedType T>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void grouped_grad_kernel(GroupedArgs g) {
+// 128 x 256 tiles, two workgroups to a CU: for short sums, whose tiles take as long to
+// begin and to store as for their product (384 rows of a weights' gradient: 2 + 3 us and
+// 10); another workgroup's product goes on meanwhile.  Weights' gradient of 12288 rows over
+// 29 groups of 2048 x 1408 FP16: 116 to 125 us, 565 TFLOP/s, 185 MB of D written.  An XCD
+// takes a run of neighbouring tiles.
+template <GroupedType T, int MODE>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void grouped_half_kernel(GroupedArgs g) {
     constexpr int LDS = 73728;
     __shared__ __attribute__((aligned(1024))) char lds_[LDS];
+    MPDT_LDS char* const lds = lds_cast(lds_);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const Tile t = scalar(tile_at<GROUPED_TN, 128>(g, lane));
-    tile_run<T, GROUPED_TN, 2, LDS>(g, t, lds_cast(lds_), wave, lane);
+    if constexpr (MODE == GROUPED_TN) {
+        tile_run<T, MODE, 2, LDS>(g, scalar(tile_at<MODE, 128>(g, lane)), lds, wave, lane);
+    } else {
+        const int tiles_n = (g.N + BN - 1) / BN;
+        int tiles = 0, most = 0;
+        for (int e0 = 0; e0 < g.groups; e0 += 64) {
+            const Counts c = lane_group(g, e0, lane, most);
+            tiles += __builtin_amdgcn_readlane(lanes_sum((c.end - c.lo + 127) / 128), 63);
+        }
+        tiles *= tiles_n;
+        const int x = blockIdx.x % NUM_XCD, n = share(tiles, x) + blockIdx.x / NUM_XCD;
+        if (n >= share(tiles, x + 1)) return;   // (the whole workgroup)
+        const RowTile r = row_tile<128>(g, n / tiles_n, lane);
+        // up to GROUP_M row tiles beside each other, then the next column tile
+        const int local = r.tile * tiles_n + n % tiles_n, s = local / (GROUP_M * tiles_n);
+        const int high = min(r.tiles - s * GROUP_M, GROUP_M), in = local - s * GROUP_M * tiles_n;
+        const Tile t = scalar(Tile{r.group, r.lo + (s * GROUP_M + in % high) * 128, r.hi, in / high * BN, 0, g.K, 2, 0});
+        if (t.m_end - t.m0 > 64) tile_run<T, MODE, 2, LDS>(g, t, lds, wave, lane);
+        else tile_run<T, MODE, 1, LDS>(g, t, lds, wave, lane);
+    }
 }
 
 // ---- few rows --------------------------------------------------------------------------
@@ -1125,13 +1145,14 @@ hipError_t launch_few(const GroupedArgs& a, hipStream_t stream) {
 
 template <GroupedType T, int MODE>
 hipError_t launch_mode(const GroupedArgs& a, hipStream_t stream) {
+    constexpr int64_t ES = T == GroupedType::I8 ? 1 : 2;
     if constexpr (MODE == GROUPED_TN) {
         // Tiles for less than half of the CUs: 64 x 64, each summed by four waves (12357 rows
         // of 2 groups into 768 x 320, 18 tiles: 28 us, 78 by tiles; 16000 rows of 2 into 1001 x
         // 1001, 64 tiles: 90 and 116; 8192 rows of 4 into 1024 x 1024, 128 tiles: 36 and 34)
         if (grouped_tiles(MODE, a, 128, BN) < CUS / 2 && by_strips<T, MODE>(a)) return launch_few<T, MODE, 2>(a, stream);
         if (!by_tiles<T, MODE>(a)) return launch_any<T, MODE>(a, stream);
-        grouped_grad_kernel<T><<<dim3((unsigned)grouped_tiles(MODE, a, 128, BN)), dim3(256), 0, stream>>>(a);
+        grouped_half_kernel<T, MODE><<<dim3((unsigned)grouped_tiles(MODE, a, 128, BN)), dim3(256), 0, stream>>>(a);
     } else {
         // Too few tiles of 64 rows for half of the CUs: strips (512 rows of 4 groups of 2048 x
         // 2048, 96 tiles: 16 us, 31 by tiles; 1024 rows, 160 tiles: 26 either way), two blocks
@@ -1148,6 +1169,14 @@ hipError_t launch_mode(const GroupedArgs& a, hipStream_t stream) {
                 return hipGetLastError();
             }
         }
+        // Short sums (16384 rows of 16 groups of 768 x 2048: 60 us, 67 by the larger tiles; of
+        // 4 groups of 128 x 4096 39 and 59; INT8, 9651 rows of 3 groups of 1280 x 5888 116 and
+        // 132; 8192 rows of 8 groups of 1024 x 4096 75 and 82, with B^T 83 and 81)
+        if (a.K > 0 && a.K * ES < 2048 + (MODE == GROUPED_NN)) {
+            const int64_t groups = grouped_tiles(MODE, a, 128, BN) + NUM_XCD;
+            grouped_half_kernel<T, MODE><<<dim3((unsigned)groups), dim3(256), 0, stream>>>(a);
+            return hipGetLastError();
+        }
         grouped_tile_kernel<T, MODE><<<dim3((unsigned)tile_workgroups(a)), dim3(256), 0, stream>>>(a);
     }
     return hipGetLastError();
@@ -1163,7 +1192,7 @@ hipError_t launch_type(int mode, const GroupedArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-bool grouped_fits(int mode, const GroupedArgs& a) { return grouped_tiles(mode, a, 128, 128) <= MAX_GROUPS; }
+bool grouped_fits(int mode, const GroupedArgs& a) { return grouped_tiles(mode, a, 128, 128) <= MAX_GROUPS - NUM_XCD; }
 
 hipError_t launch_grouped(GroupedType type, int mode, const GroupedArgs& a, hipStream_t stream) {
     switch (type) {

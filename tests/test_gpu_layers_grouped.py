@@ -72,6 +72,14 @@ SIZES = [
     ([70000], 16, 264),                 # more whole tiles than two rounds of the card
     ([300, 20000, 90, 40000, 5, 70, 8000], 24, 300),
     ([257, 0, 100] * 40, 8, 16),        # whole and part tiles past the 64th group
+    # the same with sums that are not short
+    ([700, 0, 900, 513, 129, 65, 1, 800], 1100, 1032),
+    ([700, 0, 900, 513, 129, 65, 1, 800], 2061, 1501),
+    ([4000, 17, 250], 2056, 2056),
+    ([70000], 1064, 264),
+    ([300, 20000, 90, 40000, 5, 70, 8000], 1048, 300),
+    ([257, 0, 100] * 40, 2064, 528),
+    ([9000, 300, 9, 8000], 1064, 4104),     # four rounds of the card
 ]
 
 
