@@ -103,7 +103,7 @@ __device__ __forceinline__ void put16(char* D, int64_t at, float v) {
 // of 64 bytes along the summed axis.  An operand whose rows run along that axis (KC) is
 // read back along them; one whose rows lie across it (KS) with the transposing reads.
 // Bound by the way through registers and a barrier every 64 bytes of k (3001 rows over 11
-// groups of 1003 x 1501 FP16: 79 us, 26 by the tiles below).
+// groups of 1003 x 1501 FP16: 79 us, 24 by the tiles below).
 template <GroupedType T, int MODE>
 __global__ __launch_bounds__(256) void grouped_any_kernel(GroupedArgs g) {
     constexpr Kind KD = KindOf<T>::kind;
