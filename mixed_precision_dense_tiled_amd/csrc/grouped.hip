@@ -1169,11 +1169,14 @@ hipError_t launch_mode(const GroupedArgs& a, hipStream_t stream) {
                 return hipGetLastError();
             }
         }
-        // Short sums (16384 rows of 16 groups of 768 x 2048: 60 us, 67 by the larger tiles; of
-        // 4 groups of 128 x 4096 39 and 59; INT8, 9651 rows of 3 groups of 1280 x 5888 116 and
-        // 132; 8192 rows of 8 groups of 1024 x 4096 75 and 82, with B^T 83 and 81)
-        if (a.K > 0 && a.K * ES < 2048 + (MODE == GROUPED_NN)) {
-            const int64_t groups = grouped_tiles(MODE, a, 128, BN) + NUM_XCD;
+        // Short sums, and somewhat longer ones where all tiles run at once (16384 rows of 16
+        // groups of 768 x 2048: 60 us, 67 by the larger tiles; of 4 groups of 128 x 4096 39 and 59;
+        // of 8 groups of 512 x 14336 310 and 352; INT8, 9651 rows of 3 groups of 1280 x 5888 116
+        // and 132; 3001 rows of 11 groups of 1003 x 1501 24 and 26.  But 16384 rows of 8 groups of
+        // 1000 x 14336, with B^T: 804 and 640)
+        const int64_t halves = grouped_tiles(MODE, a, 128, BN);
+        if (a.K > 0 && a.K * ES <= (halves <= 2 * CUS ? 2048 : 1536)) {
+            const int64_t groups = halves + NUM_XCD;
             grouped_half_kernel<T, MODE><<<dim3((unsigned)groups), dim3(256), 0, stream>>>(a);
             return hipGetLastError();
         }
