@@ -54,8 +54,8 @@ mpdt_status rms_norm(int dtype, int64_t rows, int64_t dim, const void* x, int64_
 
 /* The gradient of a plain rms_norm in h and weight, with grad the one in y, and
  * with the rstd [rows] that it gave:
- *   grad_h = grad_residual + rstd * (g - h * rstd^2 * mean(g * h)),  g = grad * weight
- *   grad_weight[j] = sum over rows of grad * h * rstd      (FP32, in a fixed order)
+ *   grad_h = grad_residual + rstd * (g - n * mean(g * n)),  g = grad * weight, n = h * rstd
+ *   grad_weight[j] = sum over rows of grad * n      (FP32, in a fixed order)
  * grad_residual, the gradient in h_out, may be NULL (0).  grad_h may be exactly
  * grad or grad_residual.  All [rows, dim] in dtype. */
 int64_t rms_norm_backward_workspace(int64_t rows, int64_t dim);

@@ -1,0 +1,66 @@
+"""rms_norm and its gradient where values leave the usual ranges: against the
+definition in 64 bits, and codes byte for byte."""
+import pytest
+import torch
+
+import mixed_precision_dense_tiled_amd as mp
+from layers_ref import HALF, TINY, norm_backward, norm_rstd
+
+pytestmark = pytest.mark.gpu
+# a width of every launch, none a whole number of a thread's elements
+WIDTHS = [5, 300, 700, 1501, 3001, 5003, 7001, 9001, 20001]
+
+
+def randn(shape, seed):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed))
+
+
+def close(got, want, off, dtype):
+    err = (got.cpu().double() - want).abs()
+    bound = off + HALF[dtype] * want.abs() * (1 + 2.0 ** -7) + TINY[dtype]
+    assert (err <= bound).all(), (err - bound).max()
+
+
+@pytest.mark.parametrize("dim", [4] + WIDTHS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("size", [1e37, 1e20, 1e-20, 1e-30])
+def test_backward_far_sizes(size, dtype, dim):
+    """Rows whose squares, and whose rstd's square, leave FP32: the projection on the row stays."""
+    rows = 7
+    h = (randn((rows, dim), dim) * size).to(dtype)
+    if dim == 4:
+        h[0] = torch.tensor([3e37, -1e37, 2e37, 0.5e37]).to(dtype) if size == 1e37 else h[0]
+    g = randn((rows, dim), dim + 1).to(dtype)
+    w = (1 + 0.3 * randn(dim, dim + 2)).to(dtype)
+    rstd = norm_rstd(h, 0.0)
+    gh, gw = mp.rms_norm_backward(g.cuda(), h.cuda(), w.cuda(), rstd.cuda())
+    dh, off, dw, off_w = norm_backward(g, h, w, rstd, None)
+    close(gh, dh, off, dtype)
+    assert ((gw.cpu().double() - dw).abs() <= off_w).all()
+
+
+@pytest.mark.parametrize("dim", WIDTHS)
+@pytest.mark.parametrize("size", [1e4, 1e-3, 1e-6])
+def test_backward_far_sizes_of_fp16(size, dim):
+    """FP16's largest values and its subnormals."""
+    h = (randn((7, dim), dim) * size).to(torch.float16)
+    g = (randn((7, dim), dim + 1) * min(1.0, 100 * size)).to(torch.float16)
+    w = (1 + 0.3 * randn(dim, dim + 2)).to(torch.float16)
+    rstd = norm_rstd(h, 0.0)
+    gh, gw = mp.rms_norm_backward(g.cuda(), h.cuda(), w.cuda(), rstd.cuda())
+    dh, off, dw, off_w = norm_backward(g, h, w, rstd, None)
+    close(gh, dh, off, torch.float16)
+    assert ((gw.cpu().double() - dw).abs() <= off_w).all()
+
+
+@pytest.mark.parametrize("dim", [5, 700, 3001, 20001])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_backward_of_zeros(dtype, dim):
+    """A row of zeros under an eps whose rstd's square leaves FP32: rstd * grad * weight."""
+    g, w = randn((3, dim), dim).to(dtype), (1 + 0.3 * randn(dim, dim + 1)).to(dtype)
+    h = torch.zeros((3, dim), dtype=dtype)
+    rstd = norm_rstd(h, 1e-45)
+    assert float(rstd[0]) > 2.0 ** 70
+    gh, gw = mp.rms_norm_backward(g.cuda(), h.cuda(), w.cuda(), rstd.cuda())
+    assert torch.equal(gh.cpu(), (rstd[:, None] * (g.float() * w.float())).to(dtype))
+    assert not gw.any()
