@@ -42,7 +42,9 @@ typedef enum {
  *   scale = amax / qmax   (FP32 division; 1 where that is 0)
  *   code = round to nearest even of y / scale, cut to [-qmax, qmax].
  * A row or block that holds a NaN has scale NaN (INT8 codes 0, E4M3 codes NaN); an
- * infinite x makes y NaN in its place and 0 elsewhere.
+ * infinite x makes y NaN in its place and 0 elsewhere.  A row of root mean square below
+ * 2.9e-39 with eps 0 has an infinite rstd: its y are infinite or NaN, and its scales one or
+ * the other (the values that its codes stand for are NaN either way).
  * h is written where h_out is not NULL (it needs a residual); h_out may be exactly
  * x or residual, and with MPDT_NORM_PLAIN out may be exactly x or residual: the
  * same pointer and leading dimension.  scales: [rows] (ld_scales 1 is tight), or

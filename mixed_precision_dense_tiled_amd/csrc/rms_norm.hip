@@ -217,8 +217,10 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(NormArgs 
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = mul_rn(mul_rn(h[u].get(e), rstd), w[u].get(e));
     };
-    // (past the row's end a piece holds 0 * rstd: an amax of 0, or NaN where rstd is, as
-    // it is in the whole row then)
+    // (past the row's end a piece holds 0 * rstd: an amax of 0, or NaN where rstd is, as it is in
+    // the whole row then, or where rstd is infinite, and with it every y that is not NaN.  That
+    // NaN is left in the scale: to keep it out took registers, and with them up to 30 % of other
+    // rows' speed, 4096 x 16384 BF16 into INT8 148 us against 115.)
     auto amax_of = [](const float (&y)[8]) {
         float m = fabsf(y[0]);
 #pragma unroll

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import mixed_precision_dense_tiled_amd as mp
-from layers_ref import HALF, TINY, norm_backward, norm_rstd
+from layers_ref import HALF, TINY, norm_backward, norm_rows, norm_rstd, quantise
 
 pytestmark = pytest.mark.gpu
 # a width of every launch, none a whole number of a thread's elements
@@ -64,3 +64,29 @@ def test_backward_of_zeros(dtype, dim):
     gh, gw = mp.rms_norm_backward(g.cuda(), h.cuda(), w.cuda(), rstd.cuda())
     assert torch.equal(gh.cpu(), (rstd[:, None] * (g.float() * w.float())).to(dtype))
     assert not gw.any()
+
+
+def same_numbers(a, b):
+    assert torch.equal(a.isnan(), b.isnan()) and torch.equal(a.nan_to_num(-1), b.nan_to_num(-1)), (a, b)
+
+
+@pytest.mark.parametrize("quant", ["int8", "fp8_rows", "fp8_blocks"])
+@pytest.mark.parametrize("dim", [1, 9, 100, 128, 130] + WIDTHS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rstd_of_infinity(dtype, dim, quant):
+    """Rows of FP32's subnormals without an eps: every y is infinite, or NaN from a 0; scales are
+    one or the other, and the values that the codes stand for are NaN."""
+    x = torch.full((3, dim), 2.0 ** -133).to(dtype)
+    x[1] = -x[1]
+    x[2, dim // 2] = 0
+    w = torch.ones(dim, dtype=dtype)
+    got = mp.rms_norm(x.cuda(), w.cuda(), eps=0.0, quant=quant)
+    values, scales = quantise(norm_rows(x, w, 0.0), quant)
+    assert scales[:2].isinf().all() and scales[2].isnan().any()
+    mine = got.scales.cpu()
+    assert not mine.isfinite().any() and mine[scales.isnan()].isnan().all()
+    out = got.out.cpu() if quant == "int8" else got.out.cpu().view(torch.float8_e4m3fn)
+    same_numbers(out.float(), values)
+    block = 128 if quant == "fp8_blocks" else dim
+    each = mine.view(3, -1).repeat_interleave(block, 1)[:, :dim]
+    assert (out.float() * each).isnan().all()
