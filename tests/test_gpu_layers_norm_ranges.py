@@ -90,3 +90,22 @@ def test_rstd_of_infinity(dtype, dim, quant):
     block = 128 if quant == "fp8_blocks" else dim
     each = mine.view(3, -1).repeat_interleave(block, 1)[:, :dim]
     assert (out.float() * each).isnan().all()
+
+
+@pytest.mark.parametrize("quant", ["fp8_rows", "fp8_blocks"])
+@pytest.mark.parametrize("dim", [128] + WIDTHS)
+def test_minus_zero(quant, dim):
+    """E4M3 codes keep the sign of a 0, as the division by the scale does: of -0 in x, of a
+    negative x under a weight of 0, in rows of zeros, and of what is rounded to 0."""
+    x = randn((4, dim), dim)
+    x[:, ::3] = -0.0
+    x[1] = -0.0
+    x[2, 1::3] *= 1e-6
+    w = 1 + 0.3 * randn(dim, dim + 1)
+    w[2::5] = 0
+    for dtype in (torch.bfloat16, torch.float16, torch.float32):
+        h, v = x.to(dtype), w.to(dtype)
+        got = mp.rms_norm(h.cuda(), v.cuda(), quant=quant)
+        values, _ = quantise(norm_rows(h, v, 1e-6), quant)
+        want = values.to(torch.float8_e4m3fn).view(torch.uint8)
+        assert (want == 0x80).any() and torch.equal(got.out.cpu(), want)
