@@ -71,13 +71,13 @@ mpdt_status rms_norm_backward(int dtype, int64_t rows, int64_t dim, const void* 
  *   a' = a cos t - b sin t,  b' = b cos t + a sin t,  t = p * inv_freq[i],
  * where p = lens - (cu_q[b + 1] - row) is the token's position in its sequence and
  * pair i is (i, i + pairs), or (2 i, 2 i + 1) with interleaved.  The angle is
- * formed and brought into one turn in FP64, cos, sin and the two products in FP32,
- * and a', b' are rounded once to their type (E4M3: divided by the head's scale and
- * cut first, as in paged_kv_append).  Values are stored as they are.  inv_freq
- * [pairs] FP32, 2 * pairs at most dim.  q [tokens, heads, dim] in the type of the
- * new keys, or NULL with heads 0; q_out may be exactly q.  Rows of q that belong
- * to no sequence are not written; a token without a place in the cache is dropped
- * there, and its q turned all the same. */
+ * formed, and cos and sin taken of it, in FP64, each rounded once to FP32; the two
+ * products are FP32 ones, and a', b' are rounded once to their type (E4M3: divided by
+ * the head's scale and cut first, as in paged_kv_append).  Values are stored as they
+ * are.  inv_freq [pairs] FP32, 2 * pairs at most dim.  q [tokens, heads, dim] in the
+ * type of the new keys, or NULL with heads 0; q_out may be exactly q.  Rows of q that
+ * belong to no sequence are not written; a token without a place in the cache is
+ * dropped there, and its q turned all the same. */
 mpdt_status paged_kv_append_rope(const mpdt_paged_kv* kv, const mpdt_sequences* seq, int dtype,
                                  const void* k_new, int64_t k_token, int64_t k_head,
                                  const void* v_new, int64_t v_token, int64_t v_head,
