@@ -31,7 +31,8 @@ typedef enum {
     MPDT_NORM_E4M3_BLOCKS = 3   /* E4M3 and a scale for 1 x 128: the A, scale_a of gemm_fp8_blockscaled */
 } mpdt_norm_out;
 
-/* Root-mean-square norm of rows [rows, dim], dim at most 32768, of BF16, FP16 or
+/* Root-mean-square norm of rows [rows, dim], dim at most 32768 and rows at most
+ * 4194303 (more in several calls: rows do not know of each other), of BF16, FP16 or
  * FP32 (dtype); weight [dim] in w_dtype (x's type or MPDT_F32).  For each row
  *   h = x + residual      (residual not NULL: one FP32 addition, rounded once to
  *                          x's type; else h = x)
@@ -59,7 +60,7 @@ mpdt_status rms_norm(int dtype, int64_t rows, int64_t dim, const void* x, int64_
  *   grad_h = grad_residual + rstd * (g - n * mean(g * n)),  g = grad * weight, n = h * rstd
  *   grad_weight[j] = sum over rows of grad * n      (FP32, in a fixed order)
  * grad_residual, the gradient in h_out, may be NULL (0).  grad_h may be exactly
- * grad or grad_residual.  All [rows, dim] in dtype. */
+ * grad or grad_residual.  All [rows, dim] in dtype, rows at most 2^30. */
 int64_t rms_norm_backward_workspace(int64_t rows, int64_t dim);
 mpdt_status rms_norm_backward(int dtype, int64_t rows, int64_t dim, const void* grad, int64_t ld_grad,
                               const void* h, int64_t ld_h, int w_dtype, const void* weight, const float* rstd,

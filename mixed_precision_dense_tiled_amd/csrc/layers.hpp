@@ -16,7 +16,10 @@ enum : int { NORM_PLAIN = 0, NORM_I8_ROWS = 1, NORM_E4M3_ROWS = 2, NORM_E4M3_BLO
 constexpr int CUS = 256;   // compute units
 
 constexpr int64_t NORM_MAX_DIM = 32768;
-constexpr int64_t NORM_MAX_ROWS = LAUNCH_THREADS / 1024;   // a workgroup of up to 1024 threads to a row
+// Rows of a norm's launch, a workgroup of up to 1024 threads to each.  (Its gradient's workgroups
+// walk rows: any number.)
+constexpr int64_t NORM_MAX_ROWS = LAUNCH_THREADS / 1024;
+static_assert(NORM_MAX_ROWS == 4194303, "as the C ABI says");
 
 struct NormArgs {
     const char* x;          // strides in bytes

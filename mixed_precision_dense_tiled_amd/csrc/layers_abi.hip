@@ -61,7 +61,6 @@ mpdt_status check_norm(const char* fn, int dtype, int64_t rows, int64_t dim, int
     if (w_dtype != dtype && w_dtype != MPDT_F32) return invalid(fn, "the weight must have the rows' type or FP32");
     if (!in_dims(rows, 0) || dim < 1 || dim > mpdt::NORM_MAX_DIM)
         return invalid(fn, "rows out of range, or dim outside 1 .. 32768");
-    if (rows > mpdt::NORM_MAX_ROWS) return invalid(fn, "too many rows");
     return MPDT_SUCCESS;
 }
 
@@ -79,6 +78,7 @@ MPDT_EXPORT mpdt_status rms_norm(int dtype, int64_t rows, int64_t dim, const voi
                                  void* h_out, int64_t ld_h, float* rstd, void* stream) {
     const char* fn = "rms_norm";
     TRY(check_norm(fn, dtype, rows, dim, w_dtype));
+    if (rows > mpdt::NORM_MAX_ROWS) return invalid(fn, "too many rows: at most 4194303 to a call");
     if (!(eps >= 0) || !std::isfinite(eps)) return invalid(fn, "eps must be finite and not negative");
     if (norm_out < MPDT_NORM_PLAIN || norm_out > MPDT_NORM_E4M3_BLOCKS) return invalid(fn, "unknown output");
     if (h_out && !residual) return invalid(fn, "h_out needs a residual");

@@ -124,10 +124,11 @@ def rms_norm(x, weight, eps=1e-6, residual=None, quant=None, return_rstd=False, 
     """Root-mean-square norm of rows, with the residual's addition before it and
     an output in 8 bits after it.
 
-    x [rows, dim] BF16, FP16 or FP32 (rows may be strided), dim at most 32768;
-    weight [dim] in x's type or FP32; residual like x.  With h = x + residual,
-    rounded once to x's type (x alone without a residual), rstd = 1 /
-    sqrt(mean(h^2) + eps) and y = (h * rstd) * weight in FP32.  Returns RmsNorm:
+    x [rows, dim] BF16, FP16 or FP32 (rows may be strided), dim at most 32768 and
+    rows at most 4194303 (more in several calls); weight [dim] in x's type or
+    FP32; residual like x.  With h = x + residual, rounded once to x's type (x
+    alone without a residual), rstd = 1 / sqrt(mean(h^2) + eps) and y = (h *
+    rstd) * weight in FP32.  Returns RmsNorm:
       out       y in x's type, or with quant codes of 8 bits: "int8" for
                 gemm_w8a8, "fp8_rows" (E4M3 in uint8) for gemm_fp8_rowscaled,
                 "fp8_blocks" (E4M3, 1 x 128 scales) for gemm_fp8_blockscaled

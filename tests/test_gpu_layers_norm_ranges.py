@@ -109,3 +109,15 @@ def test_minus_zero(quant, dim):
         values, _ = quantise(norm_rows(h, v, 1e-6), quant)
         want = values.to(torch.float8_e4m3fn).view(torch.uint8)
         assert (want == 0x80).any() and torch.equal(got.out.cpu(), want)
+
+
+def test_backward_of_more_rows_than_a_norm_takes():
+    """The workgroups of the gradient walk rows, of any number."""
+    rows, dim = (1 << 22) + 3, 8
+    h, g = (randn((rows, dim), i).to(torch.bfloat16) for i in (1, 2))
+    w = 1 + 0.3 * randn(dim, 3)
+    rstd = norm_rstd(h, 1e-6)
+    gh, gw = mp.rms_norm_backward(g.cuda(), h.cuda(), w.cuda(), rstd.cuda())
+    dh, off, dw, off_w = norm_backward(g, h, w, rstd, None)
+    close(gh, dh, off, torch.bfloat16)
+    assert ((gw.cpu().double() - dw).abs() <= off_w).all()
