@@ -121,3 +121,67 @@ def test_backward_of_more_rows_than_a_norm_takes():
     dh, off, dw, off_w = norm_backward(g, h, w, rstd, None)
     close(gh, dh, off, torch.bfloat16)
     assert ((gw.cpu().double() - dw).abs() <= off_w).all()
+
+
+@pytest.mark.parametrize("quant", [None, "int8", "fp8_rows", "fp8_blocks"])
+@pytest.mark.parametrize("dim", [128] + WIDTHS + [16384, 32768])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_weights_of_fp32(dtype, dim, quant):
+    """16-bit rows under FP32 weights that 16 bits do not hold, few rows and more than CUs."""
+    w = 1 + 0.3 * randn(dim, dim + 1)
+    for rows in (3, 300) if dim <= 8192 else (3,):
+        x, r = randn((rows, dim), dim).to(dtype), randn((rows, dim), dim + 2).to(dtype)
+        h = (x.float() + r.float()).to(dtype)
+        got = mp.rms_norm(x.cuda(), w.cuda(), residual=r.cuda(), quant=quant)
+        y = norm_rows(h, w, 1e-6)
+        if quant is None:
+            assert torch.equal(got.out.cpu(), y.to(dtype))
+            continue
+        values, scales = quantise(y, quant)
+        codes = got.out.cpu() if quant == "int8" else got.out.cpu().view(torch.float8_e4m3fn)
+        assert torch.equal(got.scales.cpu(), scales) and torch.equal(codes.float(), values)
+
+
+@pytest.mark.parametrize("quant", [None, "int8", "fp8_blocks"])
+@pytest.mark.parametrize("dim", [128] + WIDTHS + [16384, 32768])
+def test_in_place_at_every_width(dim, quant):
+    """x and the residual replaced by what comes of them, where a row is a wave's and where many
+    waves share it; and a gradient in place of its gradients."""
+    dtype = torch.bfloat16
+    w = (1 + 0.3 * randn(dim, dim + 1)).to(dtype)
+    for rows in (3, 300) if dim <= 8192 else (3,):
+        xc, rc, gc = (randn((rows, dim), dim + i).to(dtype) for i in (2, 3, 4))
+        want = mp.rms_norm(xc.cuda(), w.cuda(), residual=rc.cuda(), quant=quant, return_rstd=True)
+        for first in ("x", "residual"):
+            x, r = xc.cuda(), rc.cuda()
+            h, out = (x, r) if first == "x" else (r, x)
+            got = mp.rms_norm(x, w.cuda(), residual=r, quant=quant, residual_out=h, out=out if quant is None else None)
+            assert torch.equal(h, want.residual) and torch.equal(got.out, want.out)
+            if quant is not None:
+                assert torch.equal(got.scales, want.scales)
+        if quant is None:
+            gh, gw = mp.rms_norm_backward(gc.cuda(), want.residual, w.cuda(), want.rstd, grad_residual=rc.cuda())
+            for where in ("grad", "grad_residual"):
+                g, r = gc.cuda(), rc.cuda()
+                a, b = mp.rms_norm_backward(g, want.residual, w.cuda(), want.rstd, grad_residual=r,
+                                            out=g if where == "grad" else r)
+                assert torch.equal(a, gh) and torch.equal(b, gw)
+
+
+@pytest.mark.parametrize("rows, dim", [(1, 700), (3, 5003), (127, 64), (500, 513), (2500, 1000), (20000, 209), (1000, 3001),
+                                       (900, 5120), (3001, 1501), (1200, 7001), (1100, 9001), (700, 20001)])
+def test_weights_gradient_by_its_sums(rows, dim):
+    """The weight's gradient within the roundings of the additions that it takes: a workgroup's (up
+    to 1024 columns a wave's) rows one after the other, four waves' sums where they share a
+    workgroup, then the workgroups' in 64 lines and a tree of 6; and of the product (h * rstd) * grad,
+    whose last rounding is the addition's."""
+    h, g = (randn((rows, dim), dim + i).to(torch.float16) for i in (0, 1))
+    w = torch.ones(dim, dtype=torch.float16)
+    rstd = norm_rstd(h, 1e-6)
+    _, gw = mp.rms_norm_backward(g.cuda(), h.cuda(), w.cuda(), rstd.cuda())
+    size = mp.layers._lib().rms_norm_backward_workspace(rows, dim)
+    groups, waves = max(size // (4 * dim), 1), 4 if dim <= 1024 else 1
+    deep = -(-rows // (groups * waves)) + waves - 1 + (-(-groups // 64) + 6 if groups > 1 else 0)
+    each = g.double() * h.double() * rstd.double()[:, None]
+    bound = 2.0 ** -24 * (deep + 2) * each.abs().sum(0) * (1 + 1e-4)
+    assert ((gw.cpu().double() - each.sum(0)).abs() <= bound).all(), (gw.cpu().double() - each.sum(0)).abs().max()
