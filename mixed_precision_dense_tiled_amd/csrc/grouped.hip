@@ -819,8 +819,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 // 128 x 256 tiles, two workgroups to a CU: for short sums, whose tiles take as long to
 // begin and to store as for their product (384 rows of a weights' gradient: 2 + 3 us and
 // 10); another workgroup's product goes on meanwhile.  Weights' gradient of 12288 rows over
-// 29 groups of 2048 x 1408 FP16: 116 to 125 us, 565 TFLOP/s, 185 MB of D written.  An XCD
-// takes a run of neighbouring tiles.
+// 29 groups of 2048 x 1408 FP16: 116 to 125 us, 565 TFLOP/s, 185 MB of D written; its tiles go
+// to the XCDs in turn.  Of the products an XCD takes a run of neighbouring tiles.  (INT8 spills
+// 64 registers in tile_store, 16 scales and 16 biases of four columns, outside the loop.)
 template <GroupedType T, int MODE>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void grouped_half_kernel(GroupedArgs g) {
     constexpr int LDS = 73728;
@@ -917,7 +918,8 @@ struct Strip {
 // every fourth K tile each, through rings of direct loads of their own that no barrier
 // holds up, and their sums are joined in LDS at the end.  8 rows of 8 groups of 2048 x 1408:
 // 10.4 us, 24.7 by the tiles above (strips of 128 columns 12.9, rings of twice the depth in
-// one workgroup to a CU 12.0).
+// one workgroup to a CU 12.0).  Those are A . B's; with B^T, whose stages are 128 bytes of k, one
+// workgroup has a CU: 12.4 us, INT8 8.0; 8 rows of 8 of 16 groups of 4096 x 4096 46 and 27.
 template <GroupedType T, int MODE, int MT>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) void grouped_few_kernel(GroupedArgs g) {
     constexpr int SN = 64;
@@ -1169,6 +1171,9 @@ hipError_t launch_mode(const GroupedArgs& a, hipStream_t stream) {
                 return hipGetLastError();
             }
         }
+        // (Averages are all that is known here.  One group with all rows among 63 empty ones of 2048
+        // x 1408: 1200 rows 26 us, 24 where it is the only group; 3000 rows 37 and 35; 8000 57 and 56)
+        //
         // Short sums, and somewhat longer ones where all tiles run at once (16384 rows of 16
         // groups of 768 x 2048: 60 us, 67 by the larger tiles; of 4 groups of 128 x 4096 39 and 59;
         // of 8 groups of 512 x 14336 310 and 352; INT8, 9651 rows of 3 groups of 1280 x 5888 116
