@@ -12,6 +12,7 @@
 #include <stdint.h>
 
 #include "gemm_common.hpp"
+#include "layer_sizes.hpp"
 #include "layers.hpp"
 
 namespace mpdt {
@@ -1101,16 +1102,6 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
     }
 }
 
-// The most row tiles of BM rows that the groups can have.
-int64_t most_row_tiles(const GroupedArgs& a, int64_t bm) {
-    return a.rows / bm + (a.rows < a.groups ? a.rows : a.groups);
-}
-
-int64_t grouped_tiles(int mode, const GroupedArgs& a, int64_t bm, int64_t bn) {
-    const int64_t tn = (a.N + bn - 1) / bn;
-    return tn * (mode == GROUPED_TN ? (a.M + bm - 1) / bm * a.groups : most_row_tiles(a, bm));
-}
-
 template <GroupedType T, int MODE>
 hipError_t launch_any(const GroupedArgs& a, hipStream_t stream) {
     grouped_any_kernel<T, MODE><<<dim3((unsigned)grouped_tiles(MODE, a, 128, 128)), dim3(256), 0, stream>>>(a);
@@ -1200,7 +1191,8 @@ hipError_t launch_type(int mode, const GroupedArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-bool grouped_fits(int mode, const GroupedArgs& a) { return grouped_tiles(mode, a, 128, 128) <= MAX_GROUPS - NUM_XCD; }
+static_assert(NUM_XCD == 8, "as layer_sizes.hpp counts");
+bool grouped_fits(int mode, const GroupedArgs& a) { return tiles_fit(mode, a); }
 
 hipError_t launch_grouped(GroupedType type, int mode, const GroupedArgs& a, hipStream_t stream) {
     switch (type) {

@@ -20,6 +20,7 @@
 #include <stdint.h>
 
 #include "device_common.hpp"
+#include "layer_sizes.hpp"
 #include "layers.hpp"
 #include "quotient.hpp"
 
@@ -312,19 +313,7 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
 
 // ---- gradient ------------------------------------------------------------------
 
-// Each workgroup (each wave, for rows of up to 1024 elements) walks rows of its own and
-// keeps its columns' sums of grad * h * rstd in registers; a second launch adds the
-// workgroups' sums in their order.  Few workgroups leave loads waiting, many have that
-// many sums to write and read again (us at workgroups: 500 x 5120 FP16 20 at 500, 14.4 at
-// 250, 15.5 at 128 of 512 threads; 16000 x 1000 53 at 512, 27 at 1024 of four rows; 2000 x 16384 60 at
-// 512, 46 at 256).
-int grad_groups(int64_t rows, int64_t dim) {
-    const int64_t n = dim <= 1024 ? (rows + 3) / 4 : rows;     // (rows of a workgroup at a time)
-    const int64_t most = dim <= 2048 ? 1024 : dim <= 8192 ? 512 : 256;
-    const int64_t few = n < 128 ? n : n < 384 ? 128 : n / 3;
-    return (int)(few < most ? few : most);
-}
-
+// Each of grad_groups workgroups walks rows of its own; a second launch adds their sums.
 template <int T, int WT, int NT, int PIECES>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_grad_kernel(NormGradArgs a) {
     __shared__ float red[2][NT / 64];
@@ -498,10 +487,7 @@ hipError_t launch_rms_norm(const NormArgs& a, hipStream_t stream) {
     return a.w_f32 ? launch_norm<DT_F16, DT_F32>(a, stream) : launch_norm<DT_F16, DT_F16>(a, stream);
 }
 
-int64_t rms_norm_backward_ws(int64_t rows, int64_t dim) {
-    const int g = grad_groups(rows, dim);
-    return g > 1 ? 4 * g * dim : 0;
-}
+int64_t rms_norm_backward_ws(int64_t rows, int64_t dim) { return grad_sums_bytes(rows, dim); }
 
 hipError_t launch_rms_norm_backward(const NormGradArgs& a, hipStream_t stream) {
     const int groups = grad_groups(a.rows, a.dim);
