@@ -783,7 +783,7 @@ __device__ __forceinline__ void tile_run(const GroupedArgs& g, Tile t, MPDT_LDS 
 }
 
 // 256 x 256 tiles, one workgroup to a CU: bound by the matrix cores at the card's power
-// limit (16384 rows over 8 groups of 4096 x 14336 BF16: 1.70 to 1.75 ms, 1100 to 1130
+// limit (16384 rows over 8 groups of 4096 x 14336 BF16: 1.70 to 1.80 ms by the card, 1070 to 1130
 // TFLOP/s; the library's 8192^3 product reaches 1210) where groups are large, by HBM where
 // their matrices are read for few rows (INT8, 1536 rows over 16 groups of 4096 x 4096: 70
 // us, 4.1 TB/s).
