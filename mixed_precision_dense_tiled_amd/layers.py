@@ -31,6 +31,9 @@ _NORM_OUT = {None: 0, "int8": 1, "fp8_rows": 2, "fp8_blocks": 3}
 
 RmsNorm = namedtuple("RmsNorm", "out scales residual rstd")
 
+# rows of a native rms_norm call
+_NORM_ROWS = 4194303
+
 _native = None
 
 
@@ -119,16 +122,30 @@ def _norm_operands(x, weight, name):
     return rows, dim, code, _DTYPE[weight.dtype]
 
 
+def _apart(*written, rows, read):
+    """Raise ValueError where a written operand (pointer, leading dimension, element's
+    size, columns) overlaps another, other than exactly."""
+    def span(m):
+        return m[0], m[0] + ((rows - 1) * m[1] + m[3]) * m[2]
+
+    written = [m for m in written if m[0] is not None]
+    for i, a in enumerate(written):
+        for b in written[i + 1:] + [m for m in read if m[0] is not None]:
+            (lo, hi), (other, end) = span(a), span(b)
+            if lo < end and other < hi and a != b:
+                raise ValueError("an output overlaps another operand")
+
+
 def rms_norm(x, weight, eps=1e-6, residual=None, quant=None, return_rstd=False, out=None, scales_out=None,
              residual_out=None):
     """Root-mean-square norm of rows, with the residual's addition before it and
     an output in 8 bits after it.
 
-    x [rows, dim] BF16, FP16 or FP32 (rows may be strided), dim at most 32768 and
-    rows at most 4194303 (more in several calls); weight [dim] in x's type or
-    FP32; residual like x.  With h = x + residual, rounded once to x's type (x
-    alone without a residual), rstd = 1 / sqrt(mean(h^2) + eps) and y = (h *
-    rstd) * weight in FP32.  Returns RmsNorm:
+    x [rows, dim] BF16, FP16 or FP32 (rows may be strided), dim at most 32768;
+    weight [dim] in x's type or FP32; residual like x.  (Over 4194303 rows take
+    as many launches as they need.)  With h = x + residual, rounded once to x's
+    type (x alone without a residual), rstd = 1 / sqrt(mean(h^2) + eps) and y =
+    (h * rstd) * weight in FP32.  Returns RmsNorm:
       out       y in x's type, or with quant codes of 8 bits: "int8" for
                 gemm_w8a8, "fp8_rows" (E4M3 in uint8) for gemm_fp8_rowscaled,
                 "fp8_blocks" (E4M3, 1 x 128 scales) for gemm_fp8_blockscaled
@@ -186,8 +203,19 @@ def rms_norm(x, weight, eps=1e-6, residual=None, quant=None, return_rstd=False, 
     rstd = x.new_empty(rows, dtype=torch.float32) if return_rstd else None
     if rstd is not None:
         pd = rstd.data_ptr()
-    _call(x, "rms_norm", code, rows, dim, px, ldx, pr, ldr, w_code, weight.data_ptr(), eps, _NORM_OUT[quant], po,
-          ldo, ps, lds, ph, ldh, pd)
+    if rows <= _NORM_ROWS:
+        _call(x, "rms_norm", code, rows, dim, px, ldx, pr, ldr, w_code, weight.data_ptr(), eps, _NORM_OUT[quant], po,
+              ldo, ps, lds, ph, ldh, pd)
+    else:
+        es, os = dtype.itemsize, out_type.itemsize
+        # (each part's operands are checked against each other, so here all parts' at once)
+        _apart((po, ldo, os, dim), (ph, ldh, es, dim), (ps, lds, 4, grid[-1] if blocks else 1), (pd, 1, 4, 1),
+               rows=rows, read=((px, ldx, es, dim), (pr, ldr, es, dim), (weight.data_ptr(), 0, 1, dim * weight.itemsize)))
+        at = lambda p, ld, size, lo: None if p is None else p + lo * ld * size
+        for lo in range(0, rows, _NORM_ROWS):
+            _call(x, "rms_norm", code, min(_NORM_ROWS, rows - lo), dim, at(px, ldx, es, lo), ldx, at(pr, ldr, es, lo),
+                  ldr, w_code, weight.data_ptr(), eps, _NORM_OUT[quant], at(po, ldo, os, lo), ldo, at(ps, lds, 4, lo),
+                  lds, at(ph, ldh, es, lo), ldh, at(pd, 1, 4, lo))
     return RmsNorm(out, scales_out, residual_out, rstd)
 
 

@@ -185,3 +185,33 @@ def test_weights_gradient_by_its_sums(rows, dim):
     each = g.double() * h.double() * rstd.double()[:, None]
     bound = 2.0 ** -24 * (deep + 2) * each.abs().sum(0) * (1 + 1e-4)
     assert ((gw.cpu().double() - each.sum(0)).abs() <= bound).all(), (gw.cpu().double() - each.sum(0)).abs().max()
+
+
+@pytest.mark.parametrize("quant", [None, "int8", "fp8_blocks"])
+def test_more_rows_than_a_launch(quant):
+    """In place and apart; each row as by itself."""
+    most, dim = 4194303, 8
+    rows = most + 5
+    x, r = (randn((rows, dim), i).to(torch.bfloat16).cuda() for i in (1, 2))
+    w = (1 + 0.3 * randn(dim, 3)).to(torch.bfloat16).cuda()
+    parts = [mp.rms_norm(x[a:b], w, residual=r[a:b], quant=quant, return_rstd=True) for a, b in ((0, most), (most, rows))]
+    want = [None if a is None else torch.cat([a, b]) for a, b in zip(*parts)]
+    for place in (False, True):
+        got = mp.rms_norm(x, w, residual=r, quant=quant, return_rstd=True, residual_out=r if place else None,
+                          out=x if place and quant is None else None)
+        for a, b in zip(got, want):
+            assert a is b is None or torch.equal(a, b)
+
+
+def test_overlaps_across_launches():
+    """An output that lies on rows of another launch's is refused as one on its own is."""
+    most, dim = 4194303, 8
+    buf = torch.zeros((2 * most + 10, dim), dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(dim, dtype=torch.bfloat16, device="cuda")
+    x, far = buf[:most + 5], buf[most:2 * most + 5]
+    with pytest.raises(ValueError, match="overlaps"):
+        mp.rms_norm(x, w, out=far)
+    with pytest.raises(ValueError, match="overlaps"):
+        mp.rms_norm(x, w, residual=torch.zeros_like(x), residual_out=far)
+    with pytest.raises(mp.MpdtError):       # (the same buffer, both written)
+        mp.rms_norm(x, w, residual=torch.zeros_like(x), residual_out=x, out=x)
