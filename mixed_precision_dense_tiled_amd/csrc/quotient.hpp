@@ -14,8 +14,8 @@ __device__ __forceinline__ bool divides(float d) { return d >= 0x1p-60f && d <= 
 // within one, and from there another step rounds correctly (Markstein's theorem: P.
 // Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor",
 // 1990).  Holds for finite quotients; those below 2^-66 may come out with fewer bits.  The
-// remainder is taken as p * d - x and its part subtracted: for x = -0 that leaves p at -0 (0 * d
-// + 0 = +0, -0 - 0 * r = -0), where x - p * d added would make it +0.
+// remainder is taken as p * d - x and its part subtracted: for x = -0 that leaves p at -0
+// (-0 * d + 0 = +0, -0 - 0 * r = -0), where x - p * d added would make it +0.
 __device__ __forceinline__ float quotient(float x, float d, float r) {
     float p = x * r;
     p = __builtin_fmaf(-__builtin_fmaf(p, d, -x), r, p);
